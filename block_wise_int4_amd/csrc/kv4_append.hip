@@ -1,0 +1,324 @@
+// kv4_append.hip -- new keys and values into the paged 4-bit cache, with the
+// position rotation of queries and keys on the way, and stored rows back out.
+//
+// A group of `group` consecutive values of one head and token is stored as
+//   s = fp16((hi - lo) / 15), lo = min(0, min x), hi = max(0, max x),
+//   z = clamp(rne(-lo / s), 0, 15), c = clamp(rne(x / s) + z, 0, 15),
+// and stands for (c - z) s.  All steps are binary32, each rounded once (no
+// contraction), with 1 / s formed once per group.  s = 0 stores zeros; a group
+// that holds a NaN or an infinity, or whose scale passes fp16, gets s = NaN or
+// infinity and reads back as NaN.
+//
+// The work is one (token, head) to head_dim / 8 lanes, 8 values a lane: a
+// lane's 8 key codes are one word of the layout, and its 8 value codes are 8
+// bytes once the lane two over has lent its nibbles (a value byte holds two
+// dims of one token, so no byte is shared between tokens and nothing is read
+// back).  Every token is independent; the kernel is bound by the latency of
+// q_start -> kv_len -> page table at one token per sequence, and by its
+// traffic for prompts.
+#include "mnb_device.hpp"
+#include "mnb_kv4.hpp"
+
+namespace mnb {
+
+namespace {
+
+constexpr int kThreads = 256;
+
+// 8 consecutive elements as fp32, at any element alignment
+__device__ __forceinline__ void load8(const _Float16* p, float* f)
+{
+    typedef uint32_t raw __attribute__((ext_vector_type(4), aligned(2), may_alias));
+    const u4_t r = *reinterpret_cast<const raw*>(p);
+    const h8_t h = __builtin_bit_cast(h8_t, r);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) f[i] = (float)h[i];
+}
+__device__ __forceinline__ void load8(const float* p, float* f)
+{
+    typedef float raw __attribute__((ext_vector_type(4), aligned(4)));
+    const raw a = *reinterpret_cast<const raw*>(p), b = *reinterpret_cast<const raw*>(p + 4);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        f[i] = a[i];
+        f[4 + i] = b[i];
+    }
+}
+__device__ __forceinline__ void store8(_Float16* p, const float* f)
+{
+    typedef uint32_t raw __attribute__((ext_vector_type(4), aligned(2), may_alias));
+    h8_t h;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) h[i] = (_Float16)f[i];
+    *reinterpret_cast<raw*>(p) = __builtin_bit_cast(u4_t, h);
+}
+__device__ __forceinline__ void store8(float* p, const float* f)
+{
+    typedef float raw __attribute__((ext_vector_type(4), aligned(4)));
+    *reinterpret_cast<raw*>(p) = raw{f[0], f[1], f[2], f[3]};
+    *reinterpret_cast<raw*>(p + 4) = raw{f[4], f[5], f[6], f[7]};
+}
+
+// The sequence of a token, searched by LPR adjacent lanes together: each
+// round compares LPR spread offsets and keeps one LPR-th of the range.
+// Returns the number of sequences whose tokens all come before it (batch
+// when the token is past the last).
+template <int LPR>
+__device__ __forceinline__ int find_sequence(const int32_t* q_start, int batch, int token, int l)
+{
+    int lo = 0, n = batch;
+    while (n > 0) {
+        const int step = (n + LPR - 1) / LPR;
+        const int at = lo + (l + 1) * step;          // ends of sequences lo .. at - 1
+        const int end = lo + n;
+        int before = at <= end && q_start[at <= batch ? at : batch] <= token ? 1 : 0;
+#pragma unroll
+        for (int off = 1; off < LPR; off <<= 1) before += __shfl_xor(before, off);
+        lo += before * step;
+        n = step == 1 ? 0 : (end - lo < step - 1 ? end - lo : step - 1);
+    }
+    return lo;
+}
+
+struct Place {
+    int64_t pos;              // position in the sequence, < 0: none
+    unsigned char* block;     // NULL: no page
+    int key;                  // token's place in its block
+};
+
+// Position of a token and the block of its page that holds head h.  Page
+// numbers and positions outside their ranges give no block.
+template <int LPR>
+__device__ __forceinline__ Place place_of(const KvView& v, int token, int h, int64_t block_bytes, int l)
+{
+    Place r{-1, nullptr, 0};
+    int b = token, behind = 1;    // tokens of the sequence from this one on
+    if (v.q_start) {
+        b = find_sequence<LPR>(v.q_start, v.batch, token, l);
+        if (b < v.batch) behind = v.q_start[b + 1] - token;
+    }
+    if (b >= v.batch) return r;
+    r.pos = (int64_t)v.kv_len[b] - behind;
+    if (r.pos < 0) return r;
+    const int64_t page_at = r.pos >> v.page_shift;
+    if (page_at >= v.table_stride) return r;
+    const int page = v.table[b * v.table_stride + page_at];
+    if (page < 0 || page >= v.num_pages) return r;
+    const int in_page = (int)(r.pos & ((1 << v.page_shift) - 1));
+    const int nblk = 1 << (v.page_shift - 5);
+    r.block = v.cache + (((int64_t)page * v.kv_heads + h) * nblk + (in_page >> 5)) * block_bytes;
+    r.key = in_page & 31;
+    return r;
+}
+
+// Byte offsets inside a block (D = 8 LPR).
+template <int LPR> __device__ __forceinline__ int key_word_at(int key, int l)
+{
+    const int w = (key >> 4) * (LPR / 4) + (l >> 2);
+    return (w >> 2) * 1024 + ((l & 3) * 16 + (key & 15)) * 16 + (w & 3) * 4;
+}
+template <int LPR> __device__ __forceinline__ int value_byte_at(int key, int l)   // of the lane's first dim; 16 apart
+{
+    const int u = l >> 2, i = key & 3;
+    return LPR * 128 + (u >> 1) * 1024 + (((key & 15) >> 2) * 16 + (l & 1) * 8) * 16 + (u & 1) * 8 + (key >> 4) * 4 +
+           ((i & 1) * 2 + (i >> 1));
+}
+
+template <typename T, int LPR>
+__global__ __launch_bounds__(kThreads) void kv4_append_kernel(AppendArgs a)
+{
+#pragma clang fp contract(off)
+    constexpr int D = 8 * LPR;
+    const KvView& v = a.v;
+    const int l = threadIdx.x % LPR;
+    const int hq = a.q ? v.q_heads : 0;
+    const int items = hq + 2 * v.kv_heads;
+    const int64_t id = (int64_t)blockIdx.x * (kThreads / LPR) + threadIdx.x / LPR;
+    const int token = (int)(id / items);
+    if (token >= v.tokens) return;               // whole lane groups
+    const int item = (int)(id % items);
+    const bool is_q = item < hq, is_v = item >= hq + v.kv_heads;
+    const int h = is_q ? item : is_v ? item - hq - v.kv_heads : item - hq;
+    const int NG = v.groups, GL = LPR / NG;      // lanes of a group
+
+    const T* src = is_q ? static_cast<const T*>(a.q) + token * a.q_stride
+                        : is_v ? static_cast<const T*>(a.val) + token * a.v_stride
+                               : static_cast<const T*>(a.k) + token * a.k_stride;
+    src += (int64_t)h * D;
+    const int rot = is_v || !a.cos ? 0 : a.rotary_dim;
+    const int d0 = 8 * l;
+    const bool turn = d0 < rot;
+    float x[8], y[8];
+    load8(src + d0, x);
+    const int half = rot >> 1;
+    const bool second = !a.interleaved && d0 >= half;
+    if (turn && !a.interleaved) load8(src + (second ? d0 - half : d0 + half), y);
+
+    const Place at = place_of<LPR>(v, token, is_q ? 0 : h, kv_block_bytes(D, NG), l);
+    if (turn) {
+        int64_t row = at.pos < 0 ? 0 : at.pos;
+        row = row < a.rope_rows ? row : a.rope_rows - 1;
+        if (a.interleaved) {
+            const float* c = a.cos + row * half + (d0 >> 1);
+            const float* s = a.sin + row * half + (d0 >> 1);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const float e = x[2 * i], o = x[2 * i + 1];
+                x[2 * i] = e * c[i] - o * s[i];
+                x[2 * i + 1] = o * c[i] + e * s[i];
+            }
+        } else {
+            const int j = second ? d0 - half : d0;
+            float c[8], s[8];
+            load8(a.cos + row * half + j, c);
+            load8(a.sin + row * half + j, s);
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                const float p = x[i] * c[i], t = y[i] * s[i];
+                x[i] = second ? p + t : p - t;
+            }
+        }
+    }
+    if (is_q) {
+        store8(static_cast<T*>(a.q_out) + ((int64_t)token * v.q_heads + h) * D + d0, x);
+        return;
+    }
+
+    float lo = 0.0f, hi = 0.0f;
+    int bad = 0;                                  // a NaN, which min and max skip
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+        lo = fminf(lo, x[i]);
+        hi = fmaxf(hi, x[i]);
+        bad |= x[i] != x[i];
+    }
+    for (int off = 1; off < GL; off <<= 1) {
+        lo = fminf(lo, __shfl_xor(lo, off));
+        hi = fmaxf(hi, __shfl_xor(hi, off));
+        bad |= __shfl_xor(bad, off);
+    }
+    _Float16 s16 = (_Float16)((hi - lo) * (1.0f / 15.0f));
+    if (bad) s16 = (_Float16)__builtin_nanf("");
+    const float s = (float)s16;
+    const float inv = s > 0.0f && s < __builtin_inff() ? 1.0f / s : 0.0f;
+    const float z = inv > 0.0f ? fminf(fmaxf(rintf(-lo * inv), 0.0f), 15.0f) : 0.0f;
+    uint32_t nat = 0;                             // nibble i: dim d0 + i
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+        const float c = fminf(fmaxf(rintf(x[i] * inv) + z, 0.0f), 15.0f);
+        nat |= (uint32_t)c << (4 * i);
+    }
+    const uint32_t other = (uint32_t)__shfl_xor((int)nat, 2);
+    if (!at.block) return;                        // whole lane groups
+    if (l % GL == 0) {
+        const int meta = 32 * D + (is_v ? 128 * NG : 0) + (at.key * NG + l / GL) * 4;
+        *reinterpret_cast<uint32_t*>(at.block + meta) =
+            (uint32_t)__builtin_bit_cast(uint16_t, s16) | ((uint32_t)z << 16);
+    }
+    if (!is_v) {
+        // k-offsets 0,2,4,6 in the low four nibbles, 1,3,5,7 in the high four
+        uint32_t w = 0;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) w |= ((nat >> (4 * i)) & 15u) << (4 * nibble_slot(i));
+        *reinterpret_cast<uint32_t*>(at.block + key_word_at<LPR>(at.key, l)) = w;
+    } else {
+        // lanes l and l ^ 2 hold dims 16 apart: the low and the high nibble of 8
+        // bytes, of which each writes four
+        const bool upper = (l & 2) != 0;
+        const uint32_t lo4 = upper ? other : nat, hi4 = upper ? nat : other;
+        unsigned char* dst = at.block + value_byte_at<LPR>(at.key, l);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            const int i = j + (upper ? 4 : 0);
+            dst[16 * i] = (unsigned char)(((lo4 >> (4 * i)) & 15u) | (((hi4 >> (4 * i)) & 15u) << 4));
+        }
+    }
+}
+
+template <typename T, int LPR>
+__global__ __launch_bounds__(kThreads) void kv4_read_kernel(ReadArgs a)
+{
+    constexpr int D = 8 * LPR;
+    const KvView& v = a.v;
+    const int l = threadIdx.x % LPR;
+    const int items = 2 * v.kv_heads;
+    const int64_t id = (int64_t)blockIdx.x * (kThreads / LPR) + threadIdx.x / LPR;
+    const int token = (int)(id / items);
+    if (token >= v.tokens) return;
+    const int item = (int)(id % items);
+    const bool is_v = item >= v.kv_heads;
+    const int h = is_v ? item - v.kv_heads : item;
+    const int NG = v.groups, GL = LPR / NG;
+    void* out = is_v ? a.v_out : a.k_out;
+    if (!out) return;
+
+    const Place at = place_of<LPR>(v, token, h, kv_block_bytes(D, NG), l);
+    float x[8] = {0, 0, 0, 0, 0, 0, 0, 0};
+    if (at.block) {
+        const uint32_t m = *reinterpret_cast<const uint32_t*>(at.block + 32 * D + (is_v ? 128 * NG : 0) +
+                                                              (at.key * NG + l / GL) * 4);
+        const float s = (float)__builtin_bit_cast(_Float16, (uint16_t)m);
+        const int z = (int)((m >> 16) & 15u);
+        int c[8];
+        if (!is_v) {
+            const uint32_t w = *reinterpret_cast<const uint32_t*>(at.block + key_word_at<LPR>(at.key, l));
+#pragma unroll
+            for (int i = 0; i < 8; ++i) c[i] = (int)code_at(w, i);
+        } else {
+            const unsigned char* src = at.block + value_byte_at<LPR>(at.key, l);
+#pragma unroll
+            for (int i = 0; i < 8; ++i) c[i] = (src[16 * i] >> ((l & 2) * 2)) & 15;
+        }
+#pragma unroll
+        for (int i = 0; i < 8; ++i) x[i] = (float)(c[i] - z) * s;
+    }
+    store8(static_cast<T*>(out) + ((int64_t)token * v.kv_heads + h) * D + 8 * l, x);
+}
+
+inline unsigned blocks_for(int64_t items, int lanes) { return (unsigned)((items * lanes + kThreads - 1) / kThreads); }
+
+}  // namespace
+
+hipError_t launch_kv4_append(const AppendArgs& a, hipStream_t stream, const char** variant)
+{
+    const int lpr = a.v.head_dim / 8;
+    const unsigned grid = blocks_for((int64_t)a.v.tokens * ((a.q ? a.v.q_heads : 0) + 2 * a.v.kv_heads), lpr);
+    *variant = "kv4_append";
+    switch (lpr) {
+    case 8:
+        if (a.f16) kv4_append_kernel<_Float16, 8><<<grid, kThreads, 0, stream>>>(a);
+        else kv4_append_kernel<float, 8><<<grid, kThreads, 0, stream>>>(a);
+        break;
+    case 16:
+        if (a.f16) kv4_append_kernel<_Float16, 16><<<grid, kThreads, 0, stream>>>(a);
+        else kv4_append_kernel<float, 16><<<grid, kThreads, 0, stream>>>(a);
+        break;
+    default:
+        if (a.f16) kv4_append_kernel<_Float16, 32><<<grid, kThreads, 0, stream>>>(a);
+        else kv4_append_kernel<float, 32><<<grid, kThreads, 0, stream>>>(a);
+    }
+    return hipGetLastError();
+}
+
+hipError_t launch_kv4_read(const ReadArgs& a, hipStream_t stream, const char** variant)
+{
+    const int lpr = a.v.head_dim / 8;
+    const unsigned grid = blocks_for((int64_t)a.v.tokens * 2 * a.v.kv_heads, lpr);
+    *variant = "kv4_read";
+    switch (lpr) {
+    case 8:
+        if (a.f16) kv4_read_kernel<_Float16, 8><<<grid, kThreads, 0, stream>>>(a);
+        else kv4_read_kernel<float, 8><<<grid, kThreads, 0, stream>>>(a);
+        break;
+    case 16:
+        if (a.f16) kv4_read_kernel<_Float16, 16><<<grid, kThreads, 0, stream>>>(a);
+        else kv4_read_kernel<float, 16><<<grid, kThreads, 0, stream>>>(a);
+        break;
+    default:
+        if (a.f16) kv4_read_kernel<_Float16, 32><<<grid, kThreads, 0, stream>>>(a);
+        else kv4_read_kernel<float, 32><<<grid, kThreads, 0, stream>>>(a);
+    }
+    return hipGetLastError();
+}
+
+}  // namespace mnb

@@ -10,12 +10,13 @@
 
 #include <cstdarg>
 #include <cstdio>
+#include <cstring>
 #include <mutex>
-#include <string>
 #include <vector>
 
 #include "../../include/mnb.h"
 #include "mnb_acc4.hpp"
+#include "mnb_api_common.hpp"
 #include "mnb_internal.hpp"
 #include "mnb_gidx.hpp"
 
@@ -23,28 +24,85 @@ using mnb::Layout;
 
 namespace {
 
-thread_local std::string g_error;
+// fixed storage: recording an error allocates nothing and cannot throw
+thread_local char g_error[520] = "";
 thread_local const char* g_variant = "";
+
+bool aligned(const void* p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0; }
+
+}  // namespace
+
+namespace mnb {
+namespace api {
 
 mnb_status fail(mnb_status s, const char* fmt, ...)
 {
-    char buf[512];
+    memcpy(g_error, "mnb: ", 5);
     va_list ap;
     va_start(ap, fmt);
-    vsnprintf(buf, sizeof(buf), fmt, ap);
+    vsnprintf(g_error + 5, sizeof(g_error) - 5, fmt, ap);
     va_end(ap);
-    g_error = std::string("mnb: ") + buf;
     return s;
 }
 
 mnb_status ok(const char* variant)
 {
-    g_error.clear();
+    g_error[0] = 0;
     g_variant = variant ? variant : "";
     return MNB_OK;
 }
 
-bool aligned(const void* p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0; }
+mnb_status check_ptr(const void* p, uintptr_t align, const char* name)
+{
+    if (!p) return fail(MNB_ERR_INVALID_ARGUMENT, "%s is NULL", name);
+    if (!aligned(p, align))
+        return fail(MNB_ERR_INVALID_ARGUMENT, "%s must be %u-byte aligned", name, (unsigned)align);
+    return MNB_OK;
+}
+
+// A gfx950 device must be current.  The architecture is looked up once per
+// device (a property query is not free); later calls cost one hipGetDevice.
+mnb_status check_device()
+{
+    int dev = -1;
+    if (hipGetDevice(&dev) != hipSuccess || dev < 0) {
+        (void)hipGetLastError();
+        return fail(MNB_ERR_DEVICE, "no HIP device available");
+    }
+    static std::mutex mu;
+    static signed char is_gfx950[64] = {0};  // 0 unknown, 1 yes, -1 no
+    if (dev >= 64) return fail(MNB_ERR_DEVICE, "device index %d out of range", dev);
+    if (is_gfx950[dev] == 0) {
+        std::lock_guard<std::mutex> lock(mu);
+        if (is_gfx950[dev] == 0) {
+            hipDeviceProp_t prop;
+            if (hipGetDeviceProperties(&prop, dev) != hipSuccess) {
+                (void)hipGetLastError();
+                return fail(MNB_ERR_DEVICE, "cannot query device %d", dev);
+            }
+            is_gfx950[dev] = strncmp(prop.gcnArchName, "gfx950", 6) == 0 ? 1 : -1;
+        }
+    }
+    if (is_gfx950[dev] < 0) return fail(MNB_ERR_DEVICE, "device %d is not gfx950", dev);
+    return MNB_OK;
+}
+
+mnb_status launched(hipError_t e, const char* variant)
+{
+    if (e != hipSuccess) return fail(MNB_ERR_DEVICE, "launch failed: %s", hipGetErrorString(e));
+    return ok(variant);
+}
+
+}  // namespace api
+}  // namespace mnb
+
+namespace {
+
+using mnb::api::check_device;
+using mnb::api::check_ptr;
+using mnb::api::fail;
+using mnb::api::launched;
+using mnb::api::ok;
 
 mnb_status check_desc(const mnb_weight_desc* w, Layout* L)
 {
@@ -81,53 +139,6 @@ mnb_status check_act_dtype(int32_t a_dtype)
     return MNB_OK;
 }
 
-mnb_status check_ptr(const void* p, uintptr_t align, const char* name)
-{
-    if (!p) return fail(MNB_ERR_INVALID_ARGUMENT, "%s is NULL", name);
-    if (!aligned(p, align))
-        return fail(MNB_ERR_INVALID_ARGUMENT, "%s must be %u-byte aligned", name, (unsigned)align);
-    return MNB_OK;
-}
-
-// A gfx950 device must be current.  The architecture is looked up once per
-// device (a property query is not free); later calls cost one hipGetDevice.
-mnb_status check_device()
-{
-    int dev = -1;
-    if (hipGetDevice(&dev) != hipSuccess || dev < 0) {
-        (void)hipGetLastError();
-        return fail(MNB_ERR_DEVICE, "no HIP device available");
-    }
-    static std::mutex mu;
-    static signed char is_gfx950[64] = {0};  // 0 unknown, 1 yes, -1 no
-    if (dev >= 64) return fail(MNB_ERR_DEVICE, "device index %d out of range", dev);
-    if (is_gfx950[dev] == 0) {
-        std::lock_guard<std::mutex> lock(mu);
-        if (is_gfx950[dev] == 0) {
-            hipDeviceProp_t prop;
-            if (hipGetDeviceProperties(&prop, dev) != hipSuccess) {
-                (void)hipGetLastError();
-                return fail(MNB_ERR_DEVICE, "cannot query device %d", dev);
-            }
-            is_gfx950[dev] = std::string(prop.gcnArchName).rfind("gfx950", 0) == 0 ? 1 : -1;
-        }
-    }
-    if (is_gfx950[dev] < 0) return fail(MNB_ERR_DEVICE, "device %d is not gfx950", dev);
-    return MNB_OK;
-}
-
-mnb_status launched(hipError_t e, const char* variant)
-{
-    if (e != hipSuccess) return fail(MNB_ERR_DEVICE, "launch failed: %s", hipGetErrorString(e));
-    return ok(variant);
-}
-
-#define MNB_TRY(x)                           \
-    do {                                     \
-        const mnb_status s_ = (x);           \
-        if (s_ != MNB_OK) return s_;         \
-    } while (0)
-
 }  // namespace
 
 extern "C" {
@@ -136,7 +147,7 @@ size_t mnb_repacked_bytes(const mnb_weight_desc* w)
 {
     Layout L;
     if (check_desc(w, &L) != MNB_OK) return 0;
-    g_error.clear();
+    g_error[0] = 0;
     return (size_t)L.total;
 }
 
@@ -157,7 +168,7 @@ mnb_status mnb_repacked_layout(const mnb_weight_desc* w, mnb_layout* out)
     out->range_flags_offset = L.flags_off;
     out->range_flags_bytes = L.flags_bytes;
     out->total_bytes = L.total;
-    g_error.clear();
+    g_error[0] = 0;
     return MNB_OK;
 }
 
@@ -306,7 +317,7 @@ size_t mnb_gemm_workspace_bytes_for(const mnb_weight_desc* w, int64_t m, int32_t
         fail(MNB_ERR_INVALID_ARGUMENT, "M*K overflows");
         return 0;
     }
-    g_error.clear();
+    g_error[0] = 0;
     return workspace_for(L, m, a_dtype);
 }
 
@@ -453,7 +464,7 @@ size_t mnb_gemm_act_order_workspace_bytes(const mnb_weight_desc* w, int64_t m, i
         fail(MNB_ERR_INVALID_ARGUMENT, "M*K overflows");
         return 0;
     }
-    g_error.clear();
+    g_error[0] = 0;
     return act_order_a_bytes(L, m, a_dtype) + workspace_for(L, m, a_dtype);
 }
 
@@ -542,7 +553,7 @@ size_t mnb_gemm_accuracy4_workspace_bytes(const mnb_weight_desc* w, int64_t m)
     Layout L;
     if (check_desc(w, &L) != MNB_OK) return 0;
     if (m < 0 || (L.K > 0 && m > INT64_MAX / 4 / L.K)) return 0;
-    g_error.clear();
+    g_error[0] = 0;
     return acc4_scale_bytes(m) + acc4_codes_bytes(L, m) + workspace_for(L, m);
 }
 
@@ -595,6 +606,37 @@ mnb_status mnb_gemm_accuracy4(const mnb_weight_desc* w, const void* repacked, co
                               void* stream)
 {
     return accuracy4_common(w, repacked, a, m, bias, y, workspace, workspace_bytes, stream);
+}
+
+mnb_status mnb_gemm_accuracy4_codes(const mnb_weight_desc* w, const void* repacked, const void* codes,
+                                    const float* scales, int64_t m, const float* bias, float* y, void* stream)
+{
+    Layout L;
+    MNB_TRY(check_desc(w, &L));
+    if (m < 0) return fail(MNB_ERR_INVALID_ARGUMENT, "M must be >= 0 (got %lld)", (long long)m);
+    if (m > INT32_MAX) return fail(MNB_ERR_INVALID_ARGUMENT, "M must fit in 32 bits");
+    if (m == 0 || L.N == 0) return ok("noop");
+    if (m > INT64_MAX / 4 / L.K) return fail(MNB_ERR_INVALID_ARGUMENT, "M*K overflows");
+    // one row runs the small-M kernel too
+    MNB_TRY(check_gemm_k(L, m < 2 ? 2 : m));
+    MNB_TRY(check_ptr(repacked, 256, "repacked"));
+    MNB_TRY(check_ptr(codes, 16, "codes"));
+    MNB_TRY(check_ptr(scales, 4, "scales"));
+    MNB_TRY(check_ptr(y, 4, "y"));
+    if (bias) MNB_TRY(check_ptr(bias, 4, "bias"));
+    MNB_TRY(check_device());
+    const mnb::WeightView v = mnb::view_of(L, repacked);
+    const _Float16* q = static_cast<const _Float16*>(codes);
+    const hipStream_t s = static_cast<hipStream_t>(stream);
+    const char* variant = "";
+    hipError_t e = hipSuccess;
+    if (m <= kSliceMaxM) {
+        for (int64_t r0 = 0; r0 < m && e == hipSuccess; r0 += 16)
+            e = mnb::launch_gemm_small_f32(L, v, q + r0 * L.K, m - r0 < 16 ? m - r0 : 16, scales + r0, bias,
+                                           y + r0 * L.N, nullptr, s, &variant);
+    } else
+        e = mnb::launch_gemm_mfma_f32(L, v, q, m, scales, bias, y, s, &variant);
+    return launched(e, variant);
 }
 
 }  // extern "C"
@@ -655,7 +697,7 @@ const char* mnb_status_string(int32_t status)
     return "MNB_ERR_UNKNOWN";
 }
 
-const char* mnb_last_error(void) { return g_error.c_str(); }
+const char* mnb_last_error(void) { return g_error; }
 
 const char* mnb_last_variant(void) { return g_variant; }
 

@@ -1,0 +1,287 @@
+// rms_norm.hip -- RMS norm of the residual stream, one pass over the row.
+//
+//   h = x + r (rounded to the type), y = h * (mean(h^2) + eps)^-1/2 * w,
+//
+// written as values, or as 8-bit codes with one scale per row in the
+// convention of the int8-activation products: s = max|y| / 127, q = y / s
+// rounded half away from zero.  The norm's factor cancels from the codes,
+//   q = 127 h w / max|h w|,
+// so the sum of squares and the maximum are found together, by one reduction
+// of the workgroup, and the codes do not depend on how the sum was rounded.
+// h * w is exact in fp32 for fp16 operands; the quotient is formed in fp64,
+// so a code is off only where the exact quotient is a tie to within 2^-50 (fp32
+// operands: 2^-23).
+//
+// One workgroup holds one row in registers: every input byte is requested
+// before the reduction's barrier and read once.  Loads and stores are 16 bytes
+// whatever the row's alignment (unaligned access is native here); the last
+// K mod 8 (4) elements go one to a thread.
+#include "mnb_device.hpp"
+#include "mnb_kv4.hpp"
+
+namespace mnb {
+
+namespace {
+
+struct NormParams {
+    const void* x;
+    const void* residual;
+    const void* weight;
+    void* out;
+    float* scales;
+    void* residual_out;
+    int64_t x_stride, residual_stride;
+    int k;
+    float eps;
+    float inv_k;
+};
+
+// 16 bytes of T at any element alignment
+template <typename T> struct Vec;
+template <> struct Vec<_Float16> {
+    static constexpr int N = 8;
+    typedef uint32_t raw __attribute__((ext_vector_type(4), aligned(2), may_alias));
+};
+template <> struct Vec<float> {
+    static constexpr int N = 4;
+    typedef uint32_t raw __attribute__((ext_vector_type(4), aligned(4), may_alias));
+};
+
+template <typename T> __device__ __forceinline__ void unpack_vec(const u4_t& r, float* f)
+{
+    if constexpr (sizeof(T) == 2) {
+        const h8_t h = __builtin_bit_cast(h8_t, r);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) f[i] = (float)h[i];
+    } else {
+        const f4_t h = __builtin_bit_cast(f4_t, r);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) f[i] = h[i];
+    }
+}
+
+template <typename T> __device__ __forceinline__ u4_t pack_vec(const float* f)
+{
+    if constexpr (sizeof(T) == 2) {
+        h8_t h;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) h[i] = (_Float16)f[i];
+        return __builtin_bit_cast(u4_t, h);
+    } else {
+        f4_t h;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) h[i] = f[i];
+        return __builtin_bit_cast(u4_t, h);
+    }
+}
+
+// round half away from zero of 127 hw / max, as factor = 127 / max in fp64
+__device__ __forceinline__ int code_of(float hw, double factor)
+{
+    const double t = (double)hw * factor;
+    const int q = (int)(t + __builtin_copysign(0.5, t));
+    return q > 127 ? 127 : (q < -127 ? -127 : q);
+}
+
+template <typename T, int OUT, int NV>
+__global__ __launch_bounds__(1024) void rms_norm_kernel(NormParams p)
+{
+    constexpr int VE = Vec<T>::N;
+    typedef typename Vec<T>::raw raw_t;
+    __shared__ float red[2][16];
+
+    const int tid = threadIdx.x, nt = blockDim.x;
+    const int64_t row = blockIdx.x;
+    const int K = p.k;
+    const int nv = K / VE;            // whole vectors
+    const int tail = K - nv * VE;     // elements past them, one to a thread
+    const T* x = static_cast<const T*>(p.x) + row * p.x_stride;
+    const T* r = p.residual ? static_cast<const T*>(p.residual) + row * p.residual_stride : nullptr;
+    const T* w = static_cast<const T*>(p.weight);
+    T* ro = p.residual_out ? static_cast<T*>(p.residual_out) + row * (int64_t)K : nullptr;
+
+    auto load = [](const T* base, int v) -> u4_t { return *reinterpret_cast<const raw_t*>(base + (int64_t)v * VE); };
+    // h of vector v from the raw operands, rounded to T where a residual is added
+    auto sum_vec = [&](const u4_t& xv, const u4_t& rv, float* h) {
+        unpack_vec<T>(xv, h);
+        if (r) {
+            float f[VE];
+            unpack_vec<T>(rv, f);
+#pragma unroll
+            for (int i = 0; i < VE; ++i) h[i] = (float)(T)(h[i] + f[i]);
+        }
+    };
+
+    u4_t xv[NV], rv[NV], wv[NV];
+#pragma unroll
+    for (int u = 0; u < NV; ++u) {
+        const int v = tid + u * nt;
+        if (v < nv) {
+            xv[u] = load(x, v);
+            if (r) rv[u] = load(r, v);
+            wv[u] = load(w, v);
+        }
+    }
+    float ss = 0.0f, mx = 0.0f;
+    float th = 0.0f, tw = 0.0f;       // the thread's element past the vectors
+    const int te = nv * VE + tid;
+    if (tid < tail) {
+        th = (float)x[te];
+        if (r) th = (float)(T)(th + (float)r[te]);
+        tw = (float)w[te];
+        ss = th * th;
+        mx = fabsf(th * tw);
+    }
+    auto add_vec = [&](const float* h, const u4_t& wr) {
+#pragma unroll
+        for (int i = 0; i < VE; ++i) ss = __builtin_fmaf(h[i], h[i], ss);
+        if constexpr (OUT != kNormValues) {
+            float f[VE];
+            unpack_vec<T>(wr, f);
+#pragma unroll
+            for (int i = 0; i < VE; ++i) mx = fmaxf(mx, fabsf(h[i] * f[i]));
+        }
+    };
+    // the sums replace x in its registers, rounded as they are stored
+#pragma unroll
+    for (int u = 0; u < NV; ++u) {
+        if (tid + u * nt < nv) {
+            float h[VE];
+            sum_vec(xv[u], rv[u], h);
+            xv[u] = pack_vec<T>(h);
+            add_vec(h, wv[u]);
+        }
+    }
+    // rows longer than the registers: read again below
+    for (int v = tid + NV * nt; v < nv; v += nt) {
+        float h[VE];
+        sum_vec(load(x, v), r ? load(r, v) : u4_t{0, 0, 0, 0}, h);
+        add_vec(h, load(w, v));
+    }
+#pragma unroll
+    for (int off = 32; off > 0; off >>= 1) {
+        ss += __shfl_xor(ss, off);
+        if constexpr (OUT != kNormValues) mx = fmaxf(mx, __shfl_xor(mx, off));
+    }
+    const int waves = nt >> 6;
+    if (waves > 1) {
+        if ((tid & 63) == 0) {
+            red[0][tid >> 6] = ss;
+            red[1][tid >> 6] = mx;
+        }
+        __syncthreads();
+        ss = 0.0f;
+        mx = 0.0f;
+        for (int i = 0; i < waves; ++i) {
+            ss += red[0][i];
+            mx = fmaxf(mx, red[1][i]);
+        }
+    }
+    const float rs = 1.0f / sqrtf(__builtin_fmaf(ss, p.inv_k, p.eps));
+    const double factor = OUT != kNormValues && mx > 0.0f ? 127.0 / (double)mx : 0.0;
+
+    auto store_vec = [&](int v, const float* h, const u4_t& wr) {
+        if (ro) *reinterpret_cast<raw_t*>(ro + (int64_t)v * VE) = pack_vec<T>(h);
+        float f[VE];
+        unpack_vec<T>(wr, f);
+        const int64_t e = row * K + (int64_t)v * VE;
+        if constexpr (OUT == kNormValues) {
+#pragma unroll
+            for (int i = 0; i < VE; ++i) f[i] = h[i] * rs * f[i];
+            *reinterpret_cast<raw_t*>(static_cast<T*>(p.out) + e) = pack_vec<T>(f);
+        } else {
+            int q[VE];
+#pragma unroll
+            for (int i = 0; i < VE; ++i) q[i] = code_of(h[i] * f[i], factor);
+            if constexpr (OUT == kNormCodesF16) {
+                typedef uint32_t out_t __attribute__((ext_vector_type(VE / 2), aligned(2), may_alias));
+                out_t o;
+#pragma unroll
+                for (int i = 0; i < VE / 2; ++i)
+                    o[i] = as_u32(h2_t{(_Float16)(float)q[2 * i], (_Float16)(float)q[2 * i + 1]});
+                *reinterpret_cast<out_t*>(static_cast<_Float16*>(p.out) + e) = o;
+            } else {
+                typedef uint32_t out_t __attribute__((ext_vector_type(VE / 4), aligned(1), may_alias));
+                out_t o;
+#pragma unroll
+                for (int i = 0; i < VE / 4; ++i)
+                    o[i] = (uint32_t)(q[4 * i] & 255) | ((uint32_t)(q[4 * i + 1] & 255) << 8) |
+                           ((uint32_t)(q[4 * i + 2] & 255) << 16) | ((uint32_t)q[4 * i + 3] << 24);
+                *reinterpret_cast<out_t*>(static_cast<int8_t*>(p.out) + e) = o;
+            }
+        }
+    };
+    // the vectors past the registers first: they are read again, and residual_out
+    // may be x or residual itself (a thread rewrites only what it has read)
+    for (int v = tid + NV * nt; v < nv; v += nt) {
+        float h[VE];
+        sum_vec(load(x, v), r ? load(r, v) : u4_t{0, 0, 0, 0}, h);
+        store_vec(v, h, load(w, v));
+    }
+#pragma unroll
+    for (int u = 0; u < NV; ++u) {
+        const int v = tid + u * nt;
+        if (v < nv) {
+            float h[VE];
+            unpack_vec<T>(xv[u], h);
+            store_vec(v, h, wv[u]);
+        }
+    }
+    if (tid < tail) {
+        if (ro) ro[te] = (T)th;
+        const int64_t e = row * K + te;
+        if constexpr (OUT == kNormValues)
+            static_cast<T*>(p.out)[e] = (T)(th * rs * tw);
+        else if constexpr (OUT == kNormCodesF16)
+            static_cast<_Float16*>(p.out)[e] = (_Float16)(float)code_of(th * tw, factor);
+        else
+            static_cast<int8_t*>(p.out)[e] = (int8_t)code_of(th * tw, factor);
+    }
+    if (OUT != kNormValues && tid == 0) p.scales[row] = mx * rs / 127.0f;
+}
+
+template <typename T, int OUT>
+hipError_t launch_out(const NormArgs& a, const NormParams& p, hipStream_t s)
+{
+    const int64_t nv = a.k / Vec<T>::N;
+    const dim3 grid((unsigned)a.m);
+    int threads = (int)(nv < 64 ? 64 : nv > 512 ? 512 : (nv + 63) / 64 * 64);
+    if (nv <= 512)
+        rms_norm_kernel<T, OUT, 1><<<grid, dim3(threads), 0, s>>>(p);
+    else if (nv <= 1024)
+        rms_norm_kernel<T, OUT, 2><<<grid, dim3(threads), 0, s>>>(p);
+    else
+        rms_norm_kernel<T, OUT, 4><<<grid, dim3(threads), 0, s>>>(p);
+    return hipGetLastError();
+}
+
+template <typename T> hipError_t launch_type(const NormArgs& a, const NormParams& p, hipStream_t s)
+{
+    switch (a.out_kind) {
+    case kNormValues: return launch_out<T, kNormValues>(a, p, s);
+    case kNormCodesF16: return launch_out<T, kNormCodesF16>(a, p, s);
+    default: return launch_out<T, kNormCodesI8>(a, p, s);
+    }
+}
+
+}  // namespace
+
+hipError_t launch_rms_norm(const NormArgs& a, hipStream_t stream, const char** variant)
+{
+    NormParams p;
+    p.x = a.x;
+    p.residual = a.residual;
+    p.weight = a.weight;
+    p.out = a.out;
+    p.scales = a.scales;
+    p.residual_out = a.residual_out;
+    p.x_stride = a.x_stride;
+    p.residual_stride = a.residual_stride;
+    p.k = (int)a.k;
+    p.eps = a.eps;
+    p.inv_k = (float)(1.0 / (double)a.k);
+    *variant = a.out_kind == kNormValues ? "rms_norm" : a.out_kind == kNormCodesF16 ? "rms_norm_codes_f16" : "rms_norm_codes_i8";
+    return a.f16 ? launch_type<_Float16>(a, p, stream) : launch_type<float>(a, p, stream);
+}
+
+}  // namespace mnb

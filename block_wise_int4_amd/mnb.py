@@ -10,6 +10,7 @@ the import fails.
 from __future__ import annotations
 
 import ctypes
+import math
 import os
 from typing import Optional, Union
 
@@ -24,13 +25,18 @@ MNB_F32 = 0
 MNB_F16 = 1
 MNB_BIAS_FUSED = 0
 MNB_BIAS_AFTER_ROUND = 1
+MNB_NORM_VALUES = 0
+MNB_NORM_CODES_F16 = 1
+MNB_NORM_CODES_I8 = 2
 
 EXPORTS = ("mnb_repacked_bytes", "mnb_repacked_layout", "mnb_repack", "mnb_gemv",
            "mnb_gemv_gate_up_swiglu", "mnb_gemm_workspace_bytes", "mnb_gemm_workspace_bytes_for", "mnb_gemm",
            "mnb_gemm_bias",
            "mnb_act_order_permutation", "mnb_repack_act_order", "mnb_gemm_act_order_workspace_bytes",
            "mnb_gemm_act_order", "mnb_gemm_group_indices", "mnb_gemm_accuracy4_workspace_bytes", "mnb_gemm_accuracy4",
-           "mnb_gemm_accuracy4_noalloc",
+           "mnb_gemm_accuracy4_noalloc", "mnb_gemm_accuracy4_codes", "mnb_rms_norm",
+           "mnb_kv4_cache_bytes", "mnb_kv4_append", "mnb_kv4_read", "mnb_attention_kv4_workspace_bytes",
+           "mnb_attention_kv4",
            "mnb_unpack_debug", "mnb_debug_prefill_rows", "mnb_status_string", "mnb_last_error", "mnb_last_variant")
 
 
@@ -44,6 +50,12 @@ class mnb_weight_desc(ctypes.Structure):
     _fields_ = [("n", ctypes.c_int64), ("k", ctypes.c_int64), ("group_size", ctypes.c_int32),
                 ("has_zero_points", ctypes.c_int32), ("scale_dtype", ctypes.c_int32),
                 ("reserved", ctypes.c_int32)]
+
+
+class mnb_kv4_desc(ctypes.Structure):
+    _fields_ = [("q_heads", ctypes.c_int32), ("kv_heads", ctypes.c_int32), ("head_dim", ctypes.c_int32),
+                ("group_size", ctypes.c_int32), ("page_size", ctypes.c_int32), ("reserved", ctypes.c_int32),
+                ("num_pages", ctypes.c_int64)]
 
 
 class mnb_layout(ctypes.Structure):
@@ -77,7 +89,8 @@ def _load():
     lib = ctypes.CDLL(LIB_PATH)
     P = ctypes.c_void_p
     D = ctypes.POINTER(mnb_weight_desc)
-    i32, i64, sz = ctypes.c_int32, ctypes.c_int64, ctypes.c_size_t
+    KV = ctypes.POINTER(mnb_kv4_desc)
+    i32, i64, sz, f32 = ctypes.c_int32, ctypes.c_int64, ctypes.c_size_t, ctypes.c_float
     sig = {
         "mnb_repacked_bytes": (sz, [D]),
         "mnb_repacked_layout": (ctypes.c_int, [D, ctypes.POINTER(mnb_layout)]),
@@ -96,6 +109,15 @@ def _load():
         "mnb_gemm_accuracy4_workspace_bytes": (sz, [D, i64]),
         "mnb_gemm_accuracy4": (ctypes.c_int, [D, P, P, i64, P, P, P, sz, P]),
         "mnb_gemm_accuracy4_noalloc": (ctypes.c_int, [D, P, P, i64, P, P, P]),
+        "mnb_gemm_accuracy4_codes": (ctypes.c_int, [D, P, P, P, i64, P, P, P]),
+        "mnb_rms_norm": (ctypes.c_int, [P, i64, P, i64, P, i64, i64, i32, f32, i32, P, P, P, P]),
+        "mnb_kv4_cache_bytes": (sz, [KV]),
+        "mnb_kv4_append": (ctypes.c_int, [KV, P, P, i64, P, P, i64, i64, i32, P, i64, P, i64, P, i64, P, P, i64,
+                                          i32, i32, P, P]),
+        "mnb_kv4_read": (ctypes.c_int, [KV, P, P, i64, P, P, i64, i64, i32, P, P, P]),
+        "mnb_attention_kv4_workspace_bytes": (sz, [KV, i64, i64, i64, i64]),
+        "mnb_attention_kv4": (ctypes.c_int, [KV, P, P, i64, P, P, i64, i64, i64, i64, i32, P, i64, f32, i32, i64, P,
+                                             P, P, sz, P]),
         "mnb_unpack_debug": (ctypes.c_int, [D, P, P, P, P]),
         "mnb_debug_prefill_rows": (ctypes.c_int32, [ctypes.c_int32]),
         "mnb_status_string": (ctypes.c_char_p, [ctypes.c_int]),
@@ -285,6 +307,151 @@ MNB_NOALLOC_SCRATCH_BYTES = 32 << 20
 def mnb_gemm_accuracy4_noalloc(w: mnb_weight_desc, repacked: Ptr, a, m: int, bias, y, stream=None) -> None:
     _check(lib.mnb_gemm_accuracy4_noalloc(ctypes.byref(w), _ptr(repacked), _ptr(a), m, _ptr(bias), _ptr(y),
                                           _stream(stream)))
+
+
+def mnb_gemm_accuracy4_codes(w: mnb_weight_desc, repacked: Ptr, codes: Ptr, scales: Ptr, m: int, bias, y,
+                             stream=None) -> None:
+    _check(lib.mnb_gemm_accuracy4_codes(ctypes.byref(w), _ptr(repacked), _ptr(codes), _ptr(scales), m, _ptr(bias),
+                                        _ptr(y), _stream(stream)))
+
+
+# ---- between the products ---------------------------------------------------
+
+def _rows(x, name: str):
+    """Address and row stride of a tensor whose rows (all dims but the first) are dense."""
+    if not x.is_cuda:
+        raise ValueError("%s: device tensor expected" % name)
+    if x.is_contiguous():
+        return x.data_ptr(), x.stride(0) if x.dim() > 1 and x.shape[0] > 1 else math.prod(x.shape[1:])
+    dense = 1
+    for n, s in zip(reversed(x.shape[1:]), reversed(x.stride()[1:])):
+        if n != 1 and s != dense:
+            raise ValueError("%s: rows must be dense" % name)
+        dense *= n
+    return x.data_ptr(), x.stride(0) if x.shape[0] > 1 else dense
+
+
+def _expect(x, name: str, dtype, shape) -> None:
+    if x.dtype != dtype:
+        raise ValueError("%s: %s expected, got %s" % (name, dtype, x.dtype))
+    if tuple(x.shape) != tuple(shape):
+        raise ValueError("%s: shape %s expected, got %s" % (name, tuple(shape), tuple(x.shape)))
+
+
+def mnb_rms_norm(x, weight, out, eps: float, residual=None, residual_out=None, scales=None, stream=None) -> None:
+    """x, residual [m, k] (rows may be strided), out and residual_out [m, k].  Without `scales` out receives the
+    values; with it (fp32 [m]) the 8-bit codes, as int8 or as fp16 integers by out's type."""
+    import torch
+    m, k = x.shape
+    dt = _dtype_code(x)
+    _expect(weight, "weight", x.dtype, (k,))
+    if scales is None:
+        kind = MNB_NORM_VALUES
+        _expect(out, "out", x.dtype, (m, k))
+    else:
+        kind = MNB_NORM_CODES_I8 if out.dtype == torch.int8 else MNB_NORM_CODES_F16
+        _expect(out, "out", torch.int8 if kind == MNB_NORM_CODES_I8 else torch.float16, (m, k))
+        _expect(scales, "scales", torch.float32, (m,))
+    xp, xs = _rows(x, "x")
+    rp, rs = None, 0
+    if residual is not None:
+        _expect(residual, "residual", x.dtype, (m, k))
+        rp, rs = _rows(residual, "residual")
+    if residual_out is not None:
+        _expect(residual_out, "residual_out", x.dtype, (m, k))
+    _check(lib.mnb_rms_norm(xp, xs, rp, rs, _ptr(weight), m, k, dt, eps, kind, _ptr(out), _ptr(scales),
+                            _ptr(residual_out), _stream(stream)))
+
+
+def kv4_desc(q_heads: int, kv_heads: int, head_dim: int, group_size: int, page_size: int,
+             num_pages: int) -> mnb_kv4_desc:
+    return mnb_kv4_desc(q_heads, kv_heads, head_dim, group_size, page_size, 0, num_pages)
+
+
+def mnb_kv4_cache_bytes(c: mnb_kv4_desc) -> int:
+    size = lib.mnb_kv4_cache_bytes(ctypes.byref(c))
+    if size == 0:
+        raise MnbError(MNB_ERR_INVALID_ARGUMENT, lib.mnb_last_error().decode())
+    return int(size)
+
+
+def _sequences(c, cache, table, kv_len, q_start):
+    """Addresses of the sequence arrays, their table stride and batch, after a look at their types and sizes."""
+    import torch
+    i32 = torch.int32
+    if table.dtype != i32 or kv_len.dtype != i32 or (q_start is not None and q_start.dtype != i32):
+        raise ValueError("block_table, kv_len and q_start: int32 expected")
+    batch = kv_len.shape[0]
+    if table.shape[0] != batch or (q_start is not None and q_start.shape[0] != batch + 1):
+        raise ValueError("block_table, kv_len and q_start: one row, length and offset (and one more) per sequence")
+    if cache.numel() * cache.element_size() < lib.mnb_kv4_cache_bytes(ctypes.byref(c)):
+        raise ValueError("cache: %d bytes expected" % mnb_kv4_cache_bytes(c))
+    tp, ts = _rows(table, "block_table")
+    return _ptr(cache), tp, ts, _ptr(kv_len), _ptr(q_start), batch
+
+
+def mnb_kv4_append(c: mnb_kv4_desc, cache, k, v, block_table, kv_len, q_start=None, cos=None, sin=None,
+                   rotary_dim: int = 0, interleaved: bool = False, q=None, q_out=None, stream=None) -> None:
+    """k, v [tokens, kv_heads, head_dim] and q [tokens, q_heads, head_dim], tokens may be strided."""
+    import torch
+    cp, tp, ts, lp, sp, batch = _sequences(c, cache, block_table, kv_len, q_start)
+    n = k.shape[0]
+    _expect(k, "k", k.dtype, (n, c.kv_heads, c.head_dim))
+    _expect(v, "v", k.dtype, (n, c.kv_heads, c.head_dim))
+    kp, ks = _rows(k, "k")
+    vp, vs = _rows(v, "v")
+    qp, qs = None, 0
+    if q is not None:
+        _expect(q, "q", k.dtype, (n, c.q_heads, c.head_dim))
+        qp, qs = _rows(q, "q")
+    if q_out is not None:
+        _expect(q_out, "q_out", k.dtype, (n, c.q_heads, c.head_dim))
+    rows = 0
+    if cos is not None:
+        rows = cos.shape[0]
+        _expect(cos, "cos", torch.float32, (rows, rotary_dim // 2))
+    if sin is not None:
+        _expect(sin, "sin", torch.float32, (rows, rotary_dim // 2))
+    _check(lib.mnb_kv4_append(ctypes.byref(c), cp, tp, ts, lp, sp, batch, n, _dtype_code(k), qp, qs, kp, ks, vp, vs,
+                              _ptr(cos), _ptr(sin), rows, rotary_dim, int(interleaved), _ptr(q_out), _stream(stream)))
+
+
+def mnb_kv4_read(c: mnb_kv4_desc, cache, block_table, kv_len, q_start, k_out=None, v_out=None, stream=None) -> None:
+    """k_out, v_out [tokens, kv_heads, head_dim]; either may be None."""
+    cp, tp, ts, lp, sp, batch = _sequences(c, cache, block_table, kv_len, q_start)
+    some = k_out if k_out is not None else v_out
+    if some is None:
+        return
+    n = some.shape[0]
+    for x, name in ((k_out, "k_out"), (v_out, "v_out")):
+        if x is not None:
+            _expect(x, name, some.dtype, (n, c.kv_heads, c.head_dim))
+    _check(lib.mnb_kv4_read(ctypes.byref(c), cp, tp, ts, lp, sp, batch, n, _dtype_code(some), _ptr(k_out), _ptr(v_out),
+                            _stream(stream)))
+
+
+def mnb_attention_kv4_workspace_bytes(c: mnb_kv4_desc, batch: int, tokens: int, max_q: int, max_kv: int) -> int:
+    return int(lib.mnb_attention_kv4_workspace_bytes(ctypes.byref(c), batch, tokens, max_q, max_kv))
+
+
+def mnb_attention_kv4(c: mnb_kv4_desc, cache, q, block_table, kv_len, q_start, max_q: int, max_kv: int, out,
+                      scale: float, causal: bool = True, window: int = 0, lse=None, workspace: Ptr = None,
+                      workspace_bytes: Optional[int] = None, stream=None) -> None:
+    """q [tokens, q_heads, head_dim] (tokens may be strided), out the same, lse fp32 [tokens, q_heads]."""
+    import torch
+    cp, tp, ts, lp, sp, batch = _sequences(c, cache, block_table, kv_len, q_start)
+    n = q.shape[0]
+    _expect(q, "q", q.dtype, (n, c.q_heads, c.head_dim))
+    _expect(out, "out", q.dtype, (n, c.q_heads, c.head_dim))
+    if lse is not None:
+        _expect(lse, "lse", torch.float32, (n, c.q_heads))
+    if workspace_bytes is None:
+        workspace_bytes = 0 if workspace is None or isinstance(workspace, int) else \
+            workspace.numel() * workspace.element_size()
+    qp, qs = _rows(q, "q")
+    _check(lib.mnb_attention_kv4(ctypes.byref(c), cp, tp, ts, lp, sp, batch, n, max_q, max_kv, _dtype_code(q), qp, qs,
+                                 scale, int(causal), window, _ptr(out), _ptr(lse), _ptr(workspace), workspace_bytes,
+                                 _stream(stream)))
 
 
 def mnb_unpack_debug(w: mnb_weight_desc, repacked: Ptr, codes: Ptr, w_f32: Ptr, stream=None) -> None:

@@ -346,6 +346,146 @@ mnb_status mnb_gemm_accuracy4(const mnb_weight_desc* w, const void* repacked, co
 mnb_status mnb_gemm_accuracy4_noalloc(const mnb_weight_desc* w, const void* repacked, const float* a,
                                       int64_t m, const float* bias, float* y, void* stream);
 
+/* ---- Between the products of a decoder layer --------------------------------
+ * An RMS norm, a paged key/value cache held in 4 bits, and the attention that
+ * reads it.  Conventions as above (streams, ownership, errors); in addition:
+ * - dtype is MNB_F16 or MNB_F32, the type of every activation operand of the
+ *   call.  Arrays that take a stride are rows of dense elements, `stride`
+ *   elements apart (slices of a wider array), and need only element alignment;
+ *   the others are dense.
+ * - lengths, offsets and page numbers are device data the host does not see.
+ *   A value out of its range gives wrong results for that sequence, never an
+ *   access outside the arrays described by the host's arguments.
+ */
+
+/* RMS norm of the residual stream, rows of k elements:
+ *   h = x + residual (rounded to dtype; residual NULL: h = x),
+ *   y = h * (mean(h^2) + eps)^(-1/2) * weight.
+ * weight [k] and residual_out [m, k] (NULL: not wanted; receives h) of dtype.
+ * out_kind (an mnb_norm_out):
+ *   MNB_NORM_VALUES     out [m, k] of dtype, y rounded once; scales NULL.
+ *   MNB_NORM_CODES_F16  8-bit codes q as fp16 integers, out fp16 [m, k], and
+ *   MNB_NORM_CODES_I8   the same codes as int8 [m, k]; scales fp32 [m]:
+ *     s = max|y| / 127 and q = y / s to the nearest integer, halves away from
+ *     zero, formed as 127 h w / max|h w| (the norm's factor cancels) in 64
+ *     bits from the product h w in binary32.  A row of zeros has s = 0 and
+ *     codes 0; a row that holds a NaN or an infinity has s = NaN.
+ *     MNB_NORM_CODES_F16 is what mnb_gemm_accuracy4_codes takes.
+ * Sums are kept in fp32.  residual_out may be x or residual themselves where
+ * their stride is k.  m <= 2^31-1, 1 <= k <= 2^31-16; m == 0 is a no-op. */
+typedef enum { MNB_NORM_VALUES = 0, MNB_NORM_CODES_F16 = 1, MNB_NORM_CODES_I8 = 2 } mnb_norm_out;
+mnb_status mnb_rms_norm(const void* x, int64_t x_stride, const void* residual, int64_t residual_stride,
+                        const void* weight, int64_t m, int64_t k, int32_t dtype, float eps, int32_t out_kind,
+                        void* out, float* scales, void* residual_out, void* stream);
+
+/* mnb_gemm_accuracy4 on activations that are in 8 bits already: codes fp16
+ * integers in -127..127 [m, k] (16-byte aligned) and scales fp32 [m], as
+ * mnb_rms_norm writes them:
+ *   y[m,n] = scales[m] * sum_b scale[n,b] * sum_{k in b} codes[m,k] * (code[n,k] - zp[n,b]) (+ bias[n]),
+ * the inner sums exact.  y and bias fp32.  No workspace.  A row whose scale is
+ * 0 gives bias (or 0).  Limits and errors as mnb_gemm with fp16 activations. */
+mnb_status mnb_gemm_accuracy4_codes(const mnb_weight_desc* w, const void* repacked, const void* codes,
+                                    const float* scales, int64_t m, const float* bias, float* y, void* stream);
+
+/* The 4-bit cache of one layer.  q_heads % kv_heads == 0 (query heads
+ * h*q_heads/kv_heads .. share key head h); head_dim 64, 128 or 256; group_size
+ * 32, 64 or 128 and at most head_dim; head_dim / group_size at most 8;
+ * page_size 32, 64, 128 or 256 tokens (else MNB_ERR_UNSUPPORTED).
+ *
+ * A group of group_size consecutive values of one token and head is stored as
+ * 4-bit codes c, an fp16 scale s and a zero point z in 0..15, and stands for
+ * (c - z) * s:
+ *   lo = min(0, min x), hi = max(0, max x), s = fp16((hi - lo) * (1/15)),
+ *   z = clamp(rne(-lo * (1/s)), 0, 15), c = clamp(rne(x * (1/s)) + z, 0, 15),
+ * each step rounded once to binary32.  s = 0 stores zeros.  A group with a NaN
+ * or an infinity, or whose scale passes fp16, reads back as NaN.
+ *
+ * Layout: page p, head h, block i of 32 tokens is at
+ *   ((p * kv_heads + h) * (page_size/32) + i) * B,  B = 32 D + 256 G,
+ * with D = head_dim, G = D / group_size.  Inside a block, for token t in 0..31:
+ *   bytes [0, 16 D): key codes.  Words of 8 codes d = 8e .. 8e+7 in the nibble
+ *     order of the repacked weights (slots 0..7 hold offsets 0,2,4,6,1,3,5,7).
+ *     With W = (t div 16)*(D/32) + e div 4, the word is at byte
+ *     1024 (W div 4) + 16 (16 (e mod 4) + t mod 16) + 4 (W mod 4).
+ *   bytes [16 D, 32 D): value codes.  The codes of dims d and d + 16, for d mod
+ *     32 < 16, are the low and high nibble of the byte at 16 D + 1024 (d div 64)
+ *     + 16 (16 ((t mod 16) div 4) + d mod 16) + 8 ((d div 32) mod 2) + 4 (t div 16)
+ *     + (0,2,1,3)[t mod 4].
+ *   bytes [32 D, 32 D + 128 G): word t G + g: key scale of group g (fp16, low
+ *     half) and its zero point (bits 16..19, the bits above 0).
+ *   bytes [32 D + 128 G, B): the same for the values.
+ * These are the operand distributions of v_mfma_f32_16x16x32_f16 in the
+ * attention's two products; no byte holds two tokens. */
+typedef struct {
+    int32_t q_heads, kv_heads, head_dim, group_size, page_size;
+    int32_t reserved; /* must be 0 */
+    int64_t num_pages;
+} mnb_kv4_desc;
+
+/* Bytes of the cache; 0 if `c` is invalid (mnb_last_error() says why).  Host
+ * only.  The cache is device memory, 256-byte aligned; it needs no
+ * initialisation. */
+size_t mnb_kv4_cache_bytes(const mnb_kv4_desc* c);
+
+/* The sequences of a call, in device memory (int32, 4-byte aligned):
+ *   block_table [batch, table_stride]: pages of each sequence, in order; only
+ *     entries of pages that hold tokens are used.
+ *   kv_len [batch]: tokens of each sequence, the new ones included.
+ *   q_start [batch + 1]: rows of the new tokens, q_start[b] .. q_start[b+1]-1 for
+ *     sequence b, non-decreasing; NULL: one each, row b (then tokens == batch).
+ * A sequence with n new tokens has them at positions kv_len - n .. kv_len - 1. */
+
+/* Append: for each new token (row of q, k, v) the keys are rotated by their
+ * position and stored with the values; the queries are rotated into q_out
+ * [tokens, q_heads, head_dim] (q and q_out NULL: no queries).  q is [tokens,
+ * q_heads, head_dim], k and v [tokens, kv_heads, head_dim], tokens *_stride
+ * elements apart.  Rotation: cos and sin fp32 [rope_rows, rotary_dim/2] (both
+ * NULL: none; rotary_dim a multiple of 16, at most head_dim, else
+ * MNB_ERR_UNSUPPORTED); at position t, the pair (a, b) becomes (a cos - b sin,
+ * b cos + a sin), pairs (i, i + rotary_dim/2), or with interleaved != 0 (2i,
+ * 2i+1); dims from rotary_dim on pass.  q_out is rounded once; keys are
+ * quantized from binary32.  A position past rope_rows uses the last row.  A
+ * token whose position is negative, past the table or on a page outside
+ * 0..num_pages-1 is not stored (padding may use page -1).  Two tokens of one
+ * call must not share a place.  Rows past q_start[batch] are ignored but for
+ * q_out, which gets them rotated by position 0. */
+mnb_status mnb_kv4_append(const mnb_kv4_desc* c, void* cache, const int32_t* block_table, int64_t table_stride,
+                          const int32_t* kv_len, const int32_t* q_start, int64_t batch, int64_t tokens,
+                          int32_t dtype, const void* q, int64_t q_stride, const void* k, int64_t k_stride,
+                          const void* v, int64_t v_stride, const float* cos, const float* sin, int64_t rope_rows,
+                          int32_t rotary_dim, int32_t interleaved, void* q_out, void* stream);
+
+/* Read: the stored keys and values of the same rows as values, k_out and v_out
+ * [tokens, kv_heads, head_dim] of dtype (either may be NULL), each (c - z) * s
+ * rounded once; zeros for a token that has no place.  With n = kv_len the whole
+ * sequence is read. */
+mnb_status mnb_kv4_read(const mnb_kv4_desc* c, const void* cache, const int32_t* block_table, int64_t table_stride,
+                        const int32_t* kv_len, const int32_t* q_start, int64_t batch, int64_t tokens,
+                        int32_t dtype, void* k_out, void* v_out, void* stream);
+
+/* Attention of the new tokens' queries over the cache:
+ *   out[t, h] = sum_j softmax_j(scale * q[t, h] . K[j]) V[j]
+ * over the keys j of t's sequence that t sees: j < kv_len; with causal != 0
+ * also j <= position of t, and with window > 0 (causal only) j > position -
+ * window.  A row that sees no key gives zeros (lse -infinity).  Keys that are
+ * hidden from a row do not touch it, NaN and infinity included.
+ * q [tokens, q_heads, head_dim], tokens q_stride elements apart; out the same,
+ * dense; lse NULL or fp32 [tokens, q_heads], the natural logarithm of the
+ * sum of exponentials.  max_q and max_kv bound the new tokens and the length of
+ * every sequence (they shape the grid; tokens past max_q get no output, keys
+ * past max_kv are not seen and positions count from min(kv_len, max_kv)).
+ * Logits, sums and outputs are kept in fp32.
+ * workspace (256-byte aligned): mnb_attention_kv4_workspace_bytes of the same
+ * arguments; contents need no initialisation.  batch <= 65535, max_kv <=
+ * 2^30.  Deterministic. */
+size_t mnb_attention_kv4_workspace_bytes(const mnb_kv4_desc* c, int64_t batch, int64_t tokens, int64_t max_q,
+                                         int64_t max_kv);
+mnb_status mnb_attention_kv4(const mnb_kv4_desc* c, const void* cache, const int32_t* block_table,
+                             int64_t table_stride, const int32_t* kv_len, const int32_t* q_start, int64_t batch,
+                             int64_t tokens, int64_t max_q, int64_t max_kv, int32_t dtype, const void* q,
+                             int64_t q_stride, float scale, int32_t causal, int64_t window, void* out, float* lse,
+                             void* workspace, size_t workspace_bytes, void* stream);
+
 /* Test-only: decode a repacked buffer with the production unpack code.
  * codes: device u8 [N,K] (the stored nibbles); w_f32: device f32 [N,K], the
  * dequantized weights (code - zp) * scale rounded once to fp32.  Either

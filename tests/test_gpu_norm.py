@@ -1,0 +1,192 @@
+"""RMS norm and its 8-bit codes on the GPU against the 64-bit oracle."""
+import numpy as np
+import pytest
+
+from oracle import decoder as o
+from oracle import oracle as mo
+from block_wise_int4_amd import synth
+from tests import gpu_util as G
+
+pytestmark = pytest.mark.gpu
+EPS = 1e-5
+
+
+@pytest.fixture(scope="module")
+def mnb():
+    from block_wise_int4_amd import mnb as m
+    return m
+
+
+def _inputs(m, k, dt, seed, spread=3.0):
+    rng = np.random.default_rng((900, m, k, seed))
+    t = np.float16 if dt == "f16" else np.float32
+    x = rng.normal(size=(m, k)).astype(t)
+    r = (rng.normal(size=(m, k)) * np.exp(rng.normal(size=(1, k)) * spread / 3)).astype(t)
+    w = (1 + 0.2 * rng.normal(size=k)).astype(t)
+    return x, r, w
+
+
+def _dev(a):
+    return G.torch().from_numpy(np.ascontiguousarray(a)).cuda()
+
+
+def _value_tolerance(y, k, dt):
+    # sum of squares in fp32 (k additions at most, halved by the root), the
+    # root, reciprocal and two products, then the output's rounding
+    rel = (0.5 * (k + 2) + 6) * o.EPS32
+    return np.abs(y) * (rel + (o.EPS16 * 1.001 if dt == "f16" else o.EPS32)) + (2.0 ** -25 if dt == "f16" else 2.0 ** -149)
+
+
+def _check_codes(codes, scales, h, w, k, dt):
+    s, q = o.norm_codes(h, w, EPS)
+    assert (np.abs(scales - s) <= s * (0.5 * (k + 2) + 10) * o.EPS32).all()
+    # the quotient is off by the roundings of h w and of the largest product:
+    # none in fp16 (11 + 11 bits), 2 x 2^-24 in fp32
+    off = 0.0 if dt == "f16" else 2 * 127 * o.EPS32
+    d = np.abs(codes.astype(np.float64) - q)
+    assert (d <= 0.5 + off + 1e-12).all()
+    half = np.abs(np.abs(q) % 1 - 0.5) < 1e-13      # an exact tie goes away from zero
+    assert (np.abs(codes[half]) > np.abs(q[half])).all()
+
+
+SHAPES = [(1, 1), (1, 7), (3, 64), (2, 100), (5, 513), (1, 4096), (16, 4096), (33, 4104), (4, 8191), (2, 11008),
+          (3, 20001), (300, 96)]
+
+
+@pytest.mark.parametrize("dt", ["f16", "f32"])
+@pytest.mark.parametrize("m,k", SHAPES)
+def test_values(mnb, m, k, dt):
+    t = G.torch()
+    x, r, w = _inputs(m, k, dt, 1)
+    out, ro = t.empty((m, k), dtype=_dev(x).dtype, device="cuda"), t.empty((m, k), dtype=_dev(x).dtype, device="cuda")
+    for res in (r, None):
+        mnb.mnb_rms_norm(_dev(x), _dev(w), out, EPS, residual=None if res is None else _dev(res), residual_out=ro)
+        h, y = o.rms_norm(x, res, w, EPS)
+        assert (ro.cpu().numpy() == h).all()
+        err = np.abs(G.host(out) - y)
+        assert (err <= _value_tolerance(y, k, dt)).all(), float((err / _value_tolerance(y, k, dt)).max())
+    mnb.mnb_rms_norm(_dev(x), _dev(w), out, EPS)       # no stream wanted
+    assert (np.abs(G.host(out) - y) <= _value_tolerance(y, k, dt)).all()
+
+
+@pytest.mark.parametrize("dt", ["f16", "f32"])
+@pytest.mark.parametrize("m,k", SHAPES)
+def test_codes(mnb, m, k, dt):
+    t = G.torch()
+    x, r, w = _inputs(m, k, dt, 2)
+    if m > 2:
+        x[1], r[1] = 0, 0                              # a row of zeros
+    h, _ = o.rms_norm(x, r, w, EPS)
+    sc = t.empty(m, device="cuda")
+    both = []
+    for kind in (t.float16, t.int8):
+        out = t.full((m, k), 99, dtype=kind, device="cuda")
+        sc.fill_(-1.0)
+        mnb.mnb_rms_norm(_dev(x), _dev(w), out, EPS, residual=_dev(r), scales=sc)
+        both.append(G.host(out))
+        _check_codes(both[-1], G.host(sc), h, w, k, dt)
+    assert (both[0] == both[1]).all()
+
+
+def test_exact_ties_go_away_from_zero(mnb):
+    t = G.torch()
+    k = 64
+    x = np.zeros((1, k), np.float16)
+    x[0, :6] = [254, 1, -1, 3, -3, 5]                  # quotients 127, +-0.5, +-1.5, 2.5
+    out, sc = t.empty((1, k), dtype=t.int8, device="cuda"), t.empty(1, device="cuda")
+    mnb.mnb_rms_norm(_dev(x), _dev(np.ones(k, np.float16)), out, EPS, scales=sc)
+    assert out.cpu().numpy()[0, :7].tolist() == [127, 1, -1, 2, -2, 3, 0]
+
+
+def test_strided_rows_and_unaligned_slices(mnb):
+    t = G.torch()
+    rng = np.random.default_rng(7)
+    for k, pad, off in ((96, 5, 1), (4096, 3, 3), (129, 130, 0)):
+        wide = rng.normal(size=(6, k + pad)).astype(np.float16)
+        res = rng.normal(size=(6, k + 7)).astype(np.float16)
+        w = rng.normal(size=k + 1).astype(np.float16)
+        xd, rd, wd = _dev(wide)[:, off:off + k], _dev(res)[:, 7:7 + k], _dev(w)[1:]
+        buf = t.full((6 * k + 2,), 77.0, dtype=t.float16, device="cuda")
+        out = buf[1:1 + 6 * k].view(6, k)
+        mnb.mnb_rms_norm(xd, wd, out, EPS, residual=rd)
+        _, y = o.rms_norm(wide[:, off:off + k], res[:, 7:7 + k], w[1:], EPS)
+        assert (np.abs(G.host(out) - y) <= _value_tolerance(y, k, "f16")).all()
+        assert buf[0] == 77 and buf[-1] == 77
+
+
+@pytest.mark.parametrize("k", [96, 4096, 40000])
+def test_the_stream_in_place(mnb, k):
+    t = G.torch()
+    x, r, w = _inputs(5, k, "f16", 3)
+    h, y = o.rms_norm(x, r, w, EPS)
+    for into in ("x", "r"):
+        xd, rd, out = _dev(x), _dev(r), t.empty((5, k), dtype=t.float16, device="cuda")
+        ro = xd if into == "x" else rd
+        mnb.mnb_rms_norm(xd, _dev(w), out, EPS, residual=rd, residual_out=ro)
+        assert (ro.cpu().numpy() == h).all()
+        assert (np.abs(G.host(out) - y) <= _value_tolerance(y, k, "f16")).all()
+
+
+def test_rows_with_nan_and_infinity_stay_apart(mnb):
+    t = G.torch()
+    x, r, w = _inputs(4, 500, "f16", 4)
+    x[1, 3], x[2, 499] = np.nan, np.inf
+    sc, out = t.empty(4, device="cuda"), t.empty((4, 500), dtype=t.float16, device="cuda")
+    mnb.mnb_rms_norm(_dev(x), _dev(w), out, EPS, residual=_dev(r))
+    y = G.host(out)
+    good = [0, 3]
+    _, want = o.rms_norm(x[good], r[good], w, EPS)
+    assert (np.abs(y[good] - want) <= _value_tolerance(want, 500, "f16")).all()
+    assert np.isnan(y[1]).all() and np.isnan(y[2, 499])
+    mnb.mnb_rms_norm(_dev(x), _dev(w), out, EPS, residual=_dev(r), scales=sc)
+    assert np.isnan(G.host(sc)[1:3]).all() and np.isfinite(G.host(sc)[good]).all()
+
+
+def test_large_row_count_and_offsets(mnb):
+    # 40000 rows of 8200: row offsets pass 2^28 elements; the last rows are checked
+    t = G.torch()
+    m, k = 40000, 8200
+    x = t.zeros((m, k), dtype=t.float16, device="cuda")
+    tail = np.random.default_rng(8).normal(size=(2, k)).astype(np.float16)
+    x[-2:] = _dev(tail)
+    out = t.empty_like(x)
+    w = np.ones(k, np.float16)
+    mnb.mnb_rms_norm(x, _dev(w), out, EPS)
+    _, y = o.rms_norm(tail, None, w, EPS)
+    assert (np.abs(G.host(out[-2:]) - y) <= _value_tolerance(y, k, "f16")).all()
+    assert not out[:-2].any()
+
+
+@pytest.mark.parametrize("M", [1, 2, 16, 17, 48, 70])
+def test_codes_into_the_int4_product(mnb, M):
+    """norm -> codes -> product, against the exact product of the codes the GPU wrote."""
+    t = G.torch()
+    N, K, g = 130, 512, 64
+    w = synth.weight(N, K, g, "f16", (0.005, 0.02), True, (910, M))
+    q = G.upload(w)
+    x, r, nw = _inputs(M, K, "f32", 5)
+    codes, sc = t.empty((M, K), dtype=t.float16, device="cuda"), t.empty(M, device="cuda")
+    mnb.mnb_rms_norm(_dev(x), _dev(nw), codes, EPS, residual=_dev(r), scales=sc)
+    bias = np.random.default_rng(9).normal(size=N).astype(np.float32)
+    y = t.empty((M, N), device="cuda")
+    W = mo.dequant(w.packed, w.scales, w.zero_points, N, K, g)
+    c64, s64 = G.host(codes), G.host(sc)
+    for b in (None, bias):
+        mnb.mnb_gemm_accuracy4_codes(q.desc, q.repacked, codes, sc, M, None if b is None else _dev(b), y)
+        want = (c64 @ W.T) * s64[:, None] + (0 if b is None else b)
+        size = (np.abs(c64) @ np.abs(W).T) * s64[:, None] + (0 if b is None else np.abs(b))
+        # exact group sums, each scaled and added in fp32
+        assert (np.abs(G.host(y) - want) <= size * (K // g + 8) * o.EPS32).all()
+
+
+def test_binding_refuses_wrong_tensors(mnb):
+    t = G.torch()
+    x, w = t.zeros((2, 64), dtype=t.float16, device="cuda"), t.ones(64, dtype=t.float16, device="cuda")
+    with pytest.raises(ValueError):
+        mnb.mnb_rms_norm(x, w.float(), t.empty_like(x), EPS)
+    with pytest.raises(ValueError):
+        mnb.mnb_rms_norm(x, w, t.empty((2, 63), dtype=t.float16, device="cuda"), EPS)
+    with pytest.raises(ValueError):
+        mnb.mnb_rms_norm(x.t(), w[:2], t.empty((64, 2), dtype=t.float16, device="cuda"), EPS)
+    with pytest.raises(ValueError):
+        mnb.mnb_rms_norm(x, w, t.empty_like(x).float(), EPS, scales=t.empty(2, device="cuda"))
