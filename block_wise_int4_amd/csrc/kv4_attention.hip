@@ -37,7 +37,6 @@ namespace mnb {
 
 namespace {
 
-constexpr int kWaves = 4;
 constexpr float kLow = -1e30f;        // "no key yet": finite, so differences stay numbers
 
 struct AttnParams {
@@ -67,10 +66,15 @@ __device__ __forceinline__ h8_t join(const h2_t q[4])
     return h8_t{q[0][0], q[0][1], q[1][0], q[1][1], q[2][0], q[2][1], q[3][0], q[3][1]};
 }
 
-// exponent e with |s| < 2^e of a finite fp16 value as fp32 (0 gives a low one)
-__device__ __forceinline__ float top_exponent(float s)
+// e with s < 2^e of an fp16 scale (low half of a word): -14 for zero and
+// subnormals, 17 for infinity and NaN
+__device__ __forceinline__ float top_exponent(uint32_t word) { return (float)((int)((word >> 10) & 31u) - 14); }
+
+typedef uint16_t us2_t __attribute__((ext_vector_type(2)));
+// the larger of both halves each: of two words, the larger scale in the low half
+__device__ __forceinline__ uint32_t max_halves(uint32_t a, uint32_t b)
 {
-    return (float)((int)((__builtin_bit_cast(uint32_t, s) >> 23) & 255u) - 126);
+    return __builtin_bit_cast(uint32_t, __builtin_elementwise_max(__builtin_bit_cast(us2_t, a), __builtin_bit_cast(us2_t, b)));
 }
 
 // Length and new tokens of a sequence, within the bounds of the call.
@@ -171,15 +175,17 @@ template <int NG> __device__ __forceinline__ void four_keys(const uint32_t* slot
 
 __device__ __forceinline__ float scale_of(uint32_t m) { return (float)__builtin_bit_cast(_Float16, (uint16_t)m); }
 
-template <int D, int NG, bool F32, bool SPLIT, int NR, int KW>
-__global__ __launch_bounds__(kWaves * 64) void kv4_attention_kernel(AttnParams p)
+// KW waves share the keys of a row set, RW row sets make a workgroup; PF blocks
+// of a wave are in registers, all but the one in work still on their way.
+template <int D, int NG, bool F32, bool SPLIT, int NR, int KW, int RW, int PF>
+__global__ __launch_bounds__(KW * RW * 64) void kv4_attention_kernel(AttnParams p)
 {
+    constexpr int kWaves = KW * RW;
     typedef typename std::conditional<F32, float, _Float16>::type T;
     constexpr int NJ = D / 32;                 // 32-dim steps of the first product
     constexpr int NT = D / 16;                 // 16-dim tiles of the second
     constexpr int NQ = F32 ? 2 : 1;            // fp16 parts of q
     constexpr int JG = NJ / NG;                // steps per group
-    constexpr int RW = kWaves / KW;            // waves with rows of their own
     constexpr int kRows = RW * NR * 16;
 
     const KvView& v = p.v;
@@ -208,7 +214,7 @@ __global__ __launch_bounds__(kWaves * 64) void kv4_attention_kernel(AttnParams p
 
     // the rows of this wave: queries as the B operand, row = column of the lane
     h8_t qf[NR][NQ][NJ];
-    float qs[NR];                              // logit factor of the lane's row
+    float qs[NR];                              // fp32 queries: the factor that was taken out of the lane's row
     int64_t out_row[NR];                       // (token, head) index, < 0: none
     int pos[NR];                               // last key the row sees
 #pragma unroll
@@ -220,7 +226,6 @@ __global__ __launch_bounds__(kWaves * 64) void kv4_attention_kernel(AttnParams p
         const T* q = static_cast<const T*>(p.q) + (int64_t)(s.first + token) * p.q_stride + (int64_t)head * D + 8 * quarter;
         out_row[n] = live ? (int64_t)(s.first + token) * v.q_heads + head : -1;
         pos[n] = p.causal ? s.len - s.count + token : s.len - 1;
-        qs[n] = p.scale_log2;
         if constexpr (!F32) {
             typedef uint32_t raw __attribute__((ext_vector_type(4), aligned(2), may_alias));
 #pragma unroll
@@ -241,7 +246,7 @@ __global__ __launch_bounds__(kWaves * 64) void kv4_attention_kernel(AttnParams p
             int e = mx > 0.0f ? (int)(__builtin_bit_cast(uint32_t, mx) >> 23) - 127 - 14 : 0;
             e = e < -126 ? -126 : e;
             const float down = __builtin_bit_cast(float, (uint32_t)(127 - e) << 23);
-            qs[n] *= __builtin_bit_cast(float, (uint32_t)(127 + e) << 23);
+            qs[n] = __builtin_bit_cast(float, (uint32_t)(127 + e) << 23);
 #pragma unroll
             for (int j = 0; j < NJ; ++j)
 #pragma unroll
@@ -319,67 +324,62 @@ __global__ __launch_bounds__(kWaves * 64) void kv4_attention_kernel(AttnParams p
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
 #pragma unroll
-                for (int n = 0; n < NR; ++n) {
-                    float f = 0.0f;
+                for (int g = 0; g < NG; ++g) {
+                    const float ks = scale_of(kw4[i * NG + g]) * p.scale_log2;
 #pragma unroll
-                    for (int g = 0; g < NG; ++g) {
-                        const float ks = scale_of(kw4[i * NG + g]);
-                        f = g == 0 ? acc[n][g][i] * ks : __builtin_fmaf(acc[n][g][i], ks, f);
-                    }
-                    x[n][t][i] = f * qs[n];
+                    for (int n = 0; n < NR; ++n)
+                        x[n][t][i] = g == 0 ? acc[n][g][i] * ks : __builtin_fmaf(acc[n][g][i], ks, x[n][t][i]);
+                }
+                if constexpr (F32) {
+#pragma unroll
+                    for (int n = 0; n < NR; ++n) x[n][t][i] *= qs[n];
                 }
             }
         }
-        // ---- value scales' exponents and masks ----
-        float ve[2][4], top = -24.0f;
+        // ---- masks, and the running reference: the largest logit plus the exponent of its value scale ----
+        uint32_t vw[2][4 * NG];
 #pragma unroll
-        for (int t = 0; t < 2; ++t) {
-            uint32_t vw4[4 * NG];
-            four_keys<NG>(slot + (32 + t * 16 + 4 * quarter) * NG, vw4);
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                float m = scale_of(vw4[i * NG]);
-#pragma unroll
-                for (int g = 1; g < NG; ++g) m = fmaxf(m, scale_of(vw4[i * NG + g]));
-                ve[t][i] = fmaxf(fminf(top_exponent(m), 16.0f), -24.0f);
-                top = fmaxf(top, ve[t][i]);
-            }
-        }
+        for (int t = 0; t < 2; ++t) four_keys<NG>(slot + (32 + t * 16 + 4 * quarter) * NG, vw[t]);
         const bool edge = blk * 32 + 32 > whole || blk * 32 < open;
         uint32_t seen[NR];                     // bit 4 t + i: the row sees the key
-        if (edge) {
+        float mxs[NR];
+        if (edge) {                            // key by key: a hidden key's scale is not looked at
 #pragma unroll
             for (int n = 0; n < NR; ++n) {
                 seen[n] = 0;
+                mxs[n] = -__builtin_inff();
                 const int below = p.causal && p.window > 0 ? pos[n] - p.window : -1;
 #pragma unroll
                 for (int t = 0; t < 2; ++t)
 #pragma unroll
                     for (int i = 0; i < 4; ++i) {
                         const int key = blk * 32 + t * 16 + 4 * quarter + i;
+                        uint32_t w = vw[t][i * NG];
+#pragma unroll
+                        for (int g = 1; g < NG; ++g) w = max_halves(w, vw[t][i * NG + g]);
                         if (key <= pos[n] && key > below && key < s.len)
                             seen[n] |= 1u << (4 * t + i);
                         else
                             x[n][t][i] = -__builtin_inff();
+                        mxs[n] = fmaxf(mxs[n], x[n][t][i] + top_exponent(w));
                     }
             }
+        } else {
+            uint32_t w = vw[0][0];
+#pragma unroll
+            for (int k = 1; k < 8 * NG; ++k) w = max_halves(w, vw[k / (4 * NG)][k % (4 * NG)]);
+            const float top = top_exponent(w);
+#pragma unroll
+            for (int n = 0; n < NR; ++n) {
+                float m = x[n][0][0];
+#pragma unroll
+                for (int k = 1; k < 8; ++k) m = fmaxf(m, x[n][k >> 2][k & 3]);
+                mxs[n] = m + top;
+            }
         }
-        // ---- running reference: the largest logit plus the exponent of its value scale ----
 #pragma unroll
         for (int n = 0; n < NR; ++n) {
-            float mx = -__builtin_inff();
-            if (edge) {                        // key by key: a hidden key's scale is not looked at
-#pragma unroll
-                for (int t = 0; t < 2; ++t)
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) mx = fmaxf(mx, x[n][t][i] + ve[t][i]);
-            } else {
-#pragma unroll
-                for (int t = 0; t < 2; ++t)
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) mx = fmaxf(mx, x[n][t][i]);
-                mx += top;
-            }
+            float mx = mxs[n];
             if (__builtin_amdgcn_ballot_w64(mx > M[n] + 14.0f)) {
                 mx = fmaxf(mx, __shfl_xor(mx, 16));
                 mx = fmaxf(mx, __shfl_xor(mx, 32));
@@ -402,26 +402,28 @@ __global__ __launch_bounds__(kWaves * 64) void kv4_attention_kernel(AttnParams p
                     l[n] += x[n][t][i];
                 }
         // ---- O^T += V^T (p s')^T, group by group ----
-        uint32_t vw[2][4 * NG];
-#pragma unroll
-        for (int t = 0; t < 2; ++t) four_keys<NG>(slot + (32 + t * 16 + 4 * quarter) * NG, vw[t]);
 #pragma unroll
         for (int g = 0; g < NG; ++g) {
             h8_t pb[NR], pl[NR];               // p s' as the B operand, its second part
+            float f[NR][8];
 #pragma unroll
-            for (int t = 0; t < 2; ++t)
+            for (int k = 0; k < 8; ++k) {
+                const float vs = scale_of(vw[k >> 2][(k & 3) * NG + g]);
 #pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    const float vs = scale_of(vw[t][i * NG + g]);
+                for (int n = 0; n < NR; ++n) f[n][k] = x[n][k >> 2][k & 3] * vs;
+            }
+            if (edge) {                        // a hidden key adds nothing whatever its scale is
 #pragma unroll
-                    for (int n = 0; n < NR; ++n) {
-                        float f = x[n][t][i] * vs;
-                        // a hidden key adds nothing whatever its scale is
-                        if (edge) f = (seen[n] >> (4 * t + i)) & 1u ? f : 0.0f;
-                        const _Float16 hi16 = (_Float16)f;
-                        pb[n][4 * t + i] = hi16;
-                        if constexpr (SPLIT) pl[n][4 * t + i] = (_Float16)(f - (float)hi16);
-                    }
+                for (int n = 0; n < NR; ++n)
+#pragma unroll
+                    for (int k = 0; k < 8; ++k) f[n][k] = (seen[n] >> k) & 1u ? f[n][k] : 0.0f;
+            }
+#pragma unroll
+            for (int n = 0; n < NR; ++n)
+#pragma unroll
+                for (int k = 0; k < 8; ++k) {
+                    pb[n][k] = (_Float16)f[n][k];
+                    if constexpr (SPLIT) pl[n][k] = (_Float16)(f[n][k] - (float)pb[n][k]);
                 }
             // zero points of the lane's 8 keys, in the pairs of the unpack
             h2_t zl[4], zh[4];
@@ -461,21 +463,32 @@ __global__ __launch_bounds__(kWaves * 64) void kv4_attention_kernel(AttnParams p
         __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");   // before the slot's next words
     };
 
-    // ---- the wave's blocks, one ahead in flight ----
+    // ---- the wave's blocks, PF register sets in turn ----
     int blk = blk0 + kw;
     if (blk < blk1) {
-        RawBlock<D, NG> cur, nxt;
-        load_block<D, NG>(block_at(page_of(blk), blk), lane, cur);
-        int page = page_of(blk + KW);
+        RawBlock<D, NG> set[PF];
+        // the block after the last is the last again: requested, not used
+        auto within = [&](int k) { return k < blk1 ? k : blk; };
+#pragma unroll
+        for (int i = 0; i < PF; ++i) {
+            const int k = within(blk + i * KW);
+            load_block<D, NG>(block_at(page_of(k), k), lane, set[i]);
+        }
+        int page = page_of(blk + PF * KW);     // of the block that the next load fetches
         while (true) {
-            const int after = blk + KW;
-            const int ahead = after < blk1 ? after : blk;   // the last block is requested again, unused
-            load_block<D, NG>(block_at(after < blk1 ? page : page_of(blk), ahead), lane, nxt);
-            page = page_of(after + KW);
-            compute(cur, blk);
-            if (after >= blk1) break;
-            cur = nxt;
-            blk = after;
+            bool more = true;
+#pragma unroll
+            for (int i = 0; i < PF; ++i) {
+                if (!more) break;
+                const int next = blk + PF * KW;
+                const int after = page_of(next + KW);
+                compute(set[i], blk);
+                if (next < blk1) load_block<D, NG>(block_at(page, next), lane, set[i]);
+                page = after;
+                blk += KW;
+                more = blk < blk1;
+            }
+            if (!more) break;
         }
     }
 #pragma unroll
@@ -484,9 +497,10 @@ __global__ __launch_bounds__(kWaves * 64) void kv4_attention_kernel(AttnParams p
         l[n] += __shfl_xor(l[n], 32);
     }
 
-    // ---- waves of the same rows join through LDS, 16 rows by 128 dims at a time ----
+    // ---- waves of the same rows join through LDS, 16 rows by up to 128 dims at a time ----
     if constexpr (KW > 1) {
-        constexpr int kDims = D < 128 ? D : 128, kPitch = kDims + 4;   // rows start in different banks
+        constexpr int kMost = KW > 4 ? 64 : 128;           // at most 34 KB
+        constexpr int kDims = D < kMost ? D : kMost, kPitch = kDims + 4;   // rows start in different banks
         constexpr int kParts = D / kDims;
         __shared__ __align__(16) float so[kWaves][16][kPitch];
         __shared__ float ml[kWaves][NR][16][2];
@@ -522,7 +536,7 @@ __global__ __launch_bounds__(kWaves * 64) void kv4_attention_kernel(AttnParams p
                 }
 #pragma unroll
                 for (int t = 0; t < kDims / 16; ++t) {
-                    if (t % KW != kw) continue;
+                    if ((part * (kDims / 16) + t) % KW != kw) continue;
                     f4_t a = {0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
                     for (int k = 0; k < KW; ++k)
@@ -567,13 +581,22 @@ __global__ __launch_bounds__(kWaves * 64) void kv4_attention_kernel(AttnParams p
     }
 }
 
-// Joins the splits of one (token, head): one workgroup of D / 4 lanes.
+// Joins the splits of one (token, head).  D / 4 lanes take one split's partial
+// in 16-byte loads; the workgroup's 4 to 16 such groups take one split in as many
+// and meet in LDS.  The weights are formed once, one split to a thread.
+constexpr int kJoinThreads = 256;
+constexpr int kMaxSplits = 512;
+
 template <int D, bool F32>
-__global__ __launch_bounds__(64) void kv4_join_kernel(AttnParams p)
+__global__ __launch_bounds__(kJoinThreads) void kv4_join_kernel(AttnParams p)
 {
     typedef typename std::conditional<F32, float, _Float16>::type T;
+    constexpr int LPR = D / 4, GR = kJoinThreads / LPR;
+    __shared__ float wgt[kMaxSplits];
+    __shared__ float red[2][kJoinThreads / 64];
+    __shared__ __align__(16) float sums[GR][D];
     const KvView& v = p.v;
-    const int lane = threadIdx.x;
+    const int tid = threadIdx.x;
     const int h = blockIdx.x % v.q_heads;
     const int i = blockIdx.x / v.q_heads;      // token of the sequence
     const Sequence s = sequence_of(v, blockIdx.y, p.max_q, p.max_kv);
@@ -586,33 +609,61 @@ __global__ __launch_bounds__(64) void kv4_join_kernel(AttnParams p)
     const int r0 = r / p.rows_per_wg * p.rows_per_wg;
     const int r1 = r0 + p.rows_per_wg <= rows ? r0 + p.rows_per_wg - 1 : rows - 1;
     key_range(p, s, r0 / p.gqa, r1 / p.gqa, lo, hi);
-    const int s0 = lo / p.chunk, s1 = hi > lo ? (hi + p.chunk - 1) / p.chunk : s0;
+    const int s0 = lo / p.chunk, n = hi > lo ? (hi + p.chunk - 1) / p.chunk - s0 : 0;
     const int64_t step = (int64_t)v.tokens * v.q_heads;
-    float m = kLow;
-    for (int k = s0; k < s1; ++k) m = fmaxf(m, p.part_ml[2 * (k * step + row)]);
-    float sum = 0.0f;
-    constexpr int PER = D / 64;                // dims of a lane
-    float a[PER];
+
+    const float* ml = p.part_ml + 2 * (s0 * step + row);
+    float M[kMaxSplits / kJoinThreads], L[kMaxSplits / kJoinThreads], m = kLow;
 #pragma unroll
-    for (int j = 0; j < PER; ++j) a[j] = 0.0f;
-    for (int k = s0; k < s1; ++k) {
-        const float* ml = p.part_ml + 2 * (k * step + row);
-        const float w = exp2f(ml[0] - m);
-        sum = __builtin_fmaf(ml[1], w, sum);
-        const float* o = p.part_o + (k * step + row) * D + lane * PER;
-#pragma unroll
-        for (int j = 0; j < PER; ++j) a[j] = __builtin_fmaf(o[j], w, a[j]);
+    for (int k = 0; k < kMaxSplits / kJoinThreads; ++k) {
+        const int at = k * kJoinThreads + tid;
+        M[k] = at < n ? ml[2 * at * step] : kLow;
+        L[k] = at < n ? ml[2 * at * step + 1] : 0.0f;
+        m = fmaxf(m, M[k]);
     }
-    const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
-    T* out = static_cast<T*>(p.out) + row * D + lane * PER;
 #pragma unroll
-    for (int j = 0; j < PER; ++j) out[j] = (T)(a[j] * inv);
-    if (p.lse && lane == 0) p.lse[row] = sum == 0.0f ? -__builtin_inff() : (m + log2f(sum)) * 0.69314718055994531f;
+    for (int off = 32; off > 0; off >>= 1) m = fmaxf(m, __shfl_xor(m, off));
+    if ((tid & 63) == 0) red[0][tid >> 6] = m;
+    __syncthreads();
+#pragma unroll
+    for (int k = 0; k < kJoinThreads / 64; ++k) m = fmaxf(m, red[0][k]);
+    float sum = 0.0f;
+#pragma unroll
+    for (int k = 0; k < kMaxSplits / kJoinThreads; ++k) {
+        const int at = k * kJoinThreads + tid;
+        const float w = exp2f(M[k] - m);
+        if (at < n) wgt[at] = w;
+        sum = __builtin_fmaf(L[k], w, sum);
+    }
+#pragma unroll
+    for (int off = 32; off > 0; off >>= 1) sum += __shfl_xor(sum, off);
+    if ((tid & 63) == 0) red[1][tid >> 6] = sum;
+    __syncthreads();
+    sum = 0.0f;
+#pragma unroll
+    for (int k = 0; k < kJoinThreads / 64; ++k) sum += red[1][k];
+
+    const int g = tid / LPR, d = tid % LPR * 4;
+    const float* o = p.part_o + (s0 * step + row) * D + d;
+    f4_t a = {0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll 4
+    for (int k = g; k < n; k += GR) a += *reinterpret_cast<const f4_t*>(o + k * step * D) * wgt[k];
+    *reinterpret_cast<f4_t*>(&sums[g][d]) = a;
+    __syncthreads();
+    if (tid < D) {
+        float y = 0.0f;
+#pragma unroll
+        for (int k = 0; k < GR; ++k) y += sums[k][tid];
+        const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
+        static_cast<T*>(p.out)[row * D + tid] = (T)(y * inv);
+    }
+    if (p.lse && tid == 0) p.lse[row] = sum == 0.0f ? -__builtin_inff() : (m + log2f(sum)) * 0.69314718055994531f;
 }
 
-// How a call is cut: row tiles per workgroup, waves that share keys, splits.
+// How a call is cut: row tiles per wave, waves that share keys, waves with rows
+// of their own, splits.
 struct Plan {
-    int nr, kw, rows;                 // rows per workgroup
+    int nr, kw, rw, rows;             // rows per workgroup
     int row_tiles, splits, chunk;
 };
 
@@ -620,17 +671,20 @@ Plan plan_of(const AttentionArgs& a)
 {
     Plan c;
     const int64_t rows = a.max_q * (a.v.q_heads / a.v.kv_heads);
-    // few rows: all four waves on the same rows, the keys cut between them
     c.nr = rows <= 16 || a.v.head_dim == 256 ? 1 : 2;
-    c.kw = rows <= 16 * c.nr ? 4 : 1;
-    c.rows = c.nr * 16 * (kWaves / c.kw);
+    // few rows: all waves on the same rows, the keys cut between them
+    const bool few = rows <= 16 * c.nr;
+    const bool brief = few && c.nr == 1 && a.v.head_dim < 256 && a.max_kv <= 1024;
+    c.kw = brief ? 8 : few ? 4 : 1;
+    c.rw = few ? 1 : 4;
+    c.rows = c.nr * 16 * c.rw;
     c.row_tiles = (int)((rows + c.rows - 1) / c.rows);
     const int64_t units = (int64_t)c.row_tiles * a.v.kv_heads * a.v.batch;
-    const int64_t least = 32 * c.kw;           // keys that give every wave a block
+    const int64_t least = 64 * c.kw;           // keys that give every wave two blocks
     const int64_t most = (a.max_kv + least - 1) / least;
-    int64_t splits = (1024 + units - 1) / units;
-    splits = splits < 1 ? 1 : splits > most ? most : splits;
-    if (splits < 1) splits = 1;
+    int64_t splits = brief ? 1 : ((few ? 2048 : 768) + units - 1) / units;
+    splits = splits > most ? most : splits;
+    splits = splits > kMaxSplits ? kMaxSplits : splits < 1 ? 1 : splits;
     c.chunk = (int)(((a.max_kv + splits - 1) / splits + least - 1) / least * least);
     if (c.chunk < least) c.chunk = (int)least;
     c.splits = (int)((a.max_kv + c.chunk - 1) / c.chunk);
@@ -638,15 +692,18 @@ Plan plan_of(const AttentionArgs& a)
     return c;
 }
 
-template <int D, int NG, bool F32, int NR, int KW>
+template <int D, int NG, bool F32, int NR, int KW, int RW>
 hipError_t launch_rows(const AttnParams& p, const Plan& c, hipStream_t s)
 {
     const dim3 grid((unsigned)(p.v.kv_heads * c.splits * c.row_tiles), (unsigned)p.v.batch);
+    // as many as the registers hold without spilling
+    constexpr int PF = D == 256 || (D == 128 && NR == 2 && (F32 || (NG == 4 && KW > 1))) ? 1
+                       : KW == 1 || (D == 128 && (F32 || NR == 2)) ? 2 : 3;
     // few rows: the matrix cores have time for p in two parts
-    kv4_attention_kernel<D, NG, F32, F32 || KW == 4, NR, KW><<<grid, dim3(kWaves * 64), 0, s>>>(p);
+    kv4_attention_kernel<D, NG, F32, F32 || KW >= 4, NR, KW, RW, PF><<<grid, dim3(KW * RW * 64), 0, s>>>(p);
     hipError_t e = hipGetLastError();
     if (e != hipSuccess || c.splits == 1) return e;
-    kv4_join_kernel<D, F32><<<dim3((unsigned)(p.max_q * p.v.q_heads), (unsigned)p.v.batch), dim3(64), 0, s>>>(p);
+    kv4_join_kernel<D, F32><<<dim3((unsigned)(p.max_q * p.v.q_heads), (unsigned)p.v.batch), dim3(kJoinThreads), 0, s>>>(p);
     return hipGetLastError();
 }
 
@@ -655,8 +712,10 @@ hipError_t launch_groups(const AttnParams& p, const Plan& c, hipStream_t s)
 {
     // head_dim 256 keeps one row tile a wave: two do not fit the registers
     constexpr int NR = D == 256 ? 1 : 2;
-    if (c.kw == 1) return launch_rows<D, NG, F32, NR, 1>(p, c, s);
-    return c.nr == 1 ? launch_rows<D, NG, F32, 1, 4>(p, c, s) : launch_rows<D, NG, F32, NR, 4>(p, c, s);
+    if (c.kw == 1) return launch_rows<D, NG, F32, NR, 1, 4>(p, c, s);
+    if constexpr (D < 256)
+        if (c.kw == 8) return launch_rows<D, NG, F32, 1, 8, 1>(p, c, s);
+    return c.nr == 1 ? launch_rows<D, NG, F32, 1, 4, 1>(p, c, s) : launch_rows<D, NG, F32, NR, 4, 1>(p, c, s);
 }
 
 template <int D, int NG> hipError_t launch_type(const AttnParams& p, const Plan& c, int f16, hipStream_t s)

@@ -14,6 +14,13 @@ import math
 import os
 from typing import Optional, Union
 
+try:                       # device memory and streams; the host-only calls work without it
+    import torch
+    # the current stream's handle without building a stream object (2.8 us a call)
+    from torch._C import _cuda_getCurrentRawStream as _raw_stream, _cuda_getDevice as _current_device
+except ImportError:
+    torch = _raw_stream = None
+
 HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(HERE, "lib", "libmnb.so")
 
@@ -162,20 +169,21 @@ def _ptr(x: Ptr):
     return ctypes.c_void_p(x.data_ptr())
 
 
-def _stream(stream) -> ctypes.c_void_p:
+def _stream(stream):
     if stream is None:
-        import torch
-        stream = torch.cuda.current_stream()
+        if _raw_stream is not None and torch.cuda.is_initialized():
+            return _raw_stream(_current_device())
+        import torch as _t
+        stream = _t.cuda.current_stream()
     if isinstance(stream, int):
         return ctypes.c_void_p(stream)
     return ctypes.c_void_p(stream.cuda_stream)
 
 
 def _dtype_code(t) -> int:
-    import torch
-    if t.dtype == torch.float16:
+    if t.dtype is torch.float16:
         return MNB_F16
-    if t.dtype == torch.float32:
+    if t.dtype is torch.float32:
         return MNB_F32
     raise ValueError("fp16 or fp32 tensor expected, got %s" % t.dtype)
 
@@ -316,51 +324,61 @@ def mnb_gemm_accuracy4_codes(w: mnb_weight_desc, repacked: Ptr, codes: Ptr, scal
 
 
 # ---- between the products ---------------------------------------------------
+# These calls are short on the device: the checks of a tensor are single
+# comparisons, and only a failing one builds a message.
+
+def _addr(x, name: str) -> Optional[int]:
+    """Address of a dense device tensor (or None, or an address)."""
+    if x is None or type(x) is int:
+        return x
+    if not x.is_cuda or not x.is_contiguous():
+        raise ValueError("%s: contiguous device tensor expected" % name)
+    return x.data_ptr()
+
 
 def _rows(x, name: str):
     """Address and row stride of a tensor whose rows (all dims but the first) are dense."""
     if not x.is_cuda:
         raise ValueError("%s: device tensor expected" % name)
+    shape = x.shape
     if x.is_contiguous():
-        return x.data_ptr(), x.stride(0) if x.dim() > 1 and x.shape[0] > 1 else math.prod(x.shape[1:])
-    dense = 1
-    for n, s in zip(reversed(x.shape[1:]), reversed(x.stride()[1:])):
-        if n != 1 and s != dense:
+        return x.data_ptr(), math.prod(shape[1:])
+    stride, dense = x.stride(), 1
+    for i in range(len(shape) - 1, 0, -1):
+        if shape[i] != 1 and stride[i] != dense:
             raise ValueError("%s: rows must be dense" % name)
-        dense *= n
-    return x.data_ptr(), x.stride(0) if x.shape[0] > 1 else dense
+        dense *= shape[i]
+    return x.data_ptr(), stride[0] if shape[0] > 1 else dense
 
 
 def _expect(x, name: str, dtype, shape) -> None:
-    if x.dtype != dtype:
+    if x.dtype is not dtype:
         raise ValueError("%s: %s expected, got %s" % (name, dtype, x.dtype))
-    if tuple(x.shape) != tuple(shape):
+    if x.shape != shape:
         raise ValueError("%s: shape %s expected, got %s" % (name, tuple(shape), tuple(x.shape)))
 
 
 def mnb_rms_norm(x, weight, out, eps: float, residual=None, residual_out=None, scales=None, stream=None) -> None:
     """x, residual [m, k] (rows may be strided), out and residual_out [m, k].  Without `scales` out receives the
     values; with it (fp32 [m]) the 8-bit codes, as int8 or as fp16 integers by out's type."""
-    import torch
-    m, k = x.shape
-    dt = _dtype_code(x)
-    _expect(weight, "weight", x.dtype, (k,))
-    if scales is None:
-        kind = MNB_NORM_VALUES
-        _expect(out, "out", x.dtype, (m, k))
-    else:
-        kind = MNB_NORM_CODES_I8 if out.dtype == torch.int8 else MNB_NORM_CODES_F16
-        _expect(out, "out", torch.int8 if kind == MNB_NORM_CODES_I8 else torch.float16, (m, k))
+    shape, dtype = x.shape, x.dtype
+    m, k = shape
+    kind, want = MNB_NORM_VALUES, dtype
+    if scales is not None:
+        kind, want = (MNB_NORM_CODES_I8, torch.int8) if out.dtype is torch.int8 else (MNB_NORM_CODES_F16, torch.float16)
         _expect(scales, "scales", torch.float32, (m,))
+    _expect(out, "out", want, shape)
+    _expect(weight, "weight", dtype, (k,))
     xp, xs = _rows(x, "x")
     rp, rs = None, 0
     if residual is not None:
-        _expect(residual, "residual", x.dtype, (m, k))
+        _expect(residual, "residual", dtype, shape)
         rp, rs = _rows(residual, "residual")
     if residual_out is not None:
-        _expect(residual_out, "residual_out", x.dtype, (m, k))
-    _check(lib.mnb_rms_norm(xp, xs, rp, rs, _ptr(weight), m, k, dt, eps, kind, _ptr(out), _ptr(scales),
-                            _ptr(residual_out), _stream(stream)))
+        _expect(residual_out, "residual_out", dtype, shape)
+    _check(lib.mnb_rms_norm(xp, xs, rp, rs, _addr(weight, "weight"), m, k, _dtype_code(x), eps, kind,
+                            _addr(out, "out"), _addr(scales, "scales"), _addr(residual_out, "residual_out"),
+                            _stream(stream)))
 
 
 def kv4_desc(q_heads: int, kv_heads: int, head_dim: int, group_size: int, page_size: int,
@@ -376,57 +394,58 @@ def mnb_kv4_cache_bytes(c: mnb_kv4_desc) -> int:
 
 
 def _sequences(c, cache, table, kv_len, q_start):
-    """Addresses of the sequence arrays, their table stride and batch, after a look at their types and sizes."""
-    import torch
+    """Descriptor, cache, table, table stride, lengths, offsets and batch of a call, after a look at their types and sizes."""
     i32 = torch.int32
-    if table.dtype != i32 or kv_len.dtype != i32 or (q_start is not None and q_start.dtype != i32):
+    if table.dtype is not i32 or kv_len.dtype is not i32 or (q_start is not None and q_start.dtype is not i32):
         raise ValueError("block_table, kv_len and q_start: int32 expected")
     batch = kv_len.shape[0]
     if table.shape[0] != batch or (q_start is not None and q_start.shape[0] != batch + 1):
         raise ValueError("block_table, kv_len and q_start: one row, length and offset (and one more) per sequence")
-    if cache.numel() * cache.element_size() < lib.mnb_kv4_cache_bytes(ctypes.byref(c)):
+    d = ctypes.byref(c)
+    size = lib.mnb_kv4_cache_bytes(d)
+    if cache.numel() * cache.element_size() < size or size == 0:
         raise ValueError("cache: %d bytes expected" % mnb_kv4_cache_bytes(c))
     tp, ts = _rows(table, "block_table")
-    return _ptr(cache), tp, ts, _ptr(kv_len), _ptr(q_start), batch
+    return d, _addr(cache, "cache"), tp, ts, _addr(kv_len, "kv_len"), _addr(q_start, "q_start"), batch
 
 
 def mnb_kv4_append(c: mnb_kv4_desc, cache, k, v, block_table, kv_len, q_start=None, cos=None, sin=None,
                    rotary_dim: int = 0, interleaved: bool = False, q=None, q_out=None, stream=None) -> None:
     """k, v [tokens, kv_heads, head_dim] and q [tokens, q_heads, head_dim], tokens may be strided."""
-    import torch
-    cp, tp, ts, lp, sp, batch = _sequences(c, cache, block_table, kv_len, q_start)
-    n = k.shape[0]
-    _expect(k, "k", k.dtype, (n, c.kv_heads, c.head_dim))
-    _expect(v, "v", k.dtype, (n, c.kv_heads, c.head_dim))
+    seq = _sequences(c, cache, block_table, kv_len, q_start)
+    dtype, n, D = k.dtype, k.shape[0], c.head_dim
+    shape = (n, c.kv_heads, D)
+    _expect(k, "k", dtype, shape)
+    _expect(v, "v", dtype, shape)
     kp, ks = _rows(k, "k")
     vp, vs = _rows(v, "v")
-    qp, qs = None, 0
+    qp, qs, rows = None, 0, 0
     if q is not None:
-        _expect(q, "q", k.dtype, (n, c.q_heads, c.head_dim))
+        shape = (n, c.q_heads, D)
+        _expect(q, "q", dtype, shape)
         qp, qs = _rows(q, "q")
-    if q_out is not None:
-        _expect(q_out, "q_out", k.dtype, (n, c.q_heads, c.head_dim))
-    rows = 0
+        if q_out is not None:
+            _expect(q_out, "q_out", dtype, shape)
     if cos is not None:
         rows = cos.shape[0]
         _expect(cos, "cos", torch.float32, (rows, rotary_dim // 2))
-    if sin is not None:
-        _expect(sin, "sin", torch.float32, (rows, rotary_dim // 2))
-    _check(lib.mnb_kv4_append(ctypes.byref(c), cp, tp, ts, lp, sp, batch, n, _dtype_code(k), qp, qs, kp, ks, vp, vs,
-                              _ptr(cos), _ptr(sin), rows, rotary_dim, int(interleaved), _ptr(q_out), _stream(stream)))
+        if sin is not None:
+            _expect(sin, "sin", torch.float32, (rows, rotary_dim // 2))
+    _check(lib.mnb_kv4_append(*seq, n, _dtype_code(k), qp, qs, kp, ks, vp, vs, _addr(cos, "cos"), _addr(sin, "sin"),
+                              rows, rotary_dim, 1 if interleaved else 0, _addr(q_out, "q_out"), _stream(stream)))
 
 
 def mnb_kv4_read(c: mnb_kv4_desc, cache, block_table, kv_len, q_start, k_out=None, v_out=None, stream=None) -> None:
     """k_out, v_out [tokens, kv_heads, head_dim]; either may be None."""
-    cp, tp, ts, lp, sp, batch = _sequences(c, cache, block_table, kv_len, q_start)
+    seq = _sequences(c, cache, block_table, kv_len, q_start)
     some = k_out if k_out is not None else v_out
     if some is None:
         return
-    n = some.shape[0]
-    for x, name in ((k_out, "k_out"), (v_out, "v_out")):
-        if x is not None:
-            _expect(x, name, some.dtype, (n, c.kv_heads, c.head_dim))
-    _check(lib.mnb_kv4_read(ctypes.byref(c), cp, tp, ts, lp, sp, batch, n, _dtype_code(some), _ptr(k_out), _ptr(v_out),
+    shape = (some.shape[0], c.kv_heads, c.head_dim)
+    _expect(some, "k_out" if k_out is not None else "v_out", some.dtype, shape)
+    if v_out is not None and v_out is not some:
+        _expect(v_out, "v_out", some.dtype, shape)
+    _check(lib.mnb_kv4_read(*seq, shape[0], _dtype_code(some), _addr(k_out, "k_out"), _addr(v_out, "v_out"),
                             _stream(stream)))
 
 
@@ -438,19 +457,19 @@ def mnb_attention_kv4(c: mnb_kv4_desc, cache, q, block_table, kv_len, q_start, m
                       scale: float, causal: bool = True, window: int = 0, lse=None, workspace: Ptr = None,
                       workspace_bytes: Optional[int] = None, stream=None) -> None:
     """q [tokens, q_heads, head_dim] (tokens may be strided), out the same, lse fp32 [tokens, q_heads]."""
-    import torch
-    cp, tp, ts, lp, sp, batch = _sequences(c, cache, block_table, kv_len, q_start)
-    n = q.shape[0]
-    _expect(q, "q", q.dtype, (n, c.q_heads, c.head_dim))
-    _expect(out, "out", q.dtype, (n, c.q_heads, c.head_dim))
+    seq = _sequences(c, cache, block_table, kv_len, q_start)
+    dtype, n = q.dtype, q.shape[0]
+    shape = (n, c.q_heads, c.head_dim)
+    _expect(q, "q", dtype, shape)
+    _expect(out, "out", dtype, shape)
     if lse is not None:
-        _expect(lse, "lse", torch.float32, (n, c.q_heads))
+        _expect(lse, "lse", torch.float32, shape[:2])
     if workspace_bytes is None:
-        workspace_bytes = 0 if workspace is None or isinstance(workspace, int) else \
+        workspace_bytes = 0 if workspace is None or type(workspace) is int else \
             workspace.numel() * workspace.element_size()
     qp, qs = _rows(q, "q")
-    _check(lib.mnb_attention_kv4(ctypes.byref(c), cp, tp, ts, lp, sp, batch, n, max_q, max_kv, _dtype_code(q), qp, qs,
-                                 scale, int(causal), window, _ptr(out), _ptr(lse), _ptr(workspace), workspace_bytes,
+    _check(lib.mnb_attention_kv4(*seq, n, max_q, max_kv, _dtype_code(q), qp, qs, scale, 1 if causal else 0, window,
+                                 _addr(out, "out"), _addr(lse, "lse"), _addr(workspace, "workspace"), workspace_bytes,
                                  _stream(stream)))
 
 

@@ -269,7 +269,7 @@ def test_a_captured_graph_and_another_stream(mnb):
     y = t.empty((2, 1024), dtype=t.float16, device="cuda")
     q_out, out = (t.empty((2, 4, 128), dtype=t.float16, device="cuda") for _ in range(2))
     ko = t.empty((2, 2, 128), dtype=t.float16, device="cuda")
-    n = mnb.mnb_attention_kv4_workspace_bytes(d, 2, 2, 1, 1000)
+    n = mnb.mnb_attention_kv4_workspace_bytes(d, 2, 2, 1, 20000)      # a bound that cuts the keys into splits
     assert n > 0
     ws = t.empty(n, dtype=t.uint8, device="cuda")
     qkv = y.view(2, 8, 128)
@@ -280,7 +280,7 @@ def test_a_captured_graph_and_another_stream(mnb):
         mnb.mnb_kv4_append(d, cache, qkv[:, 4:6], qkv[:, 6:], *seq, cos=cos, sin=sin, rotary_dim=128, q=qkv[:, :4],
                            q_out=q_out, stream=stream)
         mnb.mnb_kv4_read(d, cache, *seq, k_out=ko, stream=stream)
-        mnb.mnb_attention_kv4(d, cache, q_out, *seq, 1, 1000, out, 0.09, workspace=ws, stream=stream)
+        mnb.mnb_attention_kv4(d, cache, q_out, *seq, 1, 20000, out, 0.09, workspace=ws, stream=stream)
 
     outs = (y, q_out, ko, out, cache)
     issue(t.cuda.current_stream())
