@@ -149,15 +149,21 @@ template <int D, int NG> struct RawBlock {
     uint32_t meta[NG];
 };
 
+// Requests a block, or nothing where `there` is 0: buffer loads past their
+// range fetch no memory, so the instructions are issued in any case and the
+// number of loads in flight is known when the code is compiled.
 template <int D, int NG>
-__device__ __forceinline__ void load_block(const unsigned char* blk, int lane, RawBlock<D, NG>& r)
+__device__ __forceinline__ void load_block(unsigned char* blk, bool there, int lane, RawBlock<D, NG>& r)
 {
+    const __amdgpu_buffer_rsrc_t rs =
+        __builtin_amdgcn_make_buffer_rsrc(blk, 0, there ? 32 * D + 256 * NG : 0, 0x00020000);
+    const int v16 = lane * 16, v4 = lane * 4;
 #pragma unroll
-    for (int i = 0; i < D / 64; ++i) r.k[i] = reinterpret_cast<const u4_t*>(blk + i * 1024)[lane];
+    for (int i = 0; i < D / 64; ++i) r.k[i] = __builtin_amdgcn_raw_buffer_load_b128(rs, v16, i * 1024, 0);
 #pragma unroll
-    for (int i = 0; i < NG; ++i) r.meta[i] = reinterpret_cast<const uint32_t*>(blk + 32 * D)[i * 64 + lane];
+    for (int i = 0; i < NG; ++i) r.meta[i] = __builtin_amdgcn_raw_buffer_load_b32(rs, v4, 32 * D + i * 256, 0);
 #pragma unroll
-    for (int i = 0; i < D / 64; ++i) r.v[i] = reinterpret_cast<const u4_t*>(blk + 16 * D + i * 1024)[lane];
+    for (int i = 0; i < D / 64; ++i) r.v[i] = __builtin_amdgcn_raw_buffer_load_b128(rs, v16, 16 * D + i * 1024, 0);
 }
 
 // Words of keys 4q .. 4q+3 (NG each) from the wave's slot.
@@ -177,8 +183,9 @@ __device__ __forceinline__ float scale_of(uint32_t m) { return (float)__builtin_
 
 // KW waves share the keys of a row set, RW row sets make a workgroup; PF blocks
 // of a wave are in registers, all but the one in work still on their way.
-template <int D, int NG, bool F32, bool SPLIT, int NR, int KW, int RW, int PF>
-__global__ __launch_bounds__(KW * RW * 64) void kv4_attention_kernel(AttnParams p)
+// WPE: waves per SIMD that the registers are held to.
+template <int D, int NG, bool F32, bool SPLIT, int NR, int KW, int RW, int PF, int WPE>
+__global__ __launch_bounds__(KW * RW * 64, WPE) void kv4_attention_kernel(AttnParams p)
 {
     constexpr int kWaves = KW * RW;
     typedef typename std::conditional<F32, float, _Float16>::type T;
@@ -198,6 +205,24 @@ __global__ __launch_bounds__(KW * RW * 64) void kv4_attention_kernel(AttnParams 
     const int tile = p.row_tiles - 1 - (int)(blockIdx.x / v.kv_heads / p.splits);   // longest key ranges first
     const int b = blockIdx.y;
 
+    // The pages of the wave's next 64 blocks from k0 on, a lane each; entries
+    // past the table or outside the cache are replaced, so a load ahead of the
+    // sequence's end stays inside both.  Without a window the first block does not
+    // depend on the length: the table is requested beside it.
+    const int32_t* table = v.table + (int64_t)b * v.table_stride;
+    auto pages_from = [&](int k0) {
+        int64_t at = (int64_t)(k0 + lane * KW) >> (v.page_shift - 5);
+        at = at < v.table_stride ? at : v.table_stride - 1;
+        return table[at];
+    };
+    auto page_in = [&](int pages, int i) {     // i uniform
+        const int page = __builtin_amdgcn_readlane(pages, i);
+        return page < 0 || page >= v.num_pages ? 0 : page;
+    };
+    const int c0 = split * p.chunk, c1 = c0 + p.chunk;
+    int pages = 0;
+    if (p.window == 0) pages = pages_from((c0 >> 5) + kw);
+
     const Sequence s = sequence_of(v, b, p.max_q, p.max_kv);
     const int rows = s.count * p.gqa;
     const int row0 = tile * kRows;
@@ -206,11 +231,11 @@ __global__ __launch_bounds__(KW * RW * 64) void kv4_attention_kernel(AttnParams 
     int lo, hi;
     key_range(p, s, row0 / p.gqa, last_row / p.gqa, lo, hi);
     // this split's part, in blocks
-    const int c0 = split * p.chunk, c1 = c0 + p.chunk;
     const int from = lo > c0 ? lo : c0, to = hi < c1 ? hi : c1;
     const bool any = from < to;
     if (p.splits > 1 && !any) return;          // the join reads only splits with keys
     const int blk0 = from >> 5, blk1 = any ? (to + 31) >> 5 : blk0;
+    if (p.window > 0) pages = pages_from(blk0 + kw);
 
     // the rows of this wave: queries as the B operand, row = column of the lane
     h8_t qf[NR][NQ][NJ];
@@ -271,14 +296,6 @@ __global__ __launch_bounds__(KW * RW * 64) void kv4_attention_kernel(AttnParams 
 
     const int nblk = 1 << (v.page_shift - 5);
     const int64_t block_bytes = kv_block_bytes(D, NG);
-    const int32_t* table = v.table + (int64_t)b * v.table_stride;
-    const int last_page = blk1 > blk0 ? (blk1 - 1) >> (v.page_shift - 5) : 0;
-    auto page_of = [&](int blk) {              // clamped: loads ahead stay inside the table and the cache
-        int at = blk >> (v.page_shift - 5);
-        at = at < last_page ? at : last_page;
-        const int page = uniform(table[at]);
-        return page < 0 || page >= v.num_pages ? 0 : page;
-    };
     auto block_at = [&](int page, int blk) {
         return v.cache + (((int64_t)page * v.kv_heads + h) * nblk + (blk & (nblk - 1))) * block_bytes;
     };
@@ -467,29 +484,31 @@ __global__ __launch_bounds__(KW * RW * 64) void kv4_attention_kernel(AttnParams 
     int blk = blk0 + kw;
     if (blk < blk1) {
         RawBlock<D, NG> set[PF];
-        // the block after the last is the last again: requested, not used
-        auto within = [&](int k) { return k < blk1 ? k : blk; };
 #pragma unroll
-        for (int i = 0; i < PF; ++i) {
-            const int k = within(blk + i * KW);
-            load_block<D, NG>(block_at(page_of(k), k), lane, set[i]);
-        }
-        int page = page_of(blk + PF * KW);     // of the block that the next load fetches
-        while (true) {
-            bool more = true;
+        for (int i = 0; i < PF; ++i)
+            load_block<D, NG>(block_at(page_in(pages, i), blk + i * KW), blk + i * KW < blk1, lane, set[i]);
+        // whole turns of the sets, then what is left: no branch between a load and
+        // its use but the refill's, whose load is waited for where it is made
+        const int steps = (blk1 - blk + KW - 1) / KW;
+        int at = PF;                           // lane of `pages` with the next load's page
+        for (int turn = 0; turn < steps / PF; ++turn) {
+            if (at > 64 - PF) {
+                pages = pages_from(blk + PF * KW);
+                at = 0;
+                asm volatile("" : "+v"(pages));
+            }
 #pragma unroll
             for (int i = 0; i < PF; ++i) {
-                if (!more) break;
-                const int next = blk + PF * KW;
-                const int after = page_of(next + KW);
                 compute(set[i], blk);
-                if (next < blk1) load_block<D, NG>(block_at(page, next), lane, set[i]);
-                page = after;
+                const int next = blk + PF * KW;
+                load_block<D, NG>(block_at(page_in(pages, at), next), next < blk1, lane, set[i]);
+                ++at;
                 blk += KW;
-                more = blk < blk1;
             }
-            if (!more) break;
         }
+#pragma unroll
+        for (int i = 0; i < PF - 1; ++i)
+            if (i < steps % PF) compute(set[i], blk + i * KW);
     }
 #pragma unroll
     for (int n = 0; n < NR; ++n) {
@@ -682,7 +701,7 @@ Plan plan_of(const AttentionArgs& a)
     const int64_t units = (int64_t)c.row_tiles * a.v.kv_heads * a.v.batch;
     const int64_t least = 64 * c.kw;           // keys that give every wave two blocks
     const int64_t most = (a.max_kv + least - 1) / least;
-    int64_t splits = brief ? 1 : ((few ? 2048 : 768) + units - 1) / units;
+    int64_t splits = brief ? 1 : ((few ? 2048 : 256) + units - 1) / units;
     splits = splits > most ? most : splits;
     splits = splits > kMaxSplits ? kMaxSplits : splits < 1 ? 1 : splits;
     c.chunk = (int)(((a.max_kv + splits - 1) / splits + least - 1) / least * least);
@@ -697,10 +716,11 @@ hipError_t launch_rows(const AttnParams& p, const Plan& c, hipStream_t s)
 {
     const dim3 grid((unsigned)(p.v.kv_heads * c.splits * c.row_tiles), (unsigned)p.v.batch);
     // as many as the registers hold without spilling
-    constexpr int PF = D == 256 || (D == 128 && NR == 2 && (F32 || (NG == 4 && KW > 1))) ? 1
+    constexpr int PF = KW == 8 ? 4 - 2 * (D == 128 && F32) : D == 256 || (D == 128 && NR == 2 && (F32 || (NG == 4 && KW > 1))) ? 1
                        : KW == 1 || (D == 128 && (F32 || NR == 2)) ? 2 : 3;
+    constexpr int WPE = NR == 1 && KW == 4 && D == 128 && NG == 1 && !F32 ? 3 : 1;
     // few rows: the matrix cores have time for p in two parts
-    kv4_attention_kernel<D, NG, F32, F32 || KW >= 4, NR, KW, RW, PF><<<grid, dim3(KW * RW * 64), 0, s>>>(p);
+    kv4_attention_kernel<D, NG, F32, F32 || KW >= 4, NR, KW, RW, PF, WPE><<<grid, dim3(KW * RW * 64), 0, s>>>(p);
     hipError_t e = hipGetLastError();
     if (e != hipSuccess || c.splits == 1) return e;
     kv4_join_kernel<D, F32><<<dim3((unsigned)(p.max_q * p.v.q_heads), (unsigned)p.v.batch), dim3(kJoinThreads), 0, s>>>(p);
