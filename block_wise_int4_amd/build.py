@@ -17,7 +17,7 @@ LIB = os.path.join(LIB_DIR, "libmnb.so")
 
 SOURCES = ["mnb_api.cpp", "repack.hip", "act_order.hip", "gemv.hip", "gemm_small.hip", "gemm_mfma.hip",
            "noalloc.hip", "f32_split.hip", "gidx.hip",
-           "acc4.hip", "rms_norm.hip", "kv4_append.hip", "kv4_attention.hip", "mnb_decoder_api.cpp"]
+           "acc4.hip", "rms_norm.hip", "kv4_append.hip", "kv4_attention.hip", "kv4_prompt.hip", "mnb_decoder_api.cpp"]
 
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
 ARCH = "gfx950"
@@ -39,6 +39,7 @@ DEVICE_FLAGS = [
 EXTRA_FLAGS = {"gemm_mfma.hip": ["-mllvm", "-amdgpu-mfma-vgpr-form"],
                # the attention rescales its accumulators and reads its logits the same way
                "kv4_attention.hip": ["-mllvm", "-amdgpu-mfma-vgpr-form"],
+               "kv4_prompt.hip": ["-mllvm", "-amdgpu-mfma-vgpr-form"],
                # the first 16 argument dwords of the fp16 GEMV and the small-M kernel
                # arrive in SGPRs (measured faster; the int8-activation GEMV measured
                # slower with it)

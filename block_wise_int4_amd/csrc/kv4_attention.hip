@@ -1,4 +1,5 @@
-// kv4_attention.hip -- attention over the paged 4-bit cache.
+// kv4_attention.hip -- attention over the paged 4-bit cache: the kernel for few
+// query rows per key head, the join of splits, and the choice between kernels.
 //
 //   x_tk = scale * sum_d q_td (c_kd - z_k) s_k,   p_tk = exp(x_tk - max),
 //   o_t  = sum_k p_tk (c'_kd - z'_k) s'_k / sum_k p_tk,
@@ -7,139 +8,39 @@
 // A code minus its zero point is an integer of at most 15 in magnitude: exact
 // in fp16.  So the products run on the fp16 matrix cores on exact operands: q as
 // it is (fp32 queries as a (hi, lo) pair of fp16), scales applied in fp32 to the
-// logits, and the value's scale multiplied into p before p is rounded to
-// fp16.  That rounding and the output's are the only ones to 16 bits; with SPLIT,
-// p too is a (hi, lo) pair.
+// logits, and the value's scale multiplied into p before p is rounded to fp16.
+// That rounding (2^-12 on average over many keys) and the output's are the only
+// ones to 16 bits; in fp32 calls p too is a (hi, lo) pair.
 //
 // Layout.  A wave computes S^T = K Q^T on v_mfma_f32_16x16x32_f16: 16 keys by
-// 16 query rows, the key codes of a lane being one word per 32 dims.  The
-// result puts keys 4q..4q+3 of a row in the registers of lane (row, q), which is
+// 16 columns, the key codes of a lane being one word per 32 dims.  The result
+// puts keys 4q..4q+3 of a column in the registers of lane (column, q), which is
 // the operand distribution that O^T = V^T P^T wants for P if the 32 keys of a block
 // are counted (q, i, tile).  The cache stores the value codes in that count, so p
 // goes from the softmax to the product without leaving its lane.
 //
-// Rows are (token, head) pairs that share a key head, token-major, so grouped
-// heads fill the 16 columns.  The running reference M is common to a row's
-// four lanes and is raised only when some lane's logit passes it by 2^14 (a
-// branch of the whole wave), so the usual block needs no exchange between
-// lanes.  M also bounds the value scale's exponent: p s' stays below 2^14.
+// Rows are (token, head) pairs that share a key head.  With at most 4 (8) rows
+// the 16 columns hold them 4 (2) times over, and each copy takes a quarter (half)
+// of the keys through the softmax: its other entries of P are zeros, and
+// the copies' sums are added at the end.  The vector work of the softmax, which
+// bounds the kernel at full occupancy, then falls with the rows.  (The value's zero
+// points are taken off in the unpack: as one sum p s' z' per row, subtracted at
+// the end, they would cost 14 instructions a block less, but the difference of
+// the two sums loses what a row of equal codes and zero points leaves.)
 //
-// Work split: a workgroup is four waves, KW of them sharing the keys of one
-// set of rows (joined through LDS), and `splits` workgroups share a
-// sequence's keys (joined by a second kernel over fp32 partials), so that a
-// few long sequences fill the chip.
-#include <type_traits>
-
-#include "mnb_device.hpp"
-#include "mnb_kv4.hpp"
+// The running reference M of a column is common to its four lanes and is raised
+// only when some lane's logit passes it by 2^14 (a branch of the whole wave),
+// so the usual block needs no exchange between lanes.
+//
+// Work split: the waves of a workgroup share the keys of one set of rows (joined
+// through LDS), and `splits` workgroups share a sequence's keys (joined by a second
+// kernel over fp32 partials), so that a few long sequences fill the chip.
+#include "kv4_attention.hpp"
 
 namespace mnb {
+namespace kv4 {
 
 namespace {
-
-constexpr float kLow = -1e30f;        // "no key yet": finite, so differences stay numbers
-
-struct AttnParams {
-    KvView v;
-    const void* q;
-    int64_t q_stride;
-    void* out;
-    float* lse;
-    float* part_o;                    // [splits][tokens * q_heads][D] unnormalised
-    float* part_ml;                   // [splits][tokens * q_heads][2]: M, sum
-    float scale_log2;
-    int causal;
-    int window;                       // 0: none
-    int max_q, max_kv;
-    int gqa;                          // query heads per key head
-    int splits, chunk;                // keys per split, a multiple of 32
-    int row_tiles, rows_per_wg;
-};
-
-__device__ __forceinline__ f4_t mfma(const h8_t& a, const h8_t& b, const f4_t& c)
-{
-    return __builtin_amdgcn_mfma_f32_16x16x32_f16(a, b, c, 0, 0, 0);
-}
-
-__device__ __forceinline__ h8_t join(const h2_t q[4])
-{
-    return h8_t{q[0][0], q[0][1], q[1][0], q[1][1], q[2][0], q[2][1], q[3][0], q[3][1]};
-}
-
-// e with s < 2^e of an fp16 scale (low half of a word): -14 for zero and
-// subnormals, 17 for infinity and NaN
-__device__ __forceinline__ float top_exponent(uint32_t word) { return (float)((int)((word >> 10) & 31u) - 14); }
-
-typedef uint16_t us2_t __attribute__((ext_vector_type(2)));
-// the larger of both halves each: of two words, the larger scale in the low half
-__device__ __forceinline__ uint32_t max_halves(uint32_t a, uint32_t b)
-{
-    return __builtin_bit_cast(uint32_t, __builtin_elementwise_max(__builtin_bit_cast(us2_t, a), __builtin_bit_cast(us2_t, b)));
-}
-
-// Length and new tokens of a sequence, within the bounds of the call.
-struct Sequence {
-    int len, first, count;            // keys; first row and number of new tokens
-};
-__device__ __forceinline__ Sequence sequence_of(const KvView& v, int b, int max_q, int max_kv)
-{
-    Sequence s;
-    int64_t room = v.table_stride << v.page_shift;
-    int len = v.kv_len[b];
-    len = len < 0 ? 0 : len > max_kv ? max_kv : len;
-    s.len = (int64_t)len > room ? (int)room : len;
-    int first = b, end = b + 1;
-    if (v.q_start) {
-        first = v.q_start[b];
-        end = v.q_start[b + 1];
-    }
-    first = first < 0 ? 0 : first;
-    end = end > v.tokens ? v.tokens : end;
-    int n = end - first;
-    s.first = first;
-    s.count = n < 0 ? 0 : n > max_q ? max_q : n;
-    return s;
-}
-
-// The keys rows of tokens i0..i1 of a sequence can see: [lo, hi).
-__device__ __forceinline__ void key_range(const AttnParams& p, const Sequence& s, int i0, int i1, int& lo, int& hi)
-{
-    lo = 0;
-    hi = s.len;
-    if (p.causal) {
-        const int end = s.len - s.count + i1 + 1;
-        hi = end < hi ? end : hi;
-        if (p.window > 0) {
-            const int from = s.len - s.count + i0 - p.window + 1;
-            lo = from > 0 ? from : 0;
-        }
-    }
-    hi = hi < lo ? lo : hi;
-}
-
-template <typename T> struct Frag8;
-template <> struct Frag8<_Float16> {
-    static __device__ __forceinline__ void load(const _Float16* p, float* f)
-    {
-        typedef uint32_t raw __attribute__((ext_vector_type(4), aligned(2), may_alias));
-        const u4_t r = *reinterpret_cast<const raw*>(p);
-        const h8_t h = __builtin_bit_cast(h8_t, r);
-#pragma unroll
-        for (int i = 0; i < 8; ++i) f[i] = (float)h[i];
-    }
-};
-template <> struct Frag8<float> {
-    static __device__ __forceinline__ void load(const float* p, float* f)
-    {
-        typedef float raw __attribute__((ext_vector_type(4), aligned(4)));
-        const raw a = *reinterpret_cast<const raw*>(p), b = *reinterpret_cast<const raw*>(p + 4);
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            f[i] = a[i];
-            f[4 + i] = b[i];
-        }
-    }
-};
 
 // One block of 32 keys as it arrives from memory: codes in the products' own
 // distribution, and the block's 64 NG scale and zero-point words, NG to a
@@ -166,62 +67,64 @@ __device__ __forceinline__ void load_block(unsigned char* blk, bool there, int l
     for (int i = 0; i < D / 64; ++i) r.v[i] = __builtin_amdgcn_raw_buffer_load_b128(rs, v16, 16 * D + i * 1024, 0);
 }
 
-// Words of keys 4q .. 4q+3 (NG each) from the wave's slot.
-template <int NG> __device__ __forceinline__ void four_keys(const uint32_t* slot, uint32_t* w)
+// N consecutive words from the wave's slot.
+template <int N> __device__ __forceinline__ void words(const uint32_t* slot, uint32_t* w)
 {
+    if constexpr (N % 4 == 0) {
 #pragma unroll
-    for (int i = 0; i < NG; ++i) {
-        const u4_t r = reinterpret_cast<const u4_t*>(slot)[i];
-        w[4 * i] = r.x;
-        w[4 * i + 1] = r.y;
-        w[4 * i + 2] = r.z;
-        w[4 * i + 3] = r.w;
+        for (int i = 0; i < N / 4; ++i) {
+            const u4_t r = reinterpret_cast<const u4_t*>(slot)[i];
+            w[4 * i] = r.x;
+            w[4 * i + 1] = r.y;
+            w[4 * i + 2] = r.z;
+            w[4 * i + 3] = r.w;
+        }
+    } else if constexpr (N % 2 == 0) {
+#pragma unroll
+        for (int i = 0; i < N / 2; ++i) {
+            const uint64_t r = reinterpret_cast<const uint64_t*>(slot)[i];
+            w[2 * i] = (uint32_t)r;
+            w[2 * i + 1] = (uint32_t)(r >> 32);
+        }
+    } else {
+#pragma unroll
+        for (int i = 0; i < N; ++i) w[i] = slot[i];
     }
 }
 
-__device__ __forceinline__ float scale_of(uint32_t m) { return (float)__builtin_bit_cast(_Float16, (uint16_t)m); }
-
-// KW waves share the keys of a row set, RW row sets make a workgroup; PF blocks
-// of a wave are in registers, all but the one in work still on their way.
-// WPE: waves per SIMD that the registers are held to.
-template <int D, int NG, bool F32, bool SPLIT, int NR, int KW, int RW, int PF, int WPE>
-__global__ __launch_bounds__(KW * RW * 64, WPE) void kv4_attention_kernel(AttnParams p)
+// GRP column groups (4: up to 4 rows, 2: up to 8, 1: up to 16 NR).  KW waves
+// share the keys; PF blocks of a wave are in registers, all but the one in work
+// still on their way.  WPE: waves per SIMD that the registers are held to.
+template <int D, int NG, bool F32, int GRP, int NR, int KW, int PF, int WPE>
+__global__ __launch_bounds__(KW * 64, WPE) void kv4_attention_kernel(AttnParams p)
 {
-    constexpr int kWaves = KW * RW;
+    static_assert(GRP == 1 || NR == 1, "copies of the rows need one column tile");
     typedef typename std::conditional<F32, float, _Float16>::type T;
+    constexpr bool SPLIT = F32;                // p in two parts
     constexpr int NJ = D / 32;                 // 32-dim steps of the first product
     constexpr int NT = D / 16;                 // 16-dim tiles of the second
     constexpr int NQ = F32 ? 2 : 1;            // fp16 parts of q
     constexpr int JG = NJ / NG;                // steps per group
-    constexpr int kRows = RW * NR * 16;
+    constexpr int I = 4 / GRP;                 // keys per tile that a lane takes through the softmax
+    constexpr int R = 16 / GRP;                // rows of a column tile
+    constexpr int kRows = NR * R;
 
     const KvView& v = p.v;
     const int lane = threadIdx.x & 63;
-    const int wave = uniform(threadIdx.x >> 6);
-    const int kw = wave % KW, rw = wave / KW;
+    const int kw = uniform(threadIdx.x >> 6);
     const int col = lane & 15, quarter = lane >> 4;
+    const int copy = col / R;                  // which quarter (half) of the keys
     const int h = blockIdx.x % v.kv_heads;
     const int split = (blockIdx.x / v.kv_heads) % p.splits;
-    const int tile = p.row_tiles - 1 - (int)(blockIdx.x / v.kv_heads / p.splits);   // longest key ranges first
+    const int tile = blockIdx.x / v.kv_heads / p.splits;
     const int b = blockIdx.y;
 
-    // The pages of the wave's next 64 blocks from k0 on, a lane each; entries
-    // past the table or outside the cache are replaced, so a load ahead of the
-    // sequence's end stays inside both.  Without a window the first block does not
-    // depend on the length: the table is requested beside it.
+    // without a window the first block does not depend on the length: the table is
+    // requested beside it
     const int32_t* table = v.table + (int64_t)b * v.table_stride;
-    auto pages_from = [&](int k0) {
-        int64_t at = (int64_t)(k0 + lane * KW) >> (v.page_shift - 5);
-        at = at < v.table_stride ? at : v.table_stride - 1;
-        return table[at];
-    };
-    auto page_in = [&](int pages, int i) {     // i uniform
-        const int page = __builtin_amdgcn_readlane(pages, i);
-        return page < 0 || page >= v.num_pages ? 0 : page;
-    };
     const int c0 = split * p.chunk, c1 = c0 + p.chunk;
     int pages = 0;
-    if (p.window == 0) pages = pages_from((c0 >> 5) + kw);
+    if (p.window == 0) pages = pages_from(v, table, (c0 >> 5) + kw, KW, lane);
 
     const Sequence s = sequence_of(v, b, p.max_q, p.max_kv);
     const int rows = s.count * p.gqa;
@@ -235,53 +138,31 @@ __global__ __launch_bounds__(KW * RW * 64, WPE) void kv4_attention_kernel(AttnPa
     const bool any = from < to;
     if (p.splits > 1 && !any) return;          // the join reads only splits with keys
     const int blk0 = from >> 5, blk1 = any ? (to + 31) >> 5 : blk0;
-    if (p.window > 0) pages = pages_from(blk0 + kw);
+    if (p.window > 0) pages = pages_from(v, table, blk0 + kw, KW, lane);
 
-    // the rows of this wave: queries as the B operand, row = column of the lane
+    const int nblk = 1 << (v.page_shift - 5);
+    const int64_t block_bytes = kv_block_bytes(D, NG);
+    auto block_at = [&](int page, int blk) {
+        return v.cache + (((int64_t)page * v.kv_heads + h) * nblk + (blk & (nblk - 1))) * block_bytes;
+    };
+
     h8_t qf[NR][NQ][NJ];
-    float qs[NR];                              // fp32 queries: the factor that was taken out of the lane's row
-    int64_t out_row[NR];                       // (token, head) index, < 0: none
+    float qs[NR];                              // fp32 queries: the factor that was taken out of the row
     int pos[NR];                               // last key the row sees
 #pragma unroll
     for (int n = 0; n < NR; ++n) {
-        int r = row0 + (rw * NR + n) * 16 + col;
-        const bool live = r < rows;
-        r = live ? r : rows - 1;
+        int r = row0 + n * 16 + col % R;
+        r = r < rows ? r : rows - 1;
         const int token = r / p.gqa, head = h * p.gqa + r % p.gqa;
-        const T* q = static_cast<const T*>(p.q) + (int64_t)(s.first + token) * p.q_stride + (int64_t)head * D + 8 * quarter;
-        out_row[n] = live ? (int64_t)(s.first + token) * v.q_heads + head : -1;
         pos[n] = p.causal ? s.len - s.count + token : s.len - 1;
-        if constexpr (!F32) {
-            typedef uint32_t raw __attribute__((ext_vector_type(4), aligned(2), may_alias));
-#pragma unroll
-            for (int j = 0; j < NJ; ++j)
-                qf[n][0][j] = __builtin_bit_cast(h8_t, (u4_t)*reinterpret_cast<const raw*>(q + 32 * j));
-        } else {
-            // the row scaled by a power of two to a maximum in [2^14, 2^15), then
-            // hi = fp16(q), lo = fp16(q - hi)
-            float f[NJ][8], mx = 0.0f;
-#pragma unroll
-            for (int j = 0; j < NJ; ++j) {
-                Frag8<T>::load(q + 32 * j, f[j]);
-#pragma unroll
-                for (int i = 0; i < 8; ++i) mx = fmaxf(mx, fabsf(f[j][i]) < __builtin_inff() ? fabsf(f[j][i]) : 0.0f);
-            }
-            mx = fmaxf(mx, __shfl_xor(mx, 16));
-            mx = fmaxf(mx, __shfl_xor(mx, 32));
-            int e = mx > 0.0f ? (int)(__builtin_bit_cast(uint32_t, mx) >> 23) - 127 - 14 : 0;
-            e = e < -126 ? -126 : e;
-            const float down = __builtin_bit_cast(float, (uint32_t)(127 - e) << 23);
-            qs[n] = __builtin_bit_cast(float, (uint32_t)(127 + e) << 23);
-#pragma unroll
-            for (int j = 0; j < NJ; ++j)
-#pragma unroll
-                for (int i = 0; i < 8; ++i) {
-                    const float x = f[j][i] * down;
-                    const _Float16 top = (_Float16)x;
-                    qf[n][0][j][i] = top;
-                    qf[n][NQ - 1][j][i] = fabsf(x) < __builtin_inff() ? (_Float16)(x - (float)top) : (_Float16)0.0f;
-                }
-        }
+        qs[n] = load_query<NJ>(static_cast<const T*>(p.q) + (int64_t)(s.first + token) * p.q_stride + (int64_t)head * D +
+                                   8 * quarter, qf[n]);
+    }
+    // every row of the workgroup sees the whole of a block below `whole`, from `open` on
+    int whole = s.len, open = 0;
+    if (p.causal) {
+        whole = s.len - s.count + row0 / p.gqa + 1;
+        if (p.window > 0) open = s.len - s.count + last_row / p.gqa - p.window + 1;
     }
 
     f4_t o[NR][NT];
@@ -293,72 +174,78 @@ __global__ __launch_bounds__(KW * RW * 64, WPE) void kv4_attention_kernel(AttnPa
 #pragma unroll
         for (int t = 0; t < NT; ++t) o[n][t] = f4_t{0.0f, 0.0f, 0.0f, 0.0f};
     }
-
-    const int nblk = 1 << (v.page_shift - 5);
-    const int64_t block_bytes = kv_block_bytes(D, NG);
-    auto block_at = [&](int page, int blk) {
-        return v.cache + (((int64_t)page * v.kv_heads + h) * nblk + (blk & (nblk - 1))) * block_bytes;
-    };
-    // every row of the workgroup sees the whole of a block below `whole`, from `open` on
-    int whole = s.len, open = 0;
-    if (p.causal) {
-        whole = s.len - s.count + row0 / p.gqa + 1;
-        if (p.window > 0) open = s.len - s.count + last_row / p.gqa - p.window + 1;
+    // where the lane's two (four, eight) entries of P go among its 8 keys: masks
+    // of the halves of the four registers
+    uint32_t put[2] = {0, 0};
+    if constexpr (GRP == 4) {
+        const uint32_t half = (copy & 1) ? 0xFFFF0000u : 0x0000FFFFu;
+        put[0] = copy < 2 ? half : 0u;
+        put[1] = copy < 2 ? 0u : half;
+    } else if constexpr (GRP == 2) {
+        put[0] = copy == 0 ? 0xFFFFFFFFu : 0u;
+        put[1] = ~put[0];
     }
 
-    __shared__ __align__(16) uint32_t meta[kWaves][64 * NG];
-    uint32_t* slot = meta[wave];
+    __shared__ __align__(16) uint32_t meta[KW][64 * NG];
+    uint32_t* slot = meta[kw];
 
     auto compute = [&](const RawBlock<D, NG>& r, int blk) {
         // a wave's LDS operations complete in order: no barrier between its lanes
 #pragma unroll
         for (int i = 0; i < NG; ++i) slot[i * 64 + lane] = r.meta[i];
         __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
-        // ---- logits of 32 keys by 16 NR rows ----
-        float x[NR][2][4];
+        uint32_t kwd[2][I * NG], vwd[2][I * NG];   // words of the lane's own keys
+        const int mine = 4 * quarter + copy * I;
 #pragma unroll
         for (int t = 0; t < 2; ++t) {
-            uint32_t kw4[4 * NG];
-            four_keys<NG>(slot + (t * 16 + 4 * quarter) * NG, kw4);
-            f4_t acc[NR][NG];
+            words<I * NG>(slot + (t * 16 + mine) * NG, kwd[t]);
+            words<I * NG>(slot + (32 + t * 16 + mine) * NG, vwd[t]);
+        }
+        // ---- logits ----
+        float x[NR][2][I];
+#pragma unroll
+        for (int t = 0; t < 2; ++t) {
 #pragma unroll
             for (int g = 0; g < NG; ++g) {
                 const uint32_t zr = zp_pair((slot[(t * 16 + col) * NG + g] >> 16) & 15u);
+                f4_t acc[NR];
 #pragma unroll
-                for (int n = 0; n < NR; ++n) acc[n][g] = f4_t{0.0f, 0.0f, 0.0f, 0.0f};
+                for (int n = 0; n < NR; ++n) acc[n] = f4_t{0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
                 for (int jj = 0; jj < JG; ++jj) {
                     const int j = g * JG + jj, w = t * NJ + j;
                     h2_t a4[4];
                     unpack_zr(r.k[w >> 2][w & 3], zr, a4);
-                    const h8_t a = join(a4);
+                    const h8_t k8 = join(a4);
 #pragma unroll
                     for (int n = 0; n < NR; ++n)
 #pragma unroll
-                        for (int c = 0; c < NQ; ++c) acc[n][g] = mfma(a, qf[n][c][j], acc[n][g]);
+                        for (int c = 0; c < NQ; ++c) acc[n] = mfma(k8, qf[n][c][j], acc[n]);
                 }
-            }
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
+                for (int n = 0; n < NR; ++n)
 #pragma unroll
-                for (int g = 0; g < NG; ++g) {
-                    const float ks = scale_of(kw4[i * NG + g]) * p.scale_log2;
-#pragma unroll
-                    for (int n = 0; n < NR; ++n)
-                        x[n][t][i] = g == 0 ? acc[n][g][i] * ks : __builtin_fmaf(acc[n][g][i], ks, x[n][t][i]);
-                }
-                if constexpr (F32) {
-#pragma unroll
-                    for (int n = 0; n < NR; ++n) x[n][t][i] *= qs[n];
-                }
+                    for (int i = 0; i < I; ++i) {
+                        float dot = acc[n][i];         // of the lane's own keys
+                        if constexpr (GRP == 2) dot = copy ? acc[n][2 + i] : acc[n][i];
+                        if constexpr (GRP == 4) {
+                            const float e0 = (copy & 1) ? acc[n][1] : acc[n][0], e1 = (copy & 1) ? acc[n][3] : acc[n][2];
+                            dot = (copy & 2) ? e1 : e0;
+                        }
+                        const float ks = scale_of(kwd[t][i * NG + g]) * p.scale_log2;
+                        x[n][t][i] = g == 0 ? dot * ks : __builtin_fmaf(dot, ks, x[n][t][i]);
+                    }
             }
         }
-        // ---- masks, and the running reference: the largest logit plus the exponent of its value scale ----
-        uint32_t vw[2][4 * NG];
+        if constexpr (F32) {
 #pragma unroll
-        for (int t = 0; t < 2; ++t) four_keys<NG>(slot + (32 + t * 16 + 4 * quarter) * NG, vw[t]);
+            for (int n = 0; n < NR; ++n)
+#pragma unroll
+                for (int k = 0; k < 2 * I; ++k) x[n][k / I][k % I] *= qs[n];
+        }
+        // ---- masks, and the running reference: the largest logit plus the exponent of its value scale ----
         const bool edge = blk * 32 + 32 > whole || blk * 32 < open;
-        uint32_t seen[NR];                     // bit 4 t + i: the row sees the key
+        uint32_t seen[NR];                     // bit t I + i: the row sees the key
         float mxs[NR];
         if (edge) {                            // key by key: a hidden key's scale is not looked at
 #pragma unroll
@@ -369,38 +256,38 @@ __global__ __launch_bounds__(KW * RW * 64, WPE) void kv4_attention_kernel(AttnPa
 #pragma unroll
                 for (int t = 0; t < 2; ++t)
 #pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        const int key = blk * 32 + t * 16 + 4 * quarter + i;
-                        uint32_t w = vw[t][i * NG];
+                    for (int i = 0; i < I; ++i) {
+                        const int key = blk * 32 + t * 16 + mine + i;
+                        uint32_t w = vwd[t][i * NG];
 #pragma unroll
-                        for (int g = 1; g < NG; ++g) w = max_halves(w, vw[t][i * NG + g]);
+                        for (int g = 1; g < NG; ++g) w = max_halves(w, vwd[t][i * NG + g]);
                         if (key <= pos[n] && key > below && key < s.len)
-                            seen[n] |= 1u << (4 * t + i);
+                            seen[n] |= 1u << (I * t + i);
                         else
                             x[n][t][i] = -__builtin_inff();
                         mxs[n] = fmaxf(mxs[n], x[n][t][i] + top_exponent(w));
                     }
             }
         } else {
-            uint32_t w = vw[0][0];
+            uint32_t w = vwd[0][0];
 #pragma unroll
-            for (int k = 1; k < 8 * NG; ++k) w = max_halves(w, vw[k / (4 * NG)][k % (4 * NG)]);
+            for (int k = 1; k < 2 * I * NG; ++k) w = max_halves(w, vwd[k / (I * NG)][k % (I * NG)]);
             const float top = top_exponent(w);
 #pragma unroll
             for (int n = 0; n < NR; ++n) {
                 float m = x[n][0][0];
 #pragma unroll
-                for (int k = 1; k < 8; ++k) m = fmaxf(m, x[n][k >> 2][k & 3]);
+                for (int k = 1; k < 2 * I; ++k) m = fmaxf(m, x[n][k / I][k % I]);
                 mxs[n] = m + top;
             }
         }
 #pragma unroll
         for (int n = 0; n < NR; ++n) {
             float mx = mxs[n];
-            if (__builtin_amdgcn_ballot_w64(mx > M[n] + 14.0f)) {
+            if (__builtin_amdgcn_ballot_w64(mx > M[n] + kRaise)) {
                 mx = fmaxf(mx, __shfl_xor(mx, 16));
                 mx = fmaxf(mx, __shfl_xor(mx, 32));
-                const float next = fmaxf(M[n], mx - 10.0f);
+                const float next = fmaxf(M[n], mx - kBelow);
                 const float alpha = exp2f(M[n] - next);
                 M[n] = next;
                 l[n] *= alpha;
@@ -412,46 +299,69 @@ __global__ __launch_bounds__(KW * RW * 64, WPE) void kv4_attention_kernel(AttnPa
 #pragma unroll
         for (int n = 0; n < NR; ++n)
 #pragma unroll
-            for (int t = 0; t < 2; ++t)
-#pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    x[n][t][i] = __builtin_amdgcn_exp2f(x[n][t][i] - M[n]);
-                    l[n] += x[n][t][i];
-                }
+            for (int k = 0; k < 2 * I; ++k) {
+                float& e = x[n][k / I][k % I];
+                e = __builtin_amdgcn_exp2f(e - M[n]);
+                l[n] += e;
+            }
         // ---- O^T += V^T (p s')^T, group by group ----
+        uint32_t vall[2][4 * NG];
+#pragma unroll
+        for (int t = 0; t < 2; ++t) words<4 * NG>(slot + (32 + t * 16 + 4 * quarter) * NG, vall[t]);
 #pragma unroll
         for (int g = 0; g < NG; ++g) {
             h8_t pb[NR], pl[NR];               // p s' as the B operand, its second part
-            float f[NR][8];
+            float f[NR][2 * I];
 #pragma unroll
-            for (int k = 0; k < 8; ++k) {
-                const float vs = scale_of(vw[k >> 2][(k & 3) * NG + g]);
+            for (int k = 0; k < 2 * I; ++k) {
+                const float vs = scale_of(vwd[k / I][(k % I) * NG + g]);
 #pragma unroll
-                for (int n = 0; n < NR; ++n) f[n][k] = x[n][k >> 2][k & 3] * vs;
+                for (int n = 0; n < NR; ++n) f[n][k] = x[n][k / I][k % I] * vs;
             }
             if (edge) {                        // a hidden key adds nothing whatever its scale is
 #pragma unroll
                 for (int n = 0; n < NR; ++n)
 #pragma unroll
-                    for (int k = 0; k < 8; ++k) f[n][k] = (seen[n] >> k) & 1u ? f[n][k] : 0.0f;
+                    for (int k = 0; k < 2 * I; ++k) f[n][k] = (seen[n] >> k) & 1u ? f[n][k] : 0.0f;
             }
 #pragma unroll
-            for (int n = 0; n < NR; ++n)
+            for (int n = 0; n < NR; ++n) {
+                _Float16 top[2 * I], low[2 * I];
 #pragma unroll
-                for (int k = 0; k < 8; ++k) {
-                    pb[n][k] = (_Float16)f[n][k];
-                    if constexpr (SPLIT) pl[n][k] = (_Float16)(f[n][k] - (float)pb[n][k]);
+                for (int k = 0; k < 2 * I; ++k) {
+                    top[k] = (_Float16)f[n][k];
+                    low[k] = SPLIT ? (_Float16)(f[n][k] - (float)top[k]) : (_Float16)0.0f;
                 }
-            // zero points of the lane's 8 keys, in the pairs of the unpack
+                auto spread = [&](const _Float16* e) {
+                    u4_t w;
+                    if constexpr (GRP == 1) {
+                        h8_t b8;
+#pragma unroll
+                        for (int k = 0; k < 2 * I; ++k) b8[k] = e[k];
+                        return b8;
+                    } else {
+                        const uint32_t d0 = as_u32(GRP == 4 ? h2_t{e[0], e[0]} : h2_t{e[0], e[1]});
+                        const uint32_t d1 = as_u32(GRP == 4 ? h2_t{e[1], e[1]} : h2_t{e[2], e[3]});
+                        w.x = d0 & put[0];
+                        w.y = d0 & put[1];
+                        w.z = d1 & put[0];
+                        w.w = d1 & put[1];
+                        return __builtin_bit_cast(h8_t, w);
+                    }
+                };
+                pb[n] = spread(top);
+                if constexpr (SPLIT) pl[n] = spread(low);
+            }
+            const h2_t sixteenth = {(_Float16)0.0625f, (_Float16)0.0625f};
+            // zero points of all 8 keys of the lane's quarter, in the pairs of the unpack
             h2_t zl[4], zh[4];
 #pragma unroll
             for (int k = 0; k < 4; ++k) {
-                const uint32_t m0 = vw[k >> 1][(2 * (k & 1)) * NG + g], m1 = vw[k >> 1][(2 * (k & 1) + 1) * NG + g];
+                const uint32_t m0 = vall[k >> 1][(2 * (k & 1)) * NG + g], m1 = vall[k >> 1][(2 * (k & 1) + 1) * NG + g];
                 const uint32_t z2 = __builtin_amdgcn_perm(m1, m0, 0x07060302u);
                 zl[k] = as_h2(__builtin_amdgcn_bitop3_b32(z2, 0x000F000Fu, 0xE400E400u, 0xEA));
                 zh[k] = as_h2(__builtin_amdgcn_bitop3_b32(z2 << 4, 0x00F000F0u, 0xD400D400u, 0xEA));
             }
-            const h2_t sixteenth = {(_Float16)0.0625f, (_Float16)0.0625f};
 #pragma unroll
             for (int uu = 0; uu < JG; ++uu) {
                 const int u = g * JG + uu;     // dims 32u .. 32u+31: tiles 2u and 2u+1
@@ -486,14 +396,14 @@ __global__ __launch_bounds__(KW * RW * 64, WPE) void kv4_attention_kernel(AttnPa
         RawBlock<D, NG> set[PF];
 #pragma unroll
         for (int i = 0; i < PF; ++i)
-            load_block<D, NG>(block_at(page_in(pages, i), blk + i * KW), blk + i * KW < blk1, lane, set[i]);
+            load_block<D, NG>(block_at(page_in(v, pages, i), blk + i * KW), blk + i * KW < blk1, lane, set[i]);
         // whole turns of the sets, then what is left: no branch between a load and
         // its use but the refill's, whose load is waited for where it is made
         const int steps = (blk1 - blk + KW - 1) / KW;
         int at = PF;                           // lane of `pages` with the next load's page
         for (int turn = 0; turn < steps / PF; ++turn) {
             if (at > 64 - PF) {
-                pages = pages_from(blk + PF * KW);
+                pages = pages_from(v, table, blk + PF * KW, KW, lane);
                 at = 0;
                 asm volatile("" : "+v"(pages));
             }
@@ -501,7 +411,7 @@ __global__ __launch_bounds__(KW * RW * 64, WPE) void kv4_attention_kernel(AttnPa
             for (int i = 0; i < PF; ++i) {
                 compute(set[i], blk);
                 const int next = blk + PF * KW;
-                load_block<D, NG>(block_at(page_in(pages, at), next), next < blk1, lane, set[i]);
+                load_block<D, NG>(block_at(page_in(v, pages, at), next), next < blk1, lane, set[i]);
                 ++at;
                 blk += KW;
             }
@@ -511,90 +421,66 @@ __global__ __launch_bounds__(KW * RW * 64, WPE) void kv4_attention_kernel(AttnPa
             if (i < steps % PF) compute(set[i], blk + i * KW);
     }
 #pragma unroll
-    for (int n = 0; n < NR; ++n) {
+    for (int n = 0; n < NR; ++n) {             // the sum of a column over its lanes
         l[n] += __shfl_xor(l[n], 16);
         l[n] += __shfl_xor(l[n], 32);
     }
 
-    // ---- waves of the same rows join through LDS, 16 rows by up to 128 dims at a time ----
-    if constexpr (KW > 1) {
-        constexpr int kMost = KW > 4 ? 64 : 128;           // at most 34 KB
-        constexpr int kDims = D < kMost ? D : kMost, kPitch = kDims + 4;   // rows start in different banks
-        constexpr int kParts = D / kDims;
-        __shared__ __align__(16) float so[kWaves][16][kPitch];
-        __shared__ float ml[kWaves][NR][16][2];
-        if (quarter == 0) {
-#pragma unroll
-            for (int n = 0; n < NR; ++n) {
-                ml[wave][n][col][0] = M[n];
-                ml[wave][n][col][1] = l[n];
-            }
-        }
-        // wave kw takes every KW-th tile of its rows: M, l and o become the sums
+    // ---- the waves and the copies join through LDS, 16 columns by up to 128 dims at a time ----
+    constexpr int kMost = KW > 4 ? 64 : 128;               // at most 34 KB
+    constexpr int kDims = D < kMost ? D : kMost, kPitch = kDims + 4;   // rows start in different banks
+    constexpr int kParts = D / kDims, kTiles = kDims / 16, kJoin = KW * GRP;
+    __shared__ __align__(16) float so[KW][16][kPitch];
+    __shared__ float ml[KW][NR][16][2];
+    if (quarter == 0) {
 #pragma unroll
         for (int n = 0; n < NR; ++n) {
-            float w[KW];
-#pragma unroll
-            for (int part = 0; part < kParts; ++part) {
-                if (n + part > 0) __syncthreads();         // the last part has been read
-#pragma unroll
-                for (int t = 0; t < kDims / 16; ++t)
-                    *reinterpret_cast<f4_t*>(&so[wave][col][16 * t + 4 * quarter]) = o[n][part * (kDims / 16) + t];
-                __syncthreads();
-                if (part == 0) {
-                    float m = kLow, sum = 0.0f;
-#pragma unroll
-                    for (int k = 0; k < KW; ++k) m = fmaxf(m, ml[rw * KW + k][n][col][0]);
-#pragma unroll
-                    for (int k = 0; k < KW; ++k) {
-                        w[k] = exp2f(ml[rw * KW + k][n][col][0] - m);
-                        sum = __builtin_fmaf(ml[rw * KW + k][n][col][1], w[k], sum);
-                    }
-                    M[n] = m;
-                    l[n] = sum;
-                }
-#pragma unroll
-                for (int t = 0; t < kDims / 16; ++t) {
-                    if ((part * (kDims / 16) + t) % KW != kw) continue;
-                    f4_t a = {0.0f, 0.0f, 0.0f, 0.0f};
-#pragma unroll
-                    for (int k = 0; k < KW; ++k)
-                        a += *reinterpret_cast<const f4_t*>(&so[rw * KW + k][col][16 * t + 4 * quarter]) * w[k];
-                    o[n][part * (kDims / 16) + t] = a;
-                }
-            }
+            ml[kw][n][col][0] = M[n];
+            ml[kw][n][col][1] = l[n];
         }
     }
-
-    // ---- results or partials ----
+    const int row = col % R, worker = kw * GRP + copy;     // of a row: tile t of a part goes to worker t % kJoin
 #pragma unroll
     for (int n = 0; n < NR; ++n) {
-        if (out_row[n] < 0) continue;
-        if (p.splits == 1) {
-            const float inv = l[n] == 0.0f ? 0.0f : 1.0f / l[n];   // a row that sees nothing gives zeros
-            T* out = static_cast<T*>(p.out) + out_row[n] * D + 4 * quarter;
+        const int r = row0 + n * 16 + row;
+        const int64_t out_row = r < rows ? (int64_t)(s.first + r / p.gqa) * v.q_heads + h * p.gqa + r % p.gqa : -1;
+        float m = kLow, sum = 0.0f, w[kJoin];
 #pragma unroll
-            for (int t = 0; t < NT; ++t) {
-                if (t % KW != kw) continue;
-                typedef T out4 __attribute__((ext_vector_type(4), aligned(sizeof(T))));
-                out4 y;
+        for (int part = 0; part < kParts; ++part) {
+            if (n + part > 0) __syncthreads();             // the last part has been read
 #pragma unroll
-                for (int i = 0; i < 4; ++i) y[i] = (T)(o[n][t][i] * inv);
-                *reinterpret_cast<out4*>(out + 16 * t) = y;
+            for (int t = 0; t < kTiles; ++t)
+                *reinterpret_cast<f4_t*>(&so[kw][col][16 * t + 4 * quarter]) = o[n][part * kTiles + t];
+            __syncthreads();
+            if (part == 0) {
+#pragma unroll
+                for (int k = 0; k < kJoin; ++k) m = fmaxf(m, ml[k / GRP][n][row + k % GRP * R][0]);
+#pragma unroll
+                for (int k = 0; k < kJoin; ++k) {
+                    w[k] = exp2f(ml[k / GRP][n][row + k % GRP * R][0] - m);
+                    sum = __builtin_fmaf(ml[k / GRP][n][row + k % GRP * R][1], w[k], sum);
+                }
             }
-            if (p.lse && kw == 0 && quarter == 0)
-                p.lse[out_row[n]] = l[n] == 0.0f ? -__builtin_inff() : (M[n] + log2f(l[n])) * 0.69314718055994531f;
-        } else {
-            const int64_t at = (int64_t)split * v.tokens * v.q_heads + out_row[n];
-            float* part = p.part_o + at * D + 4 * quarter;
+            if (out_row < 0) continue;
+            for (int t = worker; t < kTiles; t += kJoin) {
+                f4_t y = {0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
-            for (int t = 0; t < NT; ++t) {
-                if (t % KW != kw) continue;
-                *reinterpret_cast<f4_t*>(part + 16 * t) = o[n][t];
+                for (int k = 0; k < kJoin; ++k)
+                    y += *reinterpret_cast<const f4_t*>(&so[k / GRP][row + k % GRP * R][16 * t + 4 * quarter]) * w[k];
+                const int d = part * kDims + 16 * t + 4 * quarter;
+                if (p.splits == 1)                         // a row that sees nothing gives zeros
+                    store4(static_cast<T*>(p.out) + out_row * D + d, y, sum == 0.0f ? 0.0f : 1.0f / sum);
+                else
+                    *reinterpret_cast<f4_t*>(p.part_o + ((int64_t)split * v.tokens * v.q_heads + out_row) * D + d) = y;
             }
-            if (kw == 0 && quarter == 0) {
-                p.part_ml[2 * at] = M[n];
-                p.part_ml[2 * at + 1] = l[n];
+            if (part == 0 && worker == 0 && quarter == 0) {
+                if (p.splits > 1) {
+                    float* e = p.part_ml + 2 * ((int64_t)split * v.tokens * v.q_heads + out_row);
+                    e[0] = m;
+                    e[1] = sum;
+                } else if (p.lse) {
+                    p.lse[out_row] = log_sum(m, sum);
+                }
             }
         }
     }
@@ -676,32 +562,36 @@ __global__ __launch_bounds__(kJoinThreads) void kv4_join_kernel(AttnParams p)
         const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
         static_cast<T*>(p.out)[row * D + tid] = (T)(y * inv);
     }
-    if (p.lse && tid == 0) p.lse[row] = sum == 0.0f ? -__builtin_inff() : (m + log2f(sum)) * 0.69314718055994531f;
+    if (p.lse && tid == 0) p.lse[row] = log_sum(m, sum);
 }
-
-// How a call is cut: row tiles per wave, waves that share keys, waves with rows
-// of their own, splits.
-struct Plan {
-    int nr, kw, rw, rows;             // rows per workgroup
-    int row_tiles, splits, chunk;
-};
 
 Plan plan_of(const AttentionArgs& a)
 {
-    Plan c;
+    Plan c = {};
     const int64_t rows = a.max_q * (a.v.q_heads / a.v.kv_heads);
-    c.nr = rows <= 16 || a.v.head_dim == 256 ? 1 : 2;
-    // few rows: all waves on the same rows, the keys cut between them
-    const bool few = rows <= 16 * c.nr;
-    const bool brief = few && c.nr == 1 && a.v.head_dim < 256 && a.max_kv <= 1024;
-    c.kw = brief ? 8 : few ? 4 : 1;
-    c.rw = few ? 1 : 4;
-    c.rows = c.nr * 16 * c.rw;
+    const bool wide = a.v.head_dim == 256;
+    int64_t least, want;                       // keys that keep every wave busy; workgroups that fill the chip
+    if (rows <= (wide || a.v.groups > 2 ? 16 : 32)) {   // two column tiles where the registers hold them
+        // few rows: the waves of a workgroup cut the keys between them
+        c.group = rows <= 4 ? 4 : rows <= 8 ? 2 : rows <= 16 ? 1 : 0;
+        c.rows = c.group ? 16 / c.group : 32;
+        // up to 1024 keys one workgroup of 8 waves does without the join
+        c.kind = !wide && a.v.groups <= 2 && c.group && a.max_kv <= 1024 ? 0 : 1;
+        least = 256;
+        want = 2048;
+    } else {
+        c.kind = 2;
+        c.waves = 8;
+        const int64_t wgs = (rows + prompt_rows(a.v.head_dim, 8) - 1) / prompt_rows(a.v.head_dim, 8) * a.v.kv_heads * a.v.batch;
+        if (wgs < 512) c.waves = 4;            // two smaller workgroups a CU
+        c.rows = prompt_rows(a.v.head_dim, c.waves);
+        least = 256;
+        want = 256;
+    }
     c.row_tiles = (int)((rows + c.rows - 1) / c.rows);
     const int64_t units = (int64_t)c.row_tiles * a.v.kv_heads * a.v.batch;
-    const int64_t least = 64 * c.kw;           // keys that give every wave two blocks
     const int64_t most = (a.max_kv + least - 1) / least;
-    int64_t splits = brief ? 1 : ((few ? 2048 : 256) + units - 1) / units;
+    int64_t splits = c.kind == 0 ? 1 : (want + units - 1) / units;
     splits = splits > most ? most : splits;
     splits = splits > kMaxSplits ? kMaxSplits : splits < 1 ? 1 : splits;
     c.chunk = (int)(((a.max_kv + splits - 1) / splits + least - 1) / least * least);
@@ -711,51 +601,90 @@ Plan plan_of(const AttentionArgs& a)
     return c;
 }
 
-template <int D, int NG, bool F32, int NR, int KW, int RW>
+template <int D, int NG, bool F32, int GRP, int NR, int KW>
 hipError_t launch_rows(const AttnParams& p, const Plan& c, hipStream_t s)
 {
     const dim3 grid((unsigned)(p.v.kv_heads * c.splits * c.row_tiles), (unsigned)p.v.batch);
-    // as many as the registers hold without spilling
-    constexpr int PF = KW == 8 ? 4 - 2 * (D == 128 && F32) : D == 256 || (D == 128 && NR == 2 && (F32 || (NG == 4 && KW > 1))) ? 1
-                       : KW == 1 || (D == 128 && (F32 || NR == 2)) ? 2 : 3;
-    constexpr int WPE = NR == 1 && KW == 4 && D == 128 && NG == 1 && !F32 ? 3 : 1;
-    // few rows: the matrix cores have time for p in two parts
-    kv4_attention_kernel<D, NG, F32, F32 || KW >= 4, NR, KW, RW, PF, WPE><<<grid, dim3(KW * RW * 64), 0, s>>>(p);
-    hipError_t e = hipGetLastError();
-    if (e != hipSuccess || c.splits == 1) return e;
-    kv4_join_kernel<D, F32><<<dim3((unsigned)(p.max_q * p.v.q_heads), (unsigned)p.v.batch), dim3(kJoinThreads), 0, s>>>(p);
+    // as many register sets as the registers hold without spilling
+    constexpr bool big = D == 256 || (NR == 2 && F32) || (D == 128 && NG == 4 && (F32 || GRP == 1));
+    constexpr bool lean = NR == 1 && KW == 4 && D == 128 && NG == 1 && !F32;
+    constexpr int PF = KW == 8 ? 4 - 2 * (D == 128 && F32) : big ? 1 : D == 128 && (F32 || NR == 2 || (lean && GRP < 4)) ? 2 : 3;
+    constexpr int WPE = lean ? 3 : 1;
+    kv4_attention_kernel<D, NG, F32, GRP, NR, KW, PF, WPE><<<grid, dim3(KW * 64), 0, s>>>(p);
     return hipGetLastError();
 }
 
-template <int D, int NG, bool F32>
-hipError_t launch_groups(const AttnParams& p, const Plan& c, hipStream_t s)
+template <int D, int NG, bool F32, int KW>
+hipError_t launch_group(const AttnParams& p, const Plan& c, hipStream_t s)
 {
-    // head_dim 256 keeps one row tile a wave: two do not fit the registers
-    constexpr int NR = D == 256 ? 1 : 2;
-    if (c.kw == 1) return launch_rows<D, NG, F32, NR, 1, 4>(p, c, s);
-    if constexpr (D < 256)
-        if (c.kw == 8) return launch_rows<D, NG, F32, 1, 8, 1>(p, c, s);
-    return c.nr == 1 ? launch_rows<D, NG, F32, 1, 4, 1>(p, c, s) : launch_rows<D, NG, F32, NR, 4, 1>(p, c, s);
+    switch (c.group) {
+    case 4: return launch_rows<D, NG, F32, 4, 1, KW>(p, c, s);
+    case 2: return launch_rows<D, NG, F32, 2, 1, KW>(p, c, s);
+    default: return launch_rows<D, NG, F32, 1, 1, KW>(p, c, s);
+    }
+}
+
+template <int D, int NG, bool F32>
+hipError_t launch_few(const AttnParams& p, const Plan& c, hipStream_t s)
+{
+    if constexpr (D < 256 && NG <= 2) {
+        if (c.group == 0) return launch_rows<D, NG, F32, 1, 2, 4>(p, c, s);
+        if (c.kind == 0) return launch_group<D, NG, F32, 8>(p, c, s);
+    }
+    return launch_group<D, NG, F32, 4>(p, c, s);
 }
 
 template <int D, int NG> hipError_t launch_type(const AttnParams& p, const Plan& c, int f16, hipStream_t s)
 {
-    return f16 ? launch_groups<D, NG, false>(p, c, s) : launch_groups<D, NG, true>(p, c, s);
+    return f16 ? launch_few<D, NG, false>(p, c, s) : launch_few<D, NG, true>(p, c, s);
+}
+
+hipError_t launch_few_rows(const AttnParams& p, const Plan& c, int f16, hipStream_t s)
+{
+    const int ng = p.v.groups;
+    switch (p.v.head_dim) {
+    case 64: return ng == 1 ? launch_type<64, 1>(p, c, f16, s) : launch_type<64, 2>(p, c, f16, s);
+    case 128:
+        return ng == 1 ? launch_type<128, 1>(p, c, f16, s)
+                       : ng == 2 ? launch_type<128, 2>(p, c, f16, s) : launch_type<128, 4>(p, c, f16, s);
+    default:
+        return ng == 2 ? launch_type<256, 2>(p, c, f16, s)
+                       : ng == 4 ? launch_type<256, 4>(p, c, f16, s) : launch_type<256, 8>(p, c, f16, s);
+    }
+}
+
+template <int D> hipError_t launch_join_dim(const AttnParams& p, int f16, hipStream_t s)
+{
+    const dim3 grid((unsigned)(p.max_q * p.v.q_heads), (unsigned)p.v.batch);
+    if (f16) kv4_join_kernel<D, false><<<grid, dim3(kJoinThreads), 0, s>>>(p);
+    else kv4_join_kernel<D, true><<<grid, dim3(kJoinThreads), 0, s>>>(p);
+    return hipGetLastError();
 }
 
 }  // namespace
 
+hipError_t launch_join(const AttnParams& p, int f16, hipStream_t s)
+{
+    switch (p.v.head_dim) {
+    case 64: return launch_join_dim<64>(p, f16, s);
+    case 128: return launch_join_dim<128>(p, f16, s);
+    default: return launch_join_dim<256>(p, f16, s);
+    }
+}
+
+}  // namespace kv4
+
 size_t kv4_attention_workspace(const AttentionArgs& a)
 {
-    const Plan c = plan_of(a);
+    const kv4::Plan c = kv4::plan_of(a);
     if (c.splits == 1) return 0;
     return (size_t)c.splits * a.v.tokens * a.v.q_heads * (a.v.head_dim + 2) * 4;
 }
 
 hipError_t launch_kv4_attention(const AttentionArgs& a, hipStream_t stream, const char** variant)
 {
-    const Plan c = plan_of(a);
-    AttnParams p;
+    const kv4::Plan c = kv4::plan_of(a);
+    kv4::AttnParams p;
     p.v = a.v;
     p.q = a.q;
     p.q_stride = a.q_stride;
@@ -773,18 +702,11 @@ hipError_t launch_kv4_attention(const AttentionArgs& a, hipStream_t stream, cons
     p.chunk = c.chunk;
     p.row_tiles = c.row_tiles;
     p.rows_per_wg = c.rows;
-    *variant = c.splits > 1 ? "attention_kv4_split" : "attention_kv4";
-    const int ng = a.v.groups;
-    switch (a.v.head_dim) {
-    case 64:
-        return ng == 1 ? launch_type<64, 1>(p, c, a.f16, stream) : launch_type<64, 2>(p, c, a.f16, stream);
-    case 128:
-        return ng == 1 ? launch_type<128, 1>(p, c, a.f16, stream)
-                       : ng == 2 ? launch_type<128, 2>(p, c, a.f16, stream) : launch_type<128, 4>(p, c, a.f16, stream);
-    default:
-        return ng == 2 ? launch_type<256, 2>(p, c, a.f16, stream)
-                       : ng == 4 ? launch_type<256, 4>(p, c, a.f16, stream) : launch_type<256, 8>(p, c, a.f16, stream);
-    }
+    *variant = c.kind == 2 ? (c.splits > 1 ? "attention_kv4_prompt_split" : "attention_kv4_prompt")
+                           : (c.splits > 1 ? "attention_kv4_split" : "attention_kv4");
+    const hipError_t e = c.kind == 2 ? kv4::launch_prompt(p, c, a.f16, stream) : kv4::launch_few_rows(p, c, a.f16, stream);
+    if (e != hipSuccess || c.splits == 1) return e;
+    return kv4::launch_join(p, a.f16, stream);
 }
 
 }  // namespace mnb

@@ -1,0 +1,454 @@
+// kv4_prompt.hip -- attention over the paged 4-bit cache for many query rows
+// per key head (prompts and long chunks): the mathematics and the operand
+// layout of kv4_attention.hip, with the unpacked keys and values shared.
+//
+// A workgroup of RW waves holds RW x 16 NR rows; its waves unpack a stage of
+// 8192 / D keys together, once, into fp16 fragments in LDS, and every wave reads
+// all of them as its A operands.  (Unpacked by each wave for itself, the codes
+// cost as many vector instructions as the softmax.)  The next stage's codes are
+// requested before a stage's products and unpacked into the other half of LDS
+// after them, so there is one barrier a stage.  What is left in the vector
+// units is the softmax, about 8 instructions' time per (row, key), half of it
+// the exponential; the matrix cores run beside it in the other wave of the SIMD.
+#include "kv4_attention.hpp"
+
+namespace mnb {
+namespace kv4 {
+
+namespace {
+
+template <int D, int NG, bool F32, int NR, int RW>
+__global__ __launch_bounds__(RW * 64, 2) void kv4_prompt_kernel(AttnParams p)
+{
+    typedef typename std::conditional<F32, float, _Float16>::type T;
+    constexpr bool SPLIT = F32;
+    constexpr int NJ = D / 32, NT = D / 16, NQ = F32 ? 2 : 1, JG = NJ / NG;
+    constexpr int kRows = RW * NR * 16;
+    constexpr int SB = 256 / D > 0 ? 256 / D : 1;      // blocks of 32 keys in a stage: 8192 / D keys
+    constexpr int QB = D / 64;                         // 1 KB quads of a block's keys (and of its values)
+    constexpr int IT = 8 / RW;                         // quads a wave unpacks: 4 of keys, 4 of values in all
+    static_assert(SB * QB == 4, "four quads of each a stage");
+
+    __shared__ __align__(16) h8_t kf[2][SB][2][NJ][64];    // key fragments: tile, 32-dim step, lane
+    __shared__ __align__(16) h8_t vf[2][SB][NT][64];       // value fragments: 16-dim tile, lane
+    __shared__ __align__(16) float ks[2][SB][NG][32];      // scale * key scale, in log2 units
+    __shared__ __align__(16) float vs[2][SB][NG][32];
+    __shared__ __align__(16) uint32_t vw[2][SB][NG][32];   // value scale words (exponents)
+
+    const KvView& v = p.v;
+    const int lane = threadIdx.x & 63;
+    const int wave = uniform(threadIdx.x >> 6);
+    const int col = lane & 15, quarter = lane >> 4;
+    const int h = blockIdx.x % v.kv_heads;
+    const int split = (blockIdx.x / v.kv_heads) % p.splits;
+    const int tile = p.row_tiles - 1 - (int)(blockIdx.x / v.kv_heads / p.splits);   // longest key ranges first
+    const int b = blockIdx.y;
+
+    const Sequence s = sequence_of(v, b, p.max_q, p.max_kv);
+    const int rows = s.count * p.gqa;
+    const int row0 = tile * kRows;
+    if (row0 >= rows) return;                          // the whole workgroup
+    const int last_row = row0 + kRows <= rows ? row0 + kRows - 1 : rows - 1;
+    int lo, hi;
+    key_range(p, s, row0 / p.gqa, last_row / p.gqa, lo, hi);
+    const int c0 = split * p.chunk, c1 = c0 + p.chunk;
+    const int from = lo > c0 ? lo : c0, to = hi < c1 ? hi : c1;
+    const bool any = from < to;
+    if (p.splits > 1 && !any) return;                  // the join reads only splits with keys
+    const int blk0 = from >> 5, blk1 = any ? (to + 31) >> 5 : blk0;
+    const int stages = (blk1 - blk0 + SB - 1) / SB;
+
+    const int nblk = 1 << (v.page_shift - 5);
+    const int64_t block_bytes = kv_block_bytes(D, NG);
+    const int32_t* table = v.table + (int64_t)b * v.table_stride;
+    int pages = pages_from(v, table, blk0, 1, lane);   // of blocks page0 ..
+    int page0 = blk0;
+
+    // the rows of this wave
+    const int wrow0 = row0 + wave * NR * 16;
+    const bool busy = wrow0 < rows;                    // a wave past the rows only unpacks
+    h8_t qf[NR][NQ][NJ];
+    float qs[NR];
+    int pos[NR];
+    int64_t out_row[NR];
+#pragma unroll
+    for (int n = 0; n < NR; ++n) {
+        int r = wrow0 + n * 16 + col;
+        const bool live = r < rows;
+        r = live ? r : rows - 1;
+        const int token = r / p.gqa, head = h * p.gqa + r % p.gqa;
+        out_row[n] = live ? (int64_t)(s.first + token) * v.q_heads + head : -1;
+        pos[n] = p.causal ? s.len - s.count + token : s.len - 1;
+        qs[n] = load_query<NJ>(static_cast<const T*>(p.q) + (int64_t)(s.first + token) * p.q_stride + (int64_t)head * D +
+                                   8 * quarter, qf[n]);
+    }
+    // every row of the wave sees the whole of a block below `whole`, from `open`
+    // on, and none of a block from `none` on
+    int whole = s.len, open = 0, none = s.len;
+    if (p.causal) {
+        const int wlast = wrow0 + NR * 16 <= rows ? wrow0 + NR * 16 - 1 : rows - 1;
+        whole = s.len - s.count + wrow0 / p.gqa + 1;
+        none = s.len - s.count + wlast / p.gqa + 1;
+        if (p.window > 0) open = s.len - s.count + wlast / p.gqa - p.window + 1;
+    }
+
+    f4_t o[NR][NT];
+    float M[NR], l[NR];
+#pragma unroll
+    for (int n = 0; n < NR; ++n) {
+        M[n] = kLow;
+        l[n] = 0.0f;
+#pragma unroll
+        for (int t = 0; t < NT; ++t) o[n][t] = f4_t{0.0f, 0.0f, 0.0f, 0.0f};
+    }
+
+    // ---- a stage's codes: requested, then unpacked into LDS ----
+    // Item it of a wave: quad Q = wave + it RW; Q < 4 keys, else values.  A key quad
+    // needs the zero points of the lane's own keys (both tiles where the quad spans
+    // them), a value quad those of the lane's 8 keys.
+    constexpr int kTilesOfQuad = D == 64 ? 2 : 1;      // key tiles in a quad
+    u4_t code[IT];
+    uint32_t zw[IT][8 * NG];
+
+    auto request = [&](int st) {
+#pragma unroll
+        for (int it = 0; it < IT; ++it) {
+            const int Q = wave + it * RW;
+            const bool is_v = Q >= 4;
+            const int qq = Q & 3, bi = qq / QB, qi = qq % QB;
+            const int blk = blk0 + st * SB + bi;
+            const bool there = blk < blk1;
+            int at = blk - page0;
+            at = at < 0 ? 0 : at > 63 ? 63 : at;
+            unsigned char* base = v.cache + (((int64_t)page_in(v, pages, at) * v.kv_heads + h) * nblk + (blk & (nblk - 1))) * block_bytes;
+            const __amdgpu_buffer_rsrc_t rs =
+                __builtin_amdgcn_make_buffer_rsrc(base, 0, there ? 32 * D + 256 * NG : 0, 0x00020000);
+            code[it] = __builtin_amdgcn_raw_buffer_load_b128(rs, lane * 16, (is_v ? 16 * D : 0) + qi * 1024, 0);
+            const int meta = 32 * D + (is_v ? 128 * NG : 0);
+            if (is_v) {
+#pragma unroll
+                for (int t = 0; t < 2; ++t)
+#pragma unroll
+                    for (int i = 0; i < NG; ++i) {
+                        const u4_t r = __builtin_amdgcn_raw_buffer_load_b128(rs, 16 * NG * quarter + 16 * i, meta + t * 64 * NG, 0);
+                        zw[it][t * 4 * NG + 4 * i] = r.x;
+                        zw[it][t * 4 * NG + 4 * i + 1] = r.y;
+                        zw[it][t * 4 * NG + 4 * i + 2] = r.z;
+                        zw[it][t * 4 * NG + 4 * i + 3] = r.w;
+                    }
+            } else {
+#pragma unroll
+                for (int t = 0; t < kTilesOfQuad; ++t) {
+                    const int tt = D == 64 ? t : qi * 4 / NJ;      // key tile
+#pragma unroll
+                    for (int g = 0; g < NG; ++g)
+                        zw[it][t * NG + g] = __builtin_amdgcn_raw_buffer_load_b32(rs, (col * NG + g) * 4, meta + tt * 64 * NG, 0);
+                }
+            }
+        }
+    };
+    auto unpack = [&](int st, int buf) {
+        const h2_t sixteenth = {(_Float16)0.0625f, (_Float16)0.0625f};
+#pragma unroll
+        for (int it = 0; it < IT; ++it) {
+            const int Q = wave + it * RW;
+            const int qq = Q & 3, bi = qq / QB, qi = qq % QB;
+            if (Q < 4) {
+#pragma unroll
+                for (int w = 0; w < 4; ++w) {
+                    const int W = qi * 4 + w, t = W / NJ, j = W % NJ;
+                    const uint32_t word = D == 64 ? zw[it][(w / 2) * NG + (w % 2) / JG] : 0u;
+                    // group of step j; the word's tile is t
+                    uint32_t m = word;
+                    if constexpr (D > 64) {
+                        m = zw[it][0];
+#pragma unroll
+                        for (int g = 1; g < NG; ++g) m = j / JG == g ? zw[it][g] : m;
+                    }
+                    h2_t a4[4];
+                    unpack_zr(code[it][w], zp_pair((m >> 16) & 15u), a4);
+                    kf[buf][bi][t][j][lane] = join(a4);
+                }
+            } else {
+#pragma unroll
+                for (int uu = 0; uu < 2; ++uu) {
+                    const int u = 2 * qi + uu, g = u / JG;
+                    h2_t lo4[4], hi4[4];
+#pragma unroll
+                    for (int w = 0; w < 2; ++w) {
+                        const uint32_t d = code[it][2 * uu + w], d8 = d >> 8;
+                        const uint32_t ml = 0x000F000Fu, mh = 0x00F000F0u, magic = 0x64006400u;
+                        uint32_t z[2];
+#pragma unroll
+                        for (int k = 0; k < 2; ++k) {
+                            uint32_t m0 = zw[it][(4 * w + 2 * k) * NG], m1 = zw[it][(4 * w + 2 * k + 1) * NG];
+#pragma unroll
+                            for (int e = 1; e < NG; ++e) {
+                                m0 = g == e ? zw[it][(4 * w + 2 * k) * NG + e] : m0;
+                                m1 = g == e ? zw[it][(4 * w + 2 * k + 1) * NG + e] : m1;
+                            }
+                            z[k] = __builtin_amdgcn_perm(m1, m0, 0x07060302u);
+                        }
+                        auto zl = [&](uint32_t z2) { return as_h2(__builtin_amdgcn_bitop3_b32(z2, ml, 0xE400E400u, 0xEA)); };
+                        auto zh = [&](uint32_t z2) { return as_h2(__builtin_amdgcn_bitop3_b32(z2 << 4, mh, 0xD400D400u, 0xEA)); };
+                        lo4[2 * w] = as_h2(__builtin_amdgcn_bitop3_b32(d, ml, magic, 0xEA)) + zl(z[0]);
+                        lo4[2 * w + 1] = as_h2(__builtin_amdgcn_bitop3_b32(d8, ml, magic, 0xEA)) + zl(z[1]);
+                        hi4[2 * w] = as_h2(__builtin_amdgcn_bitop3_b32(d, mh, magic, 0xEA)) * sixteenth + zh(z[0]);
+                        hi4[2 * w + 1] = as_h2(__builtin_amdgcn_bitop3_b32(d8, mh, magic, 0xEA)) * sixteenth + zh(z[1]);
+                    }
+                    vf[buf][bi][2 * u][lane] = join(lo4);
+                    vf[buf][bi][2 * u + 1][lane] = join(hi4);
+                }
+            }
+            // the scales: a key quad's lanes of quarter 0 hold their tile's own keys,
+            // a value quad's first column all 32 keys; the first quad of a block that
+            // has a tile writes it
+            if (Q < 4) {
+                if (quarter == 0) {
+#pragma unroll
+                    for (int t = 0; t < kTilesOfQuad; ++t) {
+                        const int tt = D == 64 ? t : qi * 4 / NJ;
+                        if (D == 64 || qi * 4 % NJ == 0) {
+#pragma unroll
+                            for (int g = 0; g < NG; ++g)
+                                ks[buf][bi][g][tt * 16 + col] = scale_of(zw[it][t * NG + g]) * p.scale_log2;
+                        }
+                    }
+                }
+            } else if (qi == 0 && col == 0) {
+#pragma unroll
+                for (int k = 0; k < 8; ++k)
+#pragma unroll
+                    for (int g = 0; g < NG; ++g) {
+                        const uint32_t m = zw[it][k * NG + g];
+                        const int key = (k >> 2) * 16 + 4 * quarter + (k & 3);
+                        vs[buf][bi][g][key] = scale_of(m);
+                        vw[buf][bi][g][key] = m;
+                    }
+            }
+        }
+    };
+
+    auto compute = [&](int buf, int bi, int blk) {
+        // ---- logits ----
+        float x[NR][2][4];
+#pragma unroll
+        for (int t = 0; t < 2; ++t) {
+#pragma unroll
+            for (int g = 0; g < NG; ++g) {
+                const f4_t k4 = *reinterpret_cast<const f4_t*>(&ks[buf][bi][g][t * 16 + 4 * quarter]);
+                f4_t acc[NR];
+#pragma unroll
+                for (int n = 0; n < NR; ++n) acc[n] = f4_t{0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+                for (int jj = 0; jj < JG; ++jj) {
+                    const int j = g * JG + jj;
+                    const h8_t k8 = kf[buf][bi][t][j][lane];
+#pragma unroll
+                    for (int n = 0; n < NR; ++n)
+#pragma unroll
+                        for (int c = 0; c < NQ; ++c) acc[n] = mfma(k8, qf[n][c][j], acc[n]);
+                }
+#pragma unroll
+                for (int n = 0; n < NR; ++n)
+#pragma unroll
+                    for (int i = 0; i < 4; ++i)
+                        x[n][t][i] = g == 0 ? acc[n][i] * k4[i] : __builtin_fmaf(acc[n][i], k4[i], x[n][t][i]);
+            }
+            if constexpr (F32) {
+#pragma unroll
+                for (int n = 0; n < NR; ++n)
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) x[n][t][i] *= qs[n];
+            }
+        }
+        // ---- masks and the running reference ----
+        const bool edge = blk * 32 + 32 > whole || blk * 32 < open;
+        uint32_t seen[NR];
+        float mxs[NR];
+        uint32_t top8[2][4];                   // per key, the largest scale over the groups
+#pragma unroll
+        for (int t = 0; t < 2; ++t) {
+            u4_t w = *reinterpret_cast<const u4_t*>(&vw[buf][bi][0][t * 16 + 4 * quarter]);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) top8[t][i] = w[i];
+#pragma unroll
+            for (int g = 1; g < NG; ++g) {
+                w = *reinterpret_cast<const u4_t*>(&vw[buf][bi][g][t * 16 + 4 * quarter]);
+#pragma unroll
+                for (int i = 0; i < 4; ++i) top8[t][i] = max_halves(top8[t][i], w[i]);
+            }
+        }
+        if (edge) {                            // key by key: a hidden key's scale is not looked at
+#pragma unroll
+            for (int n = 0; n < NR; ++n) {
+                seen[n] = 0;
+                mxs[n] = -__builtin_inff();
+                const int below = p.causal && p.window > 0 ? pos[n] - p.window : -1;
+#pragma unroll
+                for (int k = 0; k < 8; ++k) {
+                    const int key = blk * 32 + (k >> 2) * 16 + 4 * quarter + (k & 3);
+                    float& e = x[n][k >> 2][k & 3];
+                    if (key <= pos[n] && key > below && key < s.len)
+                        seen[n] |= 1u << k;
+                    else
+                        e = -__builtin_inff();
+                    mxs[n] = fmaxf(mxs[n], e + top_exponent(top8[k >> 2][k & 3]));
+                }
+            }
+        } else {
+            uint32_t w = top8[0][0];
+#pragma unroll
+            for (int k = 1; k < 8; ++k) w = max_halves(w, top8[k >> 2][k & 3]);
+            const float top = top_exponent(w);
+#pragma unroll
+            for (int n = 0; n < NR; ++n) {
+                float m = x[n][0][0];
+#pragma unroll
+                for (int k = 1; k < 8; ++k) m = fmaxf(m, x[n][k >> 2][k & 3]);
+                mxs[n] = m + top;
+            }
+        }
+#pragma unroll
+        for (int n = 0; n < NR; ++n) {
+            float mx = mxs[n];
+            if (__builtin_amdgcn_ballot_w64(mx > M[n] + kRaise)) {
+                mx = fmaxf(mx, __shfl_xor(mx, 16));
+                mx = fmaxf(mx, __shfl_xor(mx, 32));
+                const float next = fmaxf(M[n], mx - kBelow);
+                const float alpha = exp2f(M[n] - next);
+                M[n] = next;
+                l[n] *= alpha;
+#pragma unroll
+                for (int t = 0; t < NT; ++t) o[n][t] *= alpha;
+            }
+        }
+        // ---- p ----
+#pragma unroll
+        for (int n = 0; n < NR; ++n)
+#pragma unroll
+            for (int k = 0; k < 8; ++k) {
+                float& e = x[n][k >> 2][k & 3];
+                e = __builtin_amdgcn_exp2f(e - M[n]);
+                l[n] += e;
+            }
+        // ---- O^T += V^T (p s')^T, group by group ----
+#pragma unroll
+        for (int g = 0; g < NG; ++g) {
+            h8_t pb[NR], pl[NR];
+            f4_t v4[2];
+#pragma unroll
+            for (int t = 0; t < 2; ++t) v4[t] = *reinterpret_cast<const f4_t*>(&vs[buf][bi][g][t * 16 + 4 * quarter]);
+            float f[NR][8];
+#pragma unroll
+            for (int n = 0; n < NR; ++n)
+#pragma unroll
+                for (int k = 0; k < 8; ++k) f[n][k] = x[n][k >> 2][k & 3] * v4[k >> 2][k & 3];
+            if (edge) {                        // a hidden key adds nothing whatever its scale is
+#pragma unroll
+                for (int n = 0; n < NR; ++n)
+#pragma unroll
+                    for (int k = 0; k < 8; ++k) f[n][k] = (seen[n] >> k) & 1u ? f[n][k] : 0.0f;
+            }
+#pragma unroll
+            for (int n = 0; n < NR; ++n)
+#pragma unroll
+                for (int k = 0; k < 8; ++k) {
+                    pb[n][k] = (_Float16)f[n][k];
+                    if constexpr (SPLIT) pl[n][k] = (_Float16)(f[n][k] - (float)pb[n][k]);
+                }
+#pragma unroll
+            for (int tt = 0; tt < 2 * JG; ++tt) {
+                const int t = 2 * JG * g + tt;
+                const h8_t v8 = vf[buf][bi][t][lane];
+#pragma unroll
+                for (int n = 0; n < NR; ++n) {
+                    o[n][t] = mfma(v8, pb[n], o[n][t]);
+                    if constexpr (SPLIT) o[n][t] = mfma(v8, pl[n], o[n][t]);
+                }
+            }
+        }
+    };
+
+    if (stages > 0) {
+        request(0);
+        unpack(0, 0);
+        __syncthreads();
+        for (int st = 0; st < stages; ++st) {
+            const int buf = st & 1;
+            if (st + 1 < stages) {
+                // pages of the next stage: refilled before its blocks leave the register
+                if (blk0 + (st + 2) * SB > page0 + 64) {
+                    page0 = blk0 + (st + 1) * SB;
+                    pages = pages_from(v, table, page0, 1, lane);
+                }
+                request(st + 1);
+            }
+            if (busy) {
+#pragma unroll
+                for (int bi = 0; bi < SB; ++bi) {
+                    const int blk = blk0 + st * SB + bi;
+                    if (blk < blk1 && blk * 32 < none) compute(buf, bi, blk);
+                }
+            }
+            if (st + 1 < stages) unpack(st + 1, buf ^ 1);
+            __syncthreads();
+        }
+    }
+
+#pragma unroll
+    for (int n = 0; n < NR; ++n) {
+        l[n] += __shfl_xor(l[n], 16);
+        l[n] += __shfl_xor(l[n], 32);
+        if (out_row[n] < 0) continue;
+        if (p.splits == 1) {
+            const float inv = l[n] == 0.0f ? 0.0f : 1.0f / l[n];   // a row that sees nothing gives zeros
+            T* out = static_cast<T*>(p.out) + out_row[n] * D + 4 * quarter;
+#pragma unroll
+            for (int t = 0; t < NT; ++t) store4(out + 16 * t, o[n][t], inv);
+            if (p.lse && quarter == 0) p.lse[out_row[n]] = log_sum(M[n], l[n]);
+        } else {
+            const int64_t at = (int64_t)split * v.tokens * v.q_heads + out_row[n];
+            float* part = p.part_o + at * D + 4 * quarter;
+#pragma unroll
+            for (int t = 0; t < NT; ++t) *reinterpret_cast<f4_t*>(part + 16 * t) = o[n][t];
+            if (quarter == 0) {
+                p.part_ml[2 * at] = M[n];
+                p.part_ml[2 * at + 1] = l[n];
+            }
+        }
+    }
+}
+
+template <int D, int NG, bool F32> hipError_t launch_waves(const AttnParams& p, const Plan& c, hipStream_t s)
+{
+    constexpr int NR = D == 256 ? 1 : 2;
+    const dim3 grid((unsigned)(p.v.kv_heads * c.splits * c.row_tiles), (unsigned)p.v.batch);
+    if (c.waves == 8) kv4_prompt_kernel<D, NG, F32, NR, 8><<<grid, dim3(512), 0, s>>>(p);
+    else kv4_prompt_kernel<D, NG, F32, NR, 4><<<grid, dim3(256), 0, s>>>(p);
+    return hipGetLastError();
+}
+
+template <int D, int NG> hipError_t launch_type(const AttnParams& p, const Plan& c, int f16, hipStream_t s)
+{
+    return f16 ? launch_waves<D, NG, false>(p, c, s) : launch_waves<D, NG, true>(p, c, s);
+}
+
+}  // namespace
+
+hipError_t launch_prompt(const AttnParams& p, const Plan& c, int f16, hipStream_t s)
+{
+    const int ng = p.v.groups;
+    switch (p.v.head_dim) {
+    case 64: return ng == 1 ? launch_type<64, 1>(p, c, f16, s) : launch_type<64, 2>(p, c, f16, s);
+    case 128:
+        return ng == 1 ? launch_type<128, 1>(p, c, f16, s)
+                       : ng == 2 ? launch_type<128, 2>(p, c, f16, s) : launch_type<128, 4>(p, c, f16, s);
+    default:
+        return ng == 2 ? launch_type<256, 2>(p, c, f16, s)
+                       : ng == 4 ? launch_type<256, 4>(p, c, f16, s) : launch_type<256, 8>(p, c, f16, s);
+    }
+}
+
+}  // namespace kv4
+}  // namespace mnb
