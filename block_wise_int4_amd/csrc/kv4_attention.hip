@@ -583,7 +583,7 @@ Plan plan_of(const AttentionArgs& a)
         c.kind = 2;
         c.waves = 8;
         const int64_t wgs = (rows + prompt_rows(a.v.head_dim, 8) - 1) / prompt_rows(a.v.head_dim, 8) * a.v.kv_heads * a.v.batch;
-        if (wgs < 512) c.waves = 4;            // two smaller workgroups a CU
+        if (wgs < 512 && a.v.groups == 1) c.waves = 4;   // two smaller workgroups a CU
         c.rows = prompt_rows(a.v.head_dim, c.waves);
         least = 256;
         want = 256;

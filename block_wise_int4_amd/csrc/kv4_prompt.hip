@@ -5,11 +5,13 @@
 // A workgroup of RW waves holds RW x 16 NR rows; its waves unpack a stage of
 // 8192 / D keys together, once, into fp16 fragments in LDS, and every wave reads
 // all of them as its A operands.  (Unpacked by each wave for itself, the codes
-// cost as many vector instructions as the softmax.)  The next stage's codes are
-// requested before a stage's products and unpacked into the other half of LDS
-// after them, so there is one barrier a stage.  What is left in the vector
-// units is the softmax, about 8 instructions' time per (row, key), half of it
-// the exponential; the matrix cores run beside it in the other wave of the SIMD.
+// cost as many vector instructions as the softmax.)
+//
+// The next stage's codes are requested a stage ahead and unpacked into the other
+// half of LDS, so there is one barrier a stage.  With two waves a SIMD (the
+// registers allow no more) the kernel is bound by the latencies inside a wave, so a wave takes up
+// to 64 keys through its softmax at once: one look at the masks, one at the running
+// reference, and long runs of independent products and exponentials.
 #include "kv4_attention.hpp"
 
 namespace mnb {
@@ -29,11 +31,14 @@ __global__ __launch_bounds__(RW * 64, 2) void kv4_prompt_kernel(AttnParams p)
     constexpr int IT = 8 / RW;                         // quads a wave unpacks: 4 of keys, 4 of values in all
     static_assert(SB * QB == 4, "four quads of each a stage");
 
-    __shared__ __align__(16) h8_t kf[2][SB][2][NJ][64];    // key fragments: tile, 32-dim step, lane
-    __shared__ __align__(16) h8_t vf[2][SB][NT][64];       // value fragments: 16-dim tile, lane
-    __shared__ __align__(16) float ks[2][SB][NG][32];      // scale * key scale, in log2 units
-    __shared__ __align__(16) float vs[2][SB][NG][32];
-    __shared__ __align__(16) uint32_t vw[2][SB][NG][32];   // value scale words (exponents)
+    // Stages in LDS: half of them in use, half being filled.  One barrier serves
+    // EP stages.
+    constexpr int EP = RW == 8 ? 2 : 1, NB = 2 * EP;
+    __shared__ __align__(16) h8_t kf[NB][SB][2][NJ][64];    // key fragments: tile, 32-dim step, lane
+    __shared__ __align__(16) h8_t vf[NB][SB][NT][64];       // value fragments: 16-dim tile, lane
+    __shared__ __align__(16) float ks[NB][SB][NG][32];      // scale * key scale, in log2 units
+    __shared__ __align__(16) float vs[NB][SB][NG][32];
+    __shared__ float vtop[NB][SB];                          // a block's largest value scale, as its exponent
 
     const KvView& v = p.v;
     const int lane = threadIdx.x & 63;
@@ -91,6 +96,7 @@ __global__ __launch_bounds__(RW * 64, 2) void kv4_prompt_kernel(AttnParams p)
         none = s.len - s.count + wlast / p.gqa + 1;
         if (p.window > 0) open = s.len - s.count + wlast / p.gqa - p.window + 1;
     }
+    whole = whole < to ? whole : to;           // past the split's end LDS holds zeros
 
     f4_t o[NR][NT];
     float M[NR], l[NR];
@@ -147,7 +153,7 @@ __global__ __launch_bounds__(RW * 64, 2) void kv4_prompt_kernel(AttnParams p)
             }
         }
     };
-    auto unpack = [&](int st, int buf) {
+    auto unpack = [&](int buf) {
         const h2_t sixteenth = {(_Float16)0.0625f, (_Float16)0.0625f};
 #pragma unroll
         for (int it = 0; it < IT; ++it) {
@@ -215,184 +221,208 @@ __global__ __launch_bounds__(RW * 64, 2) void kv4_prompt_kernel(AttnParams p)
                         }
                     }
                 }
-            } else if (qi == 0 && col == 0) {
+            } else if (qi == 0) {
+                uint32_t most = zw[it][0];
 #pragma unroll
-                for (int k = 0; k < 8; ++k)
+                for (int k = 1; k < 8 * NG; ++k) most = max_halves(most, zw[it][k]);
+                most = max_halves(most, (uint32_t)__shfl_xor((int)most, 16));
+                most = max_halves(most, (uint32_t)__shfl_xor((int)most, 32));
+                if (lane == 0) vtop[buf][bi] = top_exponent(most);
+                if (col == 0) {
 #pragma unroll
-                    for (int g = 0; g < NG; ++g) {
-                        const uint32_t m = zw[it][k * NG + g];
-                        const int key = (k >> 2) * 16 + 4 * quarter + (k & 3);
-                        vs[buf][bi][g][key] = scale_of(m);
-                        vw[buf][bi][g][key] = m;
-                    }
+                    for (int k = 0; k < 8; ++k)
+#pragma unroll
+                        for (int g = 0; g < NG; ++g)
+                            vs[buf][bi][g][(k >> 2) * 16 + 4 * quarter + (k & 3)] = scale_of(zw[it][k * NG + g]);
+                }
             }
         }
     };
 
-    auto compute = [&](int buf, int bi, int blk) {
-        // ---- logits ----
-        float x[NR][2][4];
+    // KB blocks from b0 of a stage; the first is block blk of the sequence.
+    constexpr int KB = SB < 2 || NG >= 4 || (F32 && NG > 1) ? 1 : 2;   // two where the registers hold them
+    auto compute = [&](int buf, int b0, int blk) {
+        // ---- logits less M, 32 KB keys by 16 NR rows ----
+        float y[NR][8 * KB], Mu[NR];
 #pragma unroll
-        for (int t = 0; t < 2; ++t) {
+        for (int n = 0; n < NR; ++n) Mu[n] = M[n] == kLow ? 0.0f : M[n];
+#pragma unroll
+        for (int t = 0; t < 2 * KB; ++t) {
+            const int bi = b0 + t / 2;
 #pragma unroll
             for (int g = 0; g < NG; ++g) {
-                const f4_t k4 = *reinterpret_cast<const f4_t*>(&ks[buf][bi][g][t * 16 + 4 * quarter]);
                 f4_t acc[NR];
 #pragma unroll
                 for (int n = 0; n < NR; ++n) acc[n] = f4_t{0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
                 for (int jj = 0; jj < JG; ++jj) {
                     const int j = g * JG + jj;
-                    const h8_t k8 = kf[buf][bi][t][j][lane];
+                    const h8_t k8 = kf[buf][bi][t % 2][j][lane];
 #pragma unroll
                     for (int n = 0; n < NR; ++n)
 #pragma unroll
                         for (int c = 0; c < NQ; ++c) acc[n] = mfma(k8, qf[n][c][j], acc[n]);
                 }
+                const f4_t k4 = *reinterpret_cast<const f4_t*>(&ks[buf][bi][g][t % 2 * 16 + 4 * quarter]);
 #pragma unroll
                 for (int n = 0; n < NR; ++n)
 #pragma unroll
-                    for (int i = 0; i < 4; ++i)
-                        x[n][t][i] = g == 0 ? acc[n][i] * k4[i] : __builtin_fmaf(acc[n][i], k4[i], x[n][t][i]);
-            }
-            if constexpr (F32) {
-#pragma unroll
-                for (int n = 0; n < NR; ++n)
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) x[n][t][i] *= qs[n];
-            }
-        }
-        // ---- masks and the running reference ----
-        const bool edge = blk * 32 + 32 > whole || blk * 32 < open;
-        uint32_t seen[NR];
-        float mxs[NR];
-        uint32_t top8[2][4];                   // per key, the largest scale over the groups
-#pragma unroll
-        for (int t = 0; t < 2; ++t) {
-            u4_t w = *reinterpret_cast<const u4_t*>(&vw[buf][bi][0][t * 16 + 4 * quarter]);
-#pragma unroll
-            for (int i = 0; i < 4; ++i) top8[t][i] = w[i];
-#pragma unroll
-            for (int g = 1; g < NG; ++g) {
-                w = *reinterpret_cast<const u4_t*>(&vw[buf][bi][g][t * 16 + 4 * quarter]);
-#pragma unroll
-                for (int i = 0; i < 4; ++i) top8[t][i] = max_halves(top8[t][i], w[i]);
+                    for (int i = 0; i < 4; ++i) {
+                        float& e = y[n][4 * t + i];
+                        // fp32 queries come back to their scale last, with M
+                        const float add = g == 0 ? (F32 ? 0.0f : -Mu[n]) : e;
+                        e = __builtin_fmaf(acc[n][i], k4[i], add);
+                        if (F32 && g == NG - 1) e = __builtin_fmaf(e, qs[n], -Mu[n]);
+                    }
             }
         }
-        if (edge) {                            // key by key: a hidden key's scale is not looked at
+        // ---- masks: a hidden key's logit is -infinity ----
+        const bool edge = (blk + KB) * 32 > whole || blk * 32 < open;
+        uint32_t seen[NR];                     // bit 4 t + i: the row sees the key
+        if (edge) {
 #pragma unroll
             for (int n = 0; n < NR; ++n) {
-                seen[n] = 0;
-                mxs[n] = -__builtin_inff();
                 const int below = p.causal && p.window > 0 ? pos[n] - p.window : -1;
+                seen[n] = 0;
 #pragma unroll
-                for (int k = 0; k < 8; ++k) {
+                for (int k = 0; k < 8 * KB; ++k) {
                     const int key = blk * 32 + (k >> 2) * 16 + 4 * quarter + (k & 3);
-                    float& e = x[n][k >> 2][k & 3];
-                    if (key <= pos[n] && key > below && key < s.len)
-                        seen[n] |= 1u << k;
-                    else
-                        e = -__builtin_inff();
-                    mxs[n] = fmaxf(mxs[n], e + top_exponent(top8[k >> 2][k & 3]));
+                    const bool ok = key <= pos[n] && key > below && key < to;
+                    seen[n] |= ok ? 1u << k : 0u;
+                    y[n][k] = ok ? y[n][k] : -__builtin_inff();
                 }
             }
-        } else {
-            uint32_t w = top8[0][0];
-#pragma unroll
-            for (int k = 1; k < 8; ++k) w = max_halves(w, top8[k >> 2][k & 3]);
-            const float top = top_exponent(w);
-#pragma unroll
-            for (int n = 0; n < NR; ++n) {
-                float m = x[n][0][0];
-#pragma unroll
-                for (int k = 1; k < 8; ++k) m = fmaxf(m, x[n][k >> 2][k & 3]);
-                mxs[n] = m + top;
-            }
         }
+        // ---- the running reference ----
+        float top = vtop[buf][b0];
+        if (KB > 1) top = fmaxf(top, vtop[buf][b0 + KB - 1]);
+        float mx[NR];
+        bool raise = false;
 #pragma unroll
         for (int n = 0; n < NR; ++n) {
-            float mx = mxs[n];
-            if (__builtin_amdgcn_ballot_w64(mx > M[n] + kRaise)) {
-                mx = fmaxf(mx, __shfl_xor(mx, 16));
-                mx = fmaxf(mx, __shfl_xor(mx, 32));
-                const float next = fmaxf(M[n], mx - kBelow);
-                const float alpha = exp2f(M[n] - next);
-                M[n] = next;
+            mx[n] = y[n][0];
+#pragma unroll
+            for (int k = 1; k < 8 * KB; ++k) mx[n] = fmaxf(mx[n], y[n][k]);
+            raise |= mx[n] + top > kRaise || (M[n] == kLow && mx[n] > -__builtin_inff());
+        }
+        if (__builtin_amdgcn_ballot_w64(raise)) {
+            if (edge) {                        // key by key: a hidden key's scale is not looked at
+#pragma unroll
+                for (int n = 0; n < NR; ++n) mx[n] = -__builtin_inff();
+                for (int k = 0; k < 8 * KB; ++k) {
+                    uint32_t most = 0;         // an fp32 scale's exponent, as top_exponent has it
+#pragma unroll
+                    for (int g = 0; g < NG; ++g) {
+                        const uint32_t w = __builtin_bit_cast(uint32_t, vs[buf][b0 + (k >> 3)][g][((k >> 2) & 1) * 16 + 4 * quarter + (k & 3)]);
+                        most = w > most ? w : most;
+                    }
+                    const float e = fminf(fmaxf((float)((int)(most >> 23) - 126), -14.0f), 17.0f);
+#pragma unroll
+                    for (int n = 0; n < NR; ++n) {
+                        float yk = y[n][0];
+#pragma unroll
+                        for (int q = 1; q < 8 * KB; ++q) yk = k == q ? y[n][q] : yk;
+                        mx[n] = fmaxf(mx[n], yk + e);
+                    }
+                }
+            } else {
+#pragma unroll
+                for (int n = 0; n < NR; ++n) mx[n] += top;
+            }
+#pragma unroll
+            for (int n = 0; n < NR; ++n) {
+                mx[n] = fmaxf(mx[n], __shfl_xor(mx[n], 16));
+                mx[n] = fmaxf(mx[n], __shfl_xor(mx[n], 32));
+                const bool first = M[n] == kLow;
+                const bool move = first ? mx[n] > -__builtin_inff() : mx[n] > kRaise;
+                const float next = move ? Mu[n] + mx[n] - kBelow : Mu[n];
+                const float alpha = first ? 1.0f : exp2f(Mu[n] - next);   // nothing was summed before the first
+                const float by = next - Mu[n];
+                M[n] = move ? next : M[n];
                 l[n] *= alpha;
 #pragma unroll
                 for (int t = 0; t < NT; ++t) o[n][t] *= alpha;
+#pragma unroll
+                for (int k = 0; k < 8 * KB; ++k) y[n][k] -= by;
             }
         }
         // ---- p ----
 #pragma unroll
         for (int n = 0; n < NR; ++n)
 #pragma unroll
-            for (int k = 0; k < 8; ++k) {
-                float& e = x[n][k >> 2][k & 3];
-                e = __builtin_amdgcn_exp2f(e - M[n]);
-                l[n] += e;
+            for (int k = 0; k < 8 * KB; ++k) {
+                y[n][k] = __builtin_amdgcn_exp2f(y[n][k]);
+                l[n] += y[n][k];
             }
-        // ---- O^T += V^T (p s')^T, group by group ----
+        // ---- O^T += V^T (p s')^T, block by block and group by group ----
 #pragma unroll
-        for (int g = 0; g < NG; ++g) {
-            h8_t pb[NR], pl[NR];
-            f4_t v4[2];
+        for (int kb = 0; kb < KB; ++kb) {
 #pragma unroll
-            for (int t = 0; t < 2; ++t) v4[t] = *reinterpret_cast<const f4_t*>(&vs[buf][bi][g][t * 16 + 4 * quarter]);
-            float f[NR][8];
+            for (int g = 0; g < NG; ++g) {
+                h8_t pb[NR], pl[NR];
+                float f[NR][8];
 #pragma unroll
-            for (int n = 0; n < NR; ++n)
+                for (int t = 0; t < 2; ++t) {
+                    const f4_t v4 = *reinterpret_cast<const f4_t*>(&vs[buf][b0 + kb][g][t * 16 + 4 * quarter]);
 #pragma unroll
-                for (int k = 0; k < 8; ++k) f[n][k] = x[n][k >> 2][k & 3] * v4[k >> 2][k & 3];
-            if (edge) {                        // a hidden key adds nothing whatever its scale is
+                    for (int n = 0; n < NR; ++n)
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) f[n][4 * t + i] = y[n][8 * kb + 4 * t + i] * v4[i];
+                }
+                if (edge) {                    // a hidden key adds nothing whatever its scale is
+#pragma unroll
+                    for (int n = 0; n < NR; ++n)
+#pragma unroll
+                        for (int k = 0; k < 8; ++k) f[n][k] = (seen[n] >> (8 * kb + k)) & 1u ? f[n][k] : 0.0f;
+                }
 #pragma unroll
                 for (int n = 0; n < NR; ++n)
 #pragma unroll
-                    for (int k = 0; k < 8; ++k) f[n][k] = (seen[n] >> k) & 1u ? f[n][k] : 0.0f;
-            }
+                    for (int k = 0; k < 8; ++k) {
+                        pb[n][k] = (_Float16)f[n][k];
+                        if constexpr (SPLIT) pl[n][k] = (_Float16)(f[n][k] - (float)pb[n][k]);
+                    }
 #pragma unroll
-            for (int n = 0; n < NR; ++n)
+                for (int tt = 0; tt < 2 * JG; ++tt) {
+                    const int t = 2 * JG * g + tt;
+                    const h8_t v8 = vf[buf][b0 + kb][t][lane];
 #pragma unroll
-                for (int k = 0; k < 8; ++k) {
-                    pb[n][k] = (_Float16)f[n][k];
-                    if constexpr (SPLIT) pl[n][k] = (_Float16)(f[n][k] - (float)pb[n][k]);
-                }
-#pragma unroll
-            for (int tt = 0; tt < 2 * JG; ++tt) {
-                const int t = 2 * JG * g + tt;
-                const h8_t v8 = vf[buf][bi][t][lane];
-#pragma unroll
-                for (int n = 0; n < NR; ++n) {
-                    o[n][t] = mfma(v8, pb[n], o[n][t]);
-                    if constexpr (SPLIT) o[n][t] = mfma(v8, pl[n], o[n][t]);
+                    for (int n = 0; n < NR; ++n) {
+                        o[n][t] = mfma(v8, pb[n], o[n][t]);
+                        if constexpr (SPLIT) o[n][t] = mfma(v8, pl[n], o[n][t]);
+                    }
                 }
             }
         }
     };
 
+    auto ask = [&](int st) {
+        // pages of the blocks to request: refilled before they leave the register
+        if (blk0 + (st + 1) * SB > page0 + 64) {
+            page0 = blk0 + st * SB;
+            pages = pages_from(v, table, page0, 1, lane);
+        }
+        request(st);
+    };
     if (stages > 0) {
         request(0);
-        unpack(0, 0);
+#pragma unroll
+        for (int i = 0; i < EP; ++i) {
+            unpack(i);                         // past the end: the last codes again, unused
+            if (i + 1 < stages) ask(i + 1);
+        }
         __syncthreads();
         for (int st = 0; st < stages; ++st) {
-            const int buf = st & 1;
-            if (st + 1 < stages) {
-                // pages of the next stage: refilled before its blocks leave the register
-                if (blk0 + (st + 2) * SB > page0 + 64) {
-                    page0 = blk0 + (st + 1) * SB;
-                    pages = pages_from(v, table, page0, 1, lane);
-                }
-                request(st + 1);
-            }
-            if (busy) {
+            const int buf = st & (NB - 1);
 #pragma unroll
-                for (int bi = 0; bi < SB; ++bi) {
-                    const int blk = blk0 + st * SB + bi;
-                    if (blk < blk1 && blk * 32 < none) compute(buf, bi, blk);
-                }
+            for (int b0 = 0; b0 < SB; b0 += KB) {
+                const int blk = blk0 + st * SB + b0;
+                // blocks past the end hold zeros and are masked
+                if (busy && blk < blk1 && blk * 32 < none) compute(buf, b0, blk);
             }
-            if (st + 1 < stages) unpack(st + 1, buf ^ 1);
-            __syncthreads();
+            if (st + EP < stages) unpack((st + EP) & (NB - 1));
+            if (st + EP + 1 < stages) ask(st + EP + 1);
+            if (EP == 1 || (st & (EP - 1)) == EP - 1) __syncthreads();
         }
     }
 
@@ -424,8 +454,14 @@ template <int D, int NG, bool F32> hipError_t launch_waves(const AttnParams& p, 
 {
     constexpr int NR = D == 256 ? 1 : 2;
     const dim3 grid((unsigned)(p.v.kv_heads * c.splits * c.row_tiles), (unsigned)p.v.batch);
-    if (c.waves == 8) kv4_prompt_kernel<D, NG, F32, NR, 8><<<grid, dim3(512), 0, s>>>(p);
-    else kv4_prompt_kernel<D, NG, F32, NR, 4><<<grid, dim3(256), 0, s>>>(p);
+    // four waves unpack twice as much each: with one group only, where the registers hold it
+    if constexpr (NG == 1) {
+        if (c.waves == 4) {
+            kv4_prompt_kernel<D, NG, F32, NR, 4><<<grid, dim3(256), 0, s>>>(p);
+            return hipGetLastError();
+        }
+    }
+    kv4_prompt_kernel<D, NG, F32, NR, 8><<<grid, dim3(512), 0, s>>>(p);
     return hipGetLastError();
 }
 
