@@ -581,10 +581,12 @@ Plan plan_of(const AttentionArgs& a)
         want = 2048;
     } else {
         c.kind = 2;
-        c.waves = 8;
-        const int64_t wgs = (rows + prompt_rows(a.v.head_dim, 8) - 1) / prompt_rows(a.v.head_dim, 8) * a.v.kv_heads * a.v.batch;
-        if (wgs < 512 && a.v.groups == 1) c.waves = 4;   // two smaller workgroups a CU
-        c.rows = prompt_rows(a.v.head_dim, c.waves);
+        // two column tiles a wave where that leaves a workgroup for every CU: 1000
+        // rows of 32 heads 45 us with two, XX with one; 2048 tokens by 4 heads
+        // of 8 groups 233 with two, XX with one
+        const int64_t wgs = (rows + 255) / 256 * a.v.kv_heads * a.v.batch;
+        c.tiles = wide || wgs < 256 ? 1 : 2;
+        c.rows = kPromptWaves * 16 * c.tiles;
         least = 256;
         want = 256;
     }

@@ -38,15 +38,14 @@ struct AttnParams {
 struct Plan {
     int kind;                         // 0: one workgroup a row set; 1: few rows; 2: many rows
     int group;                        // few rows: column groups (4, 2, 1), 0 for two row tiles
-    int waves;                        // many rows: waves of a workgroup
+    int tiles;                        // many rows: column tiles of a wave
     int rows;                         // rows per workgroup
     int row_tiles, splits, chunk;
 };
 
 hipError_t launch_prompt(const AttnParams& p, const Plan& c, int f16, hipStream_t s);
 hipError_t launch_join(const AttnParams& p, int f16, hipStream_t s);
-// Rows of a workgroup of `waves` waves of the many-rows kernel.
-inline int prompt_rows(int head_dim, int waves) { return waves * (head_dim == 256 ? 16 : 32); }
+constexpr int kPromptWaves = 8;
 
 typedef uint16_t us2_t __attribute__((ext_vector_type(2)));
 

@@ -33,7 +33,7 @@ __global__ __launch_bounds__(RW * 64, 2) void kv4_prompt_kernel(AttnParams p)
 
     // Stages in LDS: half of them in use, half being filled.  One barrier serves
     // EP stages.
-    constexpr int EP = RW == 8 ? 2 : 1, NB = 2 * EP;
+    constexpr int EP = 2, NB = 2 * EP;
     __shared__ __align__(16) h8_t kf[NB][SB][2][NJ][64];    // key fragments: tile, 32-dim step, lane
     __shared__ __align__(16) h8_t vf[NB][SB][NT][64];       // value fragments: 16-dim tile, lane
     __shared__ __align__(16) float ks[NB][SB][NG][32];      // scale * key scale, in log2 units
@@ -422,7 +422,7 @@ __global__ __launch_bounds__(RW * 64, 2) void kv4_prompt_kernel(AttnParams p)
             }
             if (st + EP < stages) unpack((st + EP) & (NB - 1));
             if (st + EP + 1 < stages) ask(st + EP + 1);
-            if (EP == 1 || (st & (EP - 1)) == EP - 1) __syncthreads();
+            if ((st & (EP - 1)) == EP - 1) __syncthreads();
         }
     }
 
@@ -450,24 +450,22 @@ __global__ __launch_bounds__(RW * 64, 2) void kv4_prompt_kernel(AttnParams p)
     }
 }
 
-template <int D, int NG, bool F32> hipError_t launch_waves(const AttnParams& p, const Plan& c, hipStream_t s)
+template <int D, int NG, bool F32> hipError_t launch_tiles(const AttnParams& p, const Plan& c, hipStream_t s)
 {
-    constexpr int NR = D == 256 ? 1 : 2;
     const dim3 grid((unsigned)(p.v.kv_heads * c.splits * c.row_tiles), (unsigned)p.v.batch);
-    // four waves unpack twice as much each: with one group only, where the registers hold it
-    if constexpr (NG == 1) {
-        if (c.waves == 4) {
-            kv4_prompt_kernel<D, NG, F32, NR, 4><<<grid, dim3(256), 0, s>>>(p);
+    if constexpr (D < 256) {
+        if (c.tiles == 2) {
+            kv4_prompt_kernel<D, NG, F32, 2, kPromptWaves><<<grid, dim3(kPromptWaves * 64), 0, s>>>(p);
             return hipGetLastError();
         }
     }
-    kv4_prompt_kernel<D, NG, F32, NR, 8><<<grid, dim3(512), 0, s>>>(p);
+    kv4_prompt_kernel<D, NG, F32, 1, kPromptWaves><<<grid, dim3(kPromptWaves * 64), 0, s>>>(p);
     return hipGetLastError();
 }
 
 template <int D, int NG> hipError_t launch_type(const AttnParams& p, const Plan& c, int f16, hipStream_t s)
 {
-    return f16 ? launch_waves<D, NG, false>(p, c, s) : launch_waves<D, NG, true>(p, c, s);
+    return f16 ? launch_tiles<D, NG, false>(p, c, s) : launch_tiles<D, NG, true>(p, c, s);
 }
 
 }  // namespace
