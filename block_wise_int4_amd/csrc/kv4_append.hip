@@ -9,21 +9,22 @@
 // that holds a NaN or an infinity, or whose scale passes fp16, gets s = NaN or
 // infinity and reads back as NaN.
 //
-// The work is one (token, head) to head_dim / 8 lanes, 8 values a lane: a
-// lane's 8 key codes are one word of the layout, and its 8 value codes are 8
-// bytes once the lane two over has lent its nibbles (a value byte holds two
-// dims of one token, so no byte is shared between tokens and nothing is read
-// back).  Every token is independent; the kernel is bound by the latency of
-// q_start -> kv_len -> page table at one token per sequence, and by its
-// traffic for prompts.
+// A workgroup takes one token: its sequence, position and page are found once,
+// in scalar registers, and cos and sin are loaded once.  head_dim / 8 lanes take a
+// head, 8 values a lane, and go through the heads in turn: a lane's 8 key codes
+// are one word of the layout, and its 8 value codes are 8 bytes once the lane two
+// over has lent its nibbles (a value byte holds two dims of one token, so no
+// byte is shared between tokens and nothing is read back).
+//
+// Few tokens are bound by the chain q_start -> kv_len -> page table -> store, and
+// get a lane group for every head; many by their traffic, most of it the
+// queries' and the activations' own.
 #include "mnb_device.hpp"
 #include "mnb_kv4.hpp"
 
 namespace mnb {
 
 namespace {
-
-constexpr int kThreads = 256;
 
 // 8 consecutive elements as fp32, at any element alignment
 __device__ __forceinline__ void load8(const _Float16* p, float* f)
@@ -59,42 +60,37 @@ __device__ __forceinline__ void store8(float* p, const float* f)
     *reinterpret_cast<raw*>(p + 4) = raw{f[4], f[5], f[6], f[7]};
 }
 
-// The sequence of a token, searched by LPR adjacent lanes together: each
-// round compares LPR spread offsets and keeps one LPR-th of the range.
-// Returns the number of sequences whose tokens all come before it (batch
-// when the token is past the last).
-template <int LPR>
-__device__ __forceinline__ int find_sequence(const int32_t* q_start, int batch, int token, int l)
+// The sequence of a token, searched by the wave: each round compares 64 spread
+// offsets and keeps one 64th of the range.  Returns the number of sequences
+// whose tokens all come before it (batch when the token is past the last).
+__device__ __forceinline__ int find_sequence(const int32_t* q_start, int batch, int token, int lane)
 {
     int lo = 0, n = batch;
     while (n > 0) {
-        const int step = (n + LPR - 1) / LPR;
-        const int at = lo + (l + 1) * step;          // ends of sequences lo .. at - 1
-        const int end = lo + n;
-        int before = at <= end && q_start[at <= batch ? at : batch] <= token ? 1 : 0;
-#pragma unroll
-        for (int off = 1; off < LPR; off <<= 1) before += __shfl_xor(before, off);
-        lo += before * step;
-        n = step == 1 ? 0 : (end - lo < step - 1 ? end - lo : step - 1);
+        const int step = (n + 63) / 64;
+        const int at = lo + (lane + 1) * step;       // ends of sequences lo .. at - 1
+        const bool before = at <= lo + n && q_start[at <= batch ? at : batch] <= token;
+        const int left = lo + n;
+        lo += __builtin_popcountll(__builtin_amdgcn_ballot_w64(before)) * step;
+        n = left - lo < step - 1 ? left - lo : step - 1;
     }
-    return lo;
+    return uniform(lo);
 }
 
 struct Place {
     int64_t pos;              // position in the sequence, < 0: none
-    unsigned char* block;     // NULL: no page
+    unsigned char* page;      // block of head 0 in its page; NULL: no page
     int key;                  // token's place in its block
 };
 
-// Position of a token and the block of its page that holds head h.  Page
-// numbers and positions outside their ranges give no block.
-template <int LPR>
-__device__ __forceinline__ Place place_of(const KvView& v, int token, int h, int64_t block_bytes, int l)
+// Where a token of the workgroup is kept.  Page numbers and positions outside
+// their ranges give no page.
+__device__ __forceinline__ Place place_of(const KvView& v, int token, int64_t block_bytes)
 {
     Place r{-1, nullptr, 0};
     int b = token, behind = 1;    // tokens of the sequence from this one on
     if (v.q_start) {
-        b = find_sequence<LPR>(v.q_start, v.batch, token, l);
+        b = find_sequence(v.q_start, v.batch, token, threadIdx.x & 63);
         if (b < v.batch) behind = v.q_start[b + 1] - token;
     }
     if (b >= v.batch) return r;
@@ -106,7 +102,7 @@ __device__ __forceinline__ Place place_of(const KvView& v, int token, int h, int
     if (page < 0 || page >= v.num_pages) return r;
     const int in_page = (int)(r.pos & ((1 << v.page_shift) - 1));
     const int nblk = 1 << (v.page_shift - 5);
-    r.block = v.cache + (((int64_t)page * v.kv_heads + h) * nblk + (in_page >> 5)) * block_bytes;
+    r.page = v.cache + ((int64_t)page * v.kv_heads * nblk + (in_page >> 5)) * block_bytes;
     r.key = in_page & 31;
     return r;
 }
@@ -124,66 +120,13 @@ template <int LPR> __device__ __forceinline__ int value_byte_at(int key, int l) 
            ((i & 1) * 2 + (i >> 1));
 }
 
-template <typename T, int LPR>
-__global__ __launch_bounds__(kThreads) void kv4_append_kernel(AppendArgs a)
+// The 8 values of a lane to codes, and the codes, scale and zero point of its
+// group into a block.  The lanes of a head come together.
+template <int LPR>
+__device__ __forceinline__ void store_head(const float* x, unsigned char* block, int key, bool is_v, int l, int NG, int GL)
 {
 #pragma clang fp contract(off)
     constexpr int D = 8 * LPR;
-    const KvView& v = a.v;
-    const int l = threadIdx.x % LPR;
-    const int hq = a.q ? v.q_heads : 0;
-    const int items = hq + 2 * v.kv_heads;
-    const int64_t id = (int64_t)blockIdx.x * (kThreads / LPR) + threadIdx.x / LPR;
-    const int token = (int)(id / items);
-    if (token >= v.tokens) return;               // whole lane groups
-    const int item = (int)(id % items);
-    const bool is_q = item < hq, is_v = item >= hq + v.kv_heads;
-    const int h = is_q ? item : is_v ? item - hq - v.kv_heads : item - hq;
-    const int NG = v.groups, GL = LPR / NG;      // lanes of a group
-
-    const T* src = is_q ? static_cast<const T*>(a.q) + token * a.q_stride
-                        : is_v ? static_cast<const T*>(a.val) + token * a.v_stride
-                               : static_cast<const T*>(a.k) + token * a.k_stride;
-    src += (int64_t)h * D;
-    const int rot = is_v || !a.cos ? 0 : a.rotary_dim;
-    const int d0 = 8 * l;
-    const bool turn = d0 < rot;
-    float x[8], y[8];
-    load8(src + d0, x);
-    const int half = rot >> 1;
-    const bool second = !a.interleaved && d0 >= half;
-    if (turn && !a.interleaved) load8(src + (second ? d0 - half : d0 + half), y);
-
-    const Place at = place_of<LPR>(v, token, is_q ? 0 : h, kv_block_bytes(D, NG), l);
-    if (turn) {
-        int64_t row = at.pos < 0 ? 0 : at.pos;
-        row = row < a.rope_rows ? row : a.rope_rows - 1;
-        if (a.interleaved) {
-            const float* c = a.cos + row * half + (d0 >> 1);
-            const float* s = a.sin + row * half + (d0 >> 1);
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                const float e = x[2 * i], o = x[2 * i + 1];
-                x[2 * i] = e * c[i] - o * s[i];
-                x[2 * i + 1] = o * c[i] + e * s[i];
-            }
-        } else {
-            const int j = second ? d0 - half : d0;
-            float c[8], s[8];
-            load8(a.cos + row * half + j, c);
-            load8(a.sin + row * half + j, s);
-#pragma unroll
-            for (int i = 0; i < 8; ++i) {
-                const float p = x[i] * c[i], t = y[i] * s[i];
-                x[i] = second ? p + t : p - t;
-            }
-        }
-    }
-    if (is_q) {
-        store8(static_cast<T*>(a.q_out) + ((int64_t)token * v.q_heads + h) * D + d0, x);
-        return;
-    }
-
     float lo = 0.0f, hi = 0.0f;
     int bad = 0;                                  // a NaN, which min and max skip
 #pragma unroll
@@ -209,10 +152,9 @@ __global__ __launch_bounds__(kThreads) void kv4_append_kernel(AppendArgs a)
         nat |= (uint32_t)c << (4 * i);
     }
     const uint32_t other = (uint32_t)__shfl_xor((int)nat, 2);
-    if (!at.block) return;                        // whole lane groups
     if (l % GL == 0) {
-        const int meta = 32 * D + (is_v ? 128 * NG : 0) + (at.key * NG + l / GL) * 4;
-        *reinterpret_cast<uint32_t*>(at.block + meta) =
+        const int meta = 32 * D + (is_v ? 128 * NG : 0) + (key * NG + l / GL) * 4;
+        *reinterpret_cast<uint32_t*>(block + meta) =
             (uint32_t)__builtin_bit_cast(uint16_t, s16) | ((uint32_t)z << 16);
     }
     if (!is_v) {
@@ -220,13 +162,13 @@ __global__ __launch_bounds__(kThreads) void kv4_append_kernel(AppendArgs a)
         uint32_t w = 0;
 #pragma unroll
         for (int i = 0; i < 8; ++i) w |= ((nat >> (4 * i)) & 15u) << (4 * nibble_slot(i));
-        *reinterpret_cast<uint32_t*>(at.block + key_word_at<LPR>(at.key, l)) = w;
+        *reinterpret_cast<uint32_t*>(block + key_word_at<LPR>(key, l)) = w;
     } else {
         // lanes l and l ^ 2 hold dims 16 apart: the low and the high nibble of 8
         // bytes, of which each writes four
         const bool upper = (l & 2) != 0;
         const uint32_t lo4 = upper ? other : nat, hi4 = upper ? nat : other;
-        unsigned char* dst = at.block + value_byte_at<LPR>(at.key, l);
+        unsigned char* dst = block + value_byte_at<LPR>(key, l);
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
             const int i = j + (upper ? 4 : 0);
@@ -236,66 +178,154 @@ __global__ __launch_bounds__(kThreads) void kv4_append_kernel(AppendArgs a)
 }
 
 template <typename T, int LPR>
-__global__ __launch_bounds__(kThreads) void kv4_read_kernel(ReadArgs a)
+__global__ __launch_bounds__(1024) void kv4_append_kernel(AppendArgs a)
+{
+#pragma clang fp contract(off)
+    constexpr int D = 8 * LPR;
+    const KvView& v = a.v;
+    const int token = blockIdx.x;
+    const int l = threadIdx.x % LPR, d0 = 8 * l;
+    const int hq = a.q ? v.q_heads : 0;
+    const int items = hq + 2 * v.kv_heads;       // heads of q, then of k, then of v
+    const int step = blockDim.x / LPR;
+    const int NG = v.groups, GL = LPR / NG;      // lanes of a group
+    const int half = a.rotary_dim >> 1;
+    const bool turn = a.cos && d0 < a.rotary_dim;
+    const bool second = turn && !a.interleaved && d0 >= half;
+    const T* const srcs[3] = {static_cast<const T*>(a.q) + token * a.q_stride, static_cast<const T*>(a.k) + token * a.k_stride,
+                              static_cast<const T*>(a.val) + token * a.v_stride};
+    // 8 values of an item, and the 8 they are turned with
+    auto fetch = [&](int item, float* x, float* y) {
+        const int kind = item < hq ? 0 : item < hq + v.kv_heads ? 1 : 2;
+        const T* src = (kind == 0 ? srcs[0] : kind == 1 ? srcs[1] : srcs[2]) +
+                       (int64_t)(item - (kind == 0 ? 0 : kind == 1 ? hq : hq + v.kv_heads)) * D;
+        load8(src + d0, x);
+        if (kind < 2 && turn && !a.interleaved) load8(src + (second ? d0 - half : d0 + half), y);
+    };
+    int item = threadIdx.x / LPR;
+    float x[8], y[8];
+    if (item < items) fetch(item, x, y);
+
+    const int64_t block_bytes = kv_block_bytes(D, NG);
+    const int64_t head_bytes = block_bytes << (v.page_shift - 5);
+    const Place at = place_of(v, token, block_bytes);
+    float c[8], s[8];                            // interleaved: four of each
+    if (turn) {
+        int64_t row = at.pos < 0 ? 0 : at.pos;
+        row = (row < a.rope_rows ? row : a.rope_rows - 1) * half;
+        if (a.interleaved) {
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                c[i] = a.cos[row + (d0 >> 1) + i];
+                s[i] = a.sin[row + (d0 >> 1) + i];
+            }
+        } else {
+            load8(a.cos + row + (second ? d0 - half : d0), c);
+            load8(a.sin + row + (second ? d0 - half : d0), s);
+        }
+    }
+    for (; item < items; item += step) {
+        float nx[8], ny[8];                      // the next item's values, on their way
+        if (item + step < items) fetch(item + step, nx, ny);
+        const bool is_q = item < hq, is_v = item >= hq + v.kv_heads;
+        if (turn && !is_v) {
+            if (a.interleaved) {
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const float e = x[2 * i], o = x[2 * i + 1];
+                    x[2 * i] = e * c[i] - o * s[i];
+                    x[2 * i + 1] = o * c[i] + e * s[i];
+                }
+            } else {
+#pragma unroll
+                for (int i = 0; i < 8; ++i) {
+                    const float p = x[i] * c[i], t = y[i] * s[i];
+                    x[i] = second ? p + t : p - t;
+                }
+            }
+        }
+        if (is_q)
+            store8(static_cast<T*>(a.q_out) + ((int64_t)token * v.q_heads + item) * D + d0, x);
+        else if (at.page)
+            store_head<LPR>(x, at.page + (item - hq - (is_v ? v.kv_heads : 0)) * head_bytes, at.key, is_v, l, NG, GL);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            x[i] = nx[i];
+            y[i] = ny[i];
+        }
+    }
+}
+
+template <typename T, int LPR>
+__global__ __launch_bounds__(1024) void kv4_read_kernel(ReadArgs a)
 {
     constexpr int D = 8 * LPR;
     const KvView& v = a.v;
+    const int token = blockIdx.x;
     const int l = threadIdx.x % LPR;
-    const int items = 2 * v.kv_heads;
-    const int64_t id = (int64_t)blockIdx.x * (kThreads / LPR) + threadIdx.x / LPR;
-    const int token = (int)(id / items);
-    if (token >= v.tokens) return;
-    const int item = (int)(id % items);
-    const bool is_v = item >= v.kv_heads;
-    const int h = is_v ? item - v.kv_heads : item;
     const int NG = v.groups, GL = LPR / NG;
-    void* out = is_v ? a.v_out : a.k_out;
-    if (!out) return;
-
-    const Place at = place_of<LPR>(v, token, h, kv_block_bytes(D, NG), l);
-    float x[8] = {0, 0, 0, 0, 0, 0, 0, 0};
-    if (at.block) {
-        const uint32_t m = *reinterpret_cast<const uint32_t*>(at.block + 32 * D + (is_v ? 128 * NG : 0) +
-                                                              (at.key * NG + l / GL) * 4);
-        const float s = (float)__builtin_bit_cast(_Float16, (uint16_t)m);
-        const int z = (int)((m >> 16) & 15u);
-        int c[8];
-        if (!is_v) {
-            const uint32_t w = *reinterpret_cast<const uint32_t*>(at.block + key_word_at<LPR>(at.key, l));
+    const int step = blockDim.x / LPR;
+    const int64_t block_bytes = kv_block_bytes(D, NG);
+    const int64_t head_bytes = block_bytes << (v.page_shift - 5);
+    const Place at = place_of(v, token, block_bytes);
+    for (int item = threadIdx.x / LPR; item < 2 * v.kv_heads; item += step) {
+        const bool is_v = item >= v.kv_heads;
+        const int h = is_v ? item - v.kv_heads : item;
+        void* out = is_v ? a.v_out : a.k_out;
+        if (!out) continue;
+        float x[8] = {0, 0, 0, 0, 0, 0, 0, 0};
+        if (at.page) {
+            const unsigned char* block = at.page + h * head_bytes;
+            const uint32_t m = *reinterpret_cast<const uint32_t*>(block + 32 * D + (is_v ? 128 * NG : 0) +
+                                                                  (at.key * NG + l / GL) * 4);
+            const float s = (float)__builtin_bit_cast(_Float16, (uint16_t)m);
+            const int z = (int)((m >> 16) & 15u);
+            int c[8];
+            if (!is_v) {
+                const uint32_t w = *reinterpret_cast<const uint32_t*>(block + key_word_at<LPR>(at.key, l));
 #pragma unroll
-            for (int i = 0; i < 8; ++i) c[i] = (int)code_at(w, i);
-        } else {
-            const unsigned char* src = at.block + value_byte_at<LPR>(at.key, l);
+                for (int i = 0; i < 8; ++i) c[i] = (int)code_at(w, i);
+            } else {
+                const unsigned char* src = block + value_byte_at<LPR>(at.key, l);
 #pragma unroll
-            for (int i = 0; i < 8; ++i) c[i] = (src[16 * i] >> ((l & 2) * 2)) & 15;
+                for (int i = 0; i < 8; ++i) c[i] = (src[16 * i] >> ((l & 2) * 2)) & 15;
+            }
+#pragma unroll
+            for (int i = 0; i < 8; ++i) x[i] = (float)(c[i] - z) * s;
         }
-#pragma unroll
-        for (int i = 0; i < 8; ++i) x[i] = (float)(c[i] - z) * s;
+        store8(static_cast<T*>(out) + ((int64_t)token * v.kv_heads + h) * D + 8 * l, x);
     }
-    store8(static_cast<T*>(out) + ((int64_t)token * v.kv_heads + h) * D + 8 * l, x);
 }
 
-inline unsigned blocks_for(int64_t items, int lanes) { return (unsigned)((items * lanes + kThreads - 1) / kThreads); }
+// Threads of a token's workgroup: a lane group for every head while there are few
+// tokens, up to 256 threads otherwise.
+inline dim3 threads_for(int tokens, int items, int lanes)
+{
+    const int most = tokens <= 512 ? 1024 : 256;
+    const int want = (items * lanes + 63) / 64 * 64;
+    return dim3((unsigned)(want < most ? want : most));
+}
 
 }  // namespace
 
 hipError_t launch_kv4_append(const AppendArgs& a, hipStream_t stream, const char** variant)
 {
     const int lpr = a.v.head_dim / 8;
-    const unsigned grid = blocks_for((int64_t)a.v.tokens * ((a.q ? a.v.q_heads : 0) + 2 * a.v.kv_heads), lpr);
+    const dim3 grid((unsigned)a.v.tokens);
+    const dim3 block = threads_for(a.v.tokens, (a.q ? a.v.q_heads : 0) + 2 * a.v.kv_heads, lpr);
     *variant = "kv4_append";
     switch (lpr) {
     case 8:
-        if (a.f16) kv4_append_kernel<_Float16, 8><<<grid, kThreads, 0, stream>>>(a);
-        else kv4_append_kernel<float, 8><<<grid, kThreads, 0, stream>>>(a);
+        if (a.f16) kv4_append_kernel<_Float16, 8><<<grid, block, 0, stream>>>(a);
+        else kv4_append_kernel<float, 8><<<grid, block, 0, stream>>>(a);
         break;
     case 16:
-        if (a.f16) kv4_append_kernel<_Float16, 16><<<grid, kThreads, 0, stream>>>(a);
-        else kv4_append_kernel<float, 16><<<grid, kThreads, 0, stream>>>(a);
+        if (a.f16) kv4_append_kernel<_Float16, 16><<<grid, block, 0, stream>>>(a);
+        else kv4_append_kernel<float, 16><<<grid, block, 0, stream>>>(a);
         break;
     default:
-        if (a.f16) kv4_append_kernel<_Float16, 32><<<grid, kThreads, 0, stream>>>(a);
-        else kv4_append_kernel<float, 32><<<grid, kThreads, 0, stream>>>(a);
+        if (a.f16) kv4_append_kernel<_Float16, 32><<<grid, block, 0, stream>>>(a);
+        else kv4_append_kernel<float, 32><<<grid, block, 0, stream>>>(a);
     }
     return hipGetLastError();
 }
@@ -303,20 +333,21 @@ hipError_t launch_kv4_append(const AppendArgs& a, hipStream_t stream, const char
 hipError_t launch_kv4_read(const ReadArgs& a, hipStream_t stream, const char** variant)
 {
     const int lpr = a.v.head_dim / 8;
-    const unsigned grid = blocks_for((int64_t)a.v.tokens * 2 * a.v.kv_heads, lpr);
+    const dim3 grid((unsigned)a.v.tokens);
+    const dim3 block = threads_for(a.v.tokens, 2 * a.v.kv_heads, lpr);
     *variant = "kv4_read";
     switch (lpr) {
     case 8:
-        if (a.f16) kv4_read_kernel<_Float16, 8><<<grid, kThreads, 0, stream>>>(a);
-        else kv4_read_kernel<float, 8><<<grid, kThreads, 0, stream>>>(a);
+        if (a.f16) kv4_read_kernel<_Float16, 8><<<grid, block, 0, stream>>>(a);
+        else kv4_read_kernel<float, 8><<<grid, block, 0, stream>>>(a);
         break;
     case 16:
-        if (a.f16) kv4_read_kernel<_Float16, 16><<<grid, kThreads, 0, stream>>>(a);
-        else kv4_read_kernel<float, 16><<<grid, kThreads, 0, stream>>>(a);
+        if (a.f16) kv4_read_kernel<_Float16, 16><<<grid, block, 0, stream>>>(a);
+        else kv4_read_kernel<float, 16><<<grid, block, 0, stream>>>(a);
         break;
     default:
-        if (a.f16) kv4_read_kernel<_Float16, 32><<<grid, kThreads, 0, stream>>>(a);
-        else kv4_read_kernel<float, 32><<<grid, kThreads, 0, stream>>>(a);
+        if (a.f16) kv4_read_kernel<_Float16, 32><<<grid, block, 0, stream>>>(a);
+        else kv4_read_kernel<float, 32><<<grid, block, 0, stream>>>(a);
     }
     return hipGetLastError();
 }
