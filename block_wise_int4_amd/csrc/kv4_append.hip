@@ -225,8 +225,6 @@ __global__ __launch_bounds__(1024) void kv4_append_kernel(AppendArgs a)
         }
     }
     for (; item < items; item += step) {
-        float nx[8], ny[8];                      // the next item's values, on their way
-        if (item + step < items) fetch(item + step, nx, ny);
         const bool is_q = item < hq, is_v = item >= hq + v.kv_heads;
         if (turn && !is_v) {
             if (a.interleaved) {
@@ -248,11 +246,7 @@ __global__ __launch_bounds__(1024) void kv4_append_kernel(AppendArgs a)
             store8(static_cast<T*>(a.q_out) + ((int64_t)token * v.q_heads + item) * D + d0, x);
         else if (at.page)
             store_head<LPR>(x, at.page + (item - hq - (is_v ? v.kv_heads : 0)) * head_bytes, at.key, is_v, l, NG, GL);
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-            x[i] = nx[i];
-            y[i] = ny[i];
-        }
+        if (item + step < items) fetch(item + step, x, y);
     }
 }
 
