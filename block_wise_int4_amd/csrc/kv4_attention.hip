@@ -92,6 +92,20 @@ template <int N> __device__ __forceinline__ void words(const uint32_t* slot, uin
     }
 }
 
+// f is called with the rotations of a row of 16 lanes that bring the copies of a
+// column together (each leaves twice as many of them summed).
+template <int N> struct Turn {
+    __device__ __forceinline__ float operator()(float x) const
+    {
+        return __builtin_bit_cast(float, __builtin_amdgcn_update_dpp(0, __builtin_bit_cast(int, x), 0x120 + N, 0xF, 0xF, false));
+    }
+};
+template <int GRP, typename F> __device__ __forceinline__ void for_copies(F f)
+{
+    f(Turn<8>());
+    if constexpr (GRP == 4) f(Turn<4>());
+}
+
 // GRP column groups (4: up to 4 rows, 2: up to 8, 1: up to 16 NR).  KW waves
 // share the keys; PF blocks of a wave are in registers, all but the one in work
 // still on their way.  WPE: waves per SIMD that the registers are held to.
@@ -426,60 +440,75 @@ __global__ __launch_bounds__(KW * 64, WPE) void kv4_attention_kernel(AttnParams 
         l[n] += __shfl_xor(l[n], 32);
     }
 
-    // ---- the waves and the copies join through LDS, 16 columns by up to 128 dims at a time ----
-    constexpr int kMost = KW > 4 ? 64 : 128;               // at most 34 KB
+    // ---- the copies of a row join by rotations of the 16 columns ----
+    if constexpr (GRP > 1) {
+        float m = M[0];
+        for_copies<GRP>([&](auto turn) { m = fmaxf(m, turn(m)); });
+        const float w = exp2f(M[0] - m);
+        M[0] = m;
+        l[0] *= w;
+        for_copies<GRP>([&](auto turn) { l[0] += turn(l[0]); });
+#pragma unroll
+        for (int t = 0; t < NT; ++t)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                float y = o[0][t][i] * w;
+                for_copies<GRP>([&](auto turn) { y += turn(y); });
+                o[0][t][i] = y;
+            }
+    }
+    // ---- the waves join through LDS, R rows by up to 128 dims at a time ----
+    constexpr int kMost = KW * R > 64 ? 64 : 128;          // at most 34 KB
     constexpr int kDims = D < kMost ? D : kMost, kPitch = kDims + 4;   // rows start in different banks
-    constexpr int kParts = D / kDims, kTiles = kDims / 16, kJoin = KW * GRP;
-    __shared__ __align__(16) float so[KW][16][kPitch];
-    __shared__ float ml[KW][NR][16][2];
-    if (quarter == 0) {
+    constexpr int kParts = D / kDims, kTiles = kDims / 16, kQuads = kDims / 4;
+    __shared__ __align__(16) float so[KW][R][kPitch];
+    __shared__ float ml[KW][NR][R][2];
+    if (quarter == 0 && copy == 0) {
 #pragma unroll
         for (int n = 0; n < NR; ++n) {
             ml[kw][n][col][0] = M[n];
             ml[kw][n][col][1] = l[n];
         }
     }
-    const int row = col % R, worker = kw * GRP + copy;     // of a row: tile t of a part goes to worker t % kJoin
 #pragma unroll
     for (int n = 0; n < NR; ++n) {
-        const int r = row0 + n * 16 + row;
-        const int64_t out_row = r < rows ? (int64_t)(s.first + r / p.gqa) * v.q_heads + h * p.gqa + r % p.gqa : -1;
-        float m = kLow, sum = 0.0f, w[kJoin];
 #pragma unroll
         for (int part = 0; part < kParts; ++part) {
             if (n + part > 0) __syncthreads();             // the last part has been read
+            if (copy == 0) {
 #pragma unroll
-            for (int t = 0; t < kTiles; ++t)
-                *reinterpret_cast<f4_t*>(&so[kw][col][16 * t + 4 * quarter]) = o[n][part * kTiles + t];
-            __syncthreads();
-            if (part == 0) {
-#pragma unroll
-                for (int k = 0; k < kJoin; ++k) m = fmaxf(m, ml[k / GRP][n][row + k % GRP * R][0]);
-#pragma unroll
-                for (int k = 0; k < kJoin; ++k) {
-                    w[k] = exp2f(ml[k / GRP][n][row + k % GRP * R][0] - m);
-                    sum = __builtin_fmaf(ml[k / GRP][n][row + k % GRP * R][1], w[k], sum);
-                }
+                for (int t = 0; t < kTiles; ++t)
+                    *reinterpret_cast<f4_t*>(&so[kw][col][16 * t + 4 * quarter]) = o[n][part * kTiles + t];
             }
-            if (out_row < 0) continue;
-            for (int t = worker; t < kTiles; t += kJoin) {
+            __syncthreads();
+            // four dims of a row to a thread
+            for (int i = threadIdx.x; i < R * kQuads; i += KW * 64) {
+                const int row = i / kQuads, d = i % kQuads * 4;
+                const int r = row0 + n * 16 + row;
+                if (r >= rows) continue;
+                float m = kLow, sum = 0.0f;
                 f4_t y = {0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
-                for (int k = 0; k < kJoin; ++k)
-                    y += *reinterpret_cast<const f4_t*>(&so[k / GRP][row + k % GRP * R][16 * t + 4 * quarter]) * w[k];
-                const int d = part * kDims + 16 * t + 4 * quarter;
+                for (int k = 0; k < KW; ++k) m = fmaxf(m, ml[k][n][row][0]);
+#pragma unroll
+                for (int k = 0; k < KW; ++k) {
+                    const float w = exp2f(ml[k][n][row][0] - m);
+                    sum = __builtin_fmaf(ml[k][n][row][1], w, sum);
+                    y += *reinterpret_cast<const f4_t*>(&so[k][row][d]) * w;
+                }
+                const int64_t out_row = (int64_t)(s.first + r / p.gqa) * v.q_heads + h * p.gqa + r % p.gqa;
+                const int64_t part_row = (int64_t)split * v.tokens * v.q_heads + out_row;
                 if (p.splits == 1)                         // a row that sees nothing gives zeros
-                    store4(static_cast<T*>(p.out) + out_row * D + d, y, sum == 0.0f ? 0.0f : 1.0f / sum);
+                    store4(static_cast<T*>(p.out) + out_row * D + part * kDims + d, y, sum == 0.0f ? 0.0f : 1.0f / sum);
                 else
-                    *reinterpret_cast<f4_t*>(p.part_o + ((int64_t)split * v.tokens * v.q_heads + out_row) * D + d) = y;
-            }
-            if (part == 0 && worker == 0 && quarter == 0) {
-                if (p.splits > 1) {
-                    float* e = p.part_ml + 2 * ((int64_t)split * v.tokens * v.q_heads + out_row);
-                    e[0] = m;
-                    e[1] = sum;
-                } else if (p.lse) {
-                    p.lse[out_row] = log_sum(m, sum);
+                    *reinterpret_cast<f4_t*>(p.part_o + part_row * D + part * kDims + d) = y;
+                if (part == 0 && d == 0) {
+                    if (p.splits > 1) {
+                        p.part_ml[2 * part_row] = m;
+                        p.part_ml[2 * part_row + 1] = sum;
+                    } else if (p.lse) {
+                        p.lse[out_row] = log_sum(m, sum);
+                    }
                 }
             }
         }
@@ -578,7 +607,11 @@ Plan plan_of(const AttentionArgs& a)
         // up to 1024 keys one workgroup of 8 waves does without the join
         c.kind = !wide && a.v.groups <= 2 && c.group && a.max_kv <= 1024 ? 0 : 1;
         least = 256;
-        want = 2048;
+        // one sequence: its pieces are alike, and two workgroups a CU in one round
+        // are best (131072 keys: 34 us with 512, 44 with 2048); several of unknown
+        // lengths: more and shorter pieces even them out (32 sequences of up to 8192 keys:
+        // 45 us with 512, 41 with 3072)
+        want = a.v.batch == 1 ? 512 : 3072;
     } else {
         c.kind = 2;
         // two column tiles a wave where that leaves a workgroup for every CU: 1000
