@@ -10,7 +10,6 @@ the import fails.
 from __future__ import annotations
 
 import ctypes
-import math
 import os
 from typing import Optional, Union
 
@@ -18,6 +17,7 @@ try:                       # device memory and streams; the host-only calls work
     import torch
     # the current stream's handle without building a stream object (2.8 us a call)
     from torch._C import _cuda_getCurrentRawStream as _raw_stream, _cuda_getDevice as _current_device
+    from torch.cuda import is_initialized as _initialized
 except ImportError:
     torch = _raw_stream = None
 
@@ -171,7 +171,7 @@ def _ptr(x: Ptr):
 
 def _stream(stream):
     if stream is None:
-        if _raw_stream is not None and torch.cuda.is_initialized():
+        if _raw_stream is not None and _initialized():
             return _raw_stream(_current_device())
         import torch as _t
         stream = _t.cuda.current_stream()
@@ -336,26 +336,29 @@ def _addr(x, name: str) -> Optional[int]:
     return x.data_ptr()
 
 
-def _rows(x, name: str):
-    """Address and row stride of a tensor whose rows (all dims but the first) are dense."""
-    if not x.is_cuda:
-        raise ValueError("%s: device tensor expected" % name)
-    shape = x.shape
-    if x.is_contiguous():
-        return x.data_ptr(), math.prod(shape[1:])
-    stride, dense = x.stride(), 1
-    for i in range(len(shape) - 1, 0, -1):
-        if shape[i] != 1 and stride[i] != dense:
-            raise ValueError("%s: rows must be dense" % name)
-        dense *= shape[i]
-    return x.data_ptr(), stride[0] if shape[0] > 1 else dense
+def _refuse(tensors) -> None:
+    """Raises for the first of (tensor, name, dtype, shape) that is not as it should be."""
+    for x, name, dtype, shape in tensors:
+        if x.dtype is not dtype:
+            raise ValueError("%s: %s expected, got %s" % (name, dtype, x.dtype))
+        if x.shape != shape:
+            raise ValueError("%s: shape %s expected, got %s" % (name, tuple(shape), tuple(x.shape)))
 
 
-def _expect(x, name: str, dtype, shape) -> None:
-    if x.dtype is not dtype:
-        raise ValueError("%s: %s expected, got %s" % (name, dtype, x.dtype))
-    if x.shape != shape:
-        raise ValueError("%s: shape %s expected, got %s" % (name, tuple(shape), tuple(x.shape)))
+def _rows2(x, name: str):
+    """Address and row stride of an [m, k] tensor whose rows are dense."""
+    stride, shape = x.stride(), x.shape
+    if not x.is_cuda or (stride[1] != 1 and shape[1] > 1):
+        raise ValueError("%s: device tensor with dense rows expected" % name)
+    return x.data_ptr(), stride[0] if shape[0] > 1 else shape[1]
+
+
+def _rows3(x, heads: int, dim: int, name: str):
+    """The same for [tokens, heads, dim]: a token's heads and dims are dense."""
+    stride = x.stride()
+    if not x.is_cuda or stride[2] != 1 or (stride[1] != dim and heads > 1):
+        raise ValueError("%s: device tensor with dense rows expected" % name)
+    return x.data_ptr(), stride[0] if x.shape[0] > 1 else heads * dim
 
 
 def mnb_rms_norm(x, weight, out, eps: float, residual=None, residual_out=None, scales=None, stream=None) -> None:
@@ -366,19 +369,22 @@ def mnb_rms_norm(x, weight, out, eps: float, residual=None, residual_out=None, s
     kind, want = MNB_NORM_VALUES, dtype
     if scales is not None:
         kind, want = (MNB_NORM_CODES_I8, torch.int8) if out.dtype is torch.int8 else (MNB_NORM_CODES_F16, torch.float16)
-        _expect(scales, "scales", torch.float32, (m,))
-    _expect(out, "out", want, shape)
-    _expect(weight, "weight", dtype, (k,))
-    xp, xs = _rows(x, "x")
+        if scales.dtype is not torch.float32 or scales.shape != (m,):
+            _refuse(((scales, "scales", torch.float32, (m,)),))
+    if out.dtype is not want or out.shape != shape or weight.dtype is not dtype or weight.shape != (k,):
+        _refuse(((out, "out", want, shape), (weight, "weight", dtype, (k,))))
+    xp, xs = _rows2(x, "x")
     rp, rs = None, 0
     if residual is not None:
-        _expect(residual, "residual", dtype, shape)
-        rp, rs = _rows(residual, "residual")
-    if residual_out is not None:
-        _expect(residual_out, "residual_out", dtype, shape)
-    _check(lib.mnb_rms_norm(xp, xs, rp, rs, _addr(weight, "weight"), m, k, _dtype_code(x), eps, kind,
-                            _addr(out, "out"), _addr(scales, "scales"), _addr(residual_out, "residual_out"),
-                            _stream(stream)))
+        if residual.dtype is not dtype or residual.shape != shape:
+            _refuse(((residual, "residual", dtype, shape),))
+        rp, rs = _rows2(residual, "residual")
+    if residual_out is not None and (residual_out.dtype is not dtype or residual_out.shape != shape):
+        _refuse(((residual_out, "residual_out", dtype, shape),))
+    st = lib.mnb_rms_norm(xp, xs, rp, rs, _addr(weight, "weight"), m, k, _dtype_code(x), eps, kind, _addr(out, "out"),
+                          _addr(scales, "scales"), _addr(residual_out, "residual_out"), _stream(stream))
+    if st:
+        _check(st)
 
 
 def kv4_desc(q_heads: int, kv_heads: int, head_dim: int, group_size: int, page_size: int,
@@ -396,57 +402,63 @@ def mnb_kv4_cache_bytes(c: mnb_kv4_desc) -> int:
 def _sequences(c, cache, table, kv_len, q_start):
     """Descriptor, cache, table, table stride, lengths, offsets and batch of a call, after a look at their types and sizes."""
     i32 = torch.int32
+    batch = kv_len.shape[0]
     if table.dtype is not i32 or kv_len.dtype is not i32 or (q_start is not None and q_start.dtype is not i32):
         raise ValueError("block_table, kv_len and q_start: int32 expected")
-    batch = kv_len.shape[0]
     if table.shape[0] != batch or (q_start is not None and q_start.shape[0] != batch + 1):
         raise ValueError("block_table, kv_len and q_start: one row, length and offset (and one more) per sequence")
     d = ctypes.byref(c)
-    size = lib.mnb_kv4_cache_bytes(d)
-    if cache.numel() * cache.element_size() < size or size == 0:
+    if cache.numel() * cache.element_size() < lib.mnb_kv4_cache_bytes(d):
         raise ValueError("cache: %d bytes expected" % mnb_kv4_cache_bytes(c))
-    tp, ts = _rows(table, "block_table")
+    tp, ts = _rows2(table, "block_table")
     return d, _addr(cache, "cache"), tp, ts, _addr(kv_len, "kv_len"), _addr(q_start, "q_start"), batch
 
 
 def mnb_kv4_append(c: mnb_kv4_desc, cache, k, v, block_table, kv_len, q_start=None, cos=None, sin=None,
                    rotary_dim: int = 0, interleaved: bool = False, q=None, q_out=None, stream=None) -> None:
     """k, v [tokens, kv_heads, head_dim] and q [tokens, q_heads, head_dim], tokens may be strided."""
-    seq = _sequences(c, cache, block_table, kv_len, q_start)
-    dtype, n, D = k.dtype, k.shape[0], c.head_dim
-    shape = (n, c.kv_heads, D)
-    _expect(k, "k", dtype, shape)
-    _expect(v, "v", dtype, shape)
-    kp, ks = _rows(k, "k")
-    vp, vs = _rows(v, "v")
+    d, cp, tp, ts, lp, sp, batch = _sequences(c, cache, block_table, kv_len, q_start)
+    dtype, n, D, H = k.dtype, k.shape[0], c.head_dim, c.kv_heads
+    shape = (n, H, D)
+    if k.shape != shape or v.dtype is not dtype or v.shape != shape:
+        _refuse(((k, "k", dtype, shape), (v, "v", dtype, shape)))
+    kp, ks = _rows3(k, H, D, "k")
+    vp, vs = _rows3(v, H, D, "v")
     qp, qs, rows = None, 0, 0
     if q is not None:
-        shape = (n, c.q_heads, D)
-        _expect(q, "q", dtype, shape)
-        qp, qs = _rows(q, "q")
-        if q_out is not None:
-            _expect(q_out, "q_out", dtype, shape)
+        H = c.q_heads
+        shape = (n, H, D)
+        if q.dtype is not dtype or q.shape != shape or (q_out is not None and (q_out.dtype is not dtype or q_out.shape != shape)):
+            _refuse(((q, "q", dtype, shape), (q_out, "q_out", dtype, shape)))
+        qp, qs = _rows3(q, H, D, "q")
     if cos is not None:
         rows = cos.shape[0]
-        _expect(cos, "cos", torch.float32, (rows, rotary_dim // 2))
-        if sin is not None:
-            _expect(sin, "sin", torch.float32, (rows, rotary_dim // 2))
-    _check(lib.mnb_kv4_append(*seq, n, _dtype_code(k), qp, qs, kp, ks, vp, vs, _addr(cos, "cos"), _addr(sin, "sin"),
-                              rows, rotary_dim, 1 if interleaved else 0, _addr(q_out, "q_out"), _stream(stream)))
+        shape = (rows, rotary_dim // 2)
+        f32 = torch.float32
+        if cos.dtype is not f32 or cos.shape != shape or (sin is not None and (sin.dtype is not f32 or sin.shape != shape)):
+            _refuse(((cos, "cos", f32, shape), (sin, "sin", f32, shape)))
+    st = lib.mnb_kv4_append(d, cp, tp, ts, lp, sp, batch, n, _dtype_code(k), qp, qs, kp, ks, vp, vs, _addr(cos, "cos"),
+                            _addr(sin, "sin"), rows, rotary_dim, 1 if interleaved else 0, _addr(q_out, "q_out"),
+                            _stream(stream))
+    if st:
+        _check(st)
 
 
 def mnb_kv4_read(c: mnb_kv4_desc, cache, block_table, kv_len, q_start, k_out=None, v_out=None, stream=None) -> None:
     """k_out, v_out [tokens, kv_heads, head_dim]; either may be None."""
-    seq = _sequences(c, cache, block_table, kv_len, q_start)
+    d, cp, tp, ts, lp, sp, batch = _sequences(c, cache, block_table, kv_len, q_start)
     some = k_out if k_out is not None else v_out
     if some is None:
         return
+    dtype = some.dtype
     shape = (some.shape[0], c.kv_heads, c.head_dim)
-    _expect(some, "k_out" if k_out is not None else "v_out", some.dtype, shape)
-    if v_out is not None and v_out is not some:
-        _expect(v_out, "v_out", some.dtype, shape)
-    _check(lib.mnb_kv4_read(*seq, shape[0], _dtype_code(some), _addr(k_out, "k_out"), _addr(v_out, "v_out"),
-                            _stream(stream)))
+    for x in (k_out, v_out):
+        if x is not None and (x.dtype is not dtype or x.shape != shape):
+            _refuse(((x, "k_out and v_out", dtype, shape),))
+    st = lib.mnb_kv4_read(d, cp, tp, ts, lp, sp, batch, shape[0], _dtype_code(some), _addr(k_out, "k_out"),
+                          _addr(v_out, "v_out"), _stream(stream))
+    if st:
+        _check(st)
 
 
 def mnb_attention_kv4_workspace_bytes(c: mnb_kv4_desc, batch: int, tokens: int, max_q: int, max_kv: int) -> int:
@@ -457,20 +469,22 @@ def mnb_attention_kv4(c: mnb_kv4_desc, cache, q, block_table, kv_len, q_start, m
                       scale: float, causal: bool = True, window: int = 0, lse=None, workspace: Ptr = None,
                       workspace_bytes: Optional[int] = None, stream=None) -> None:
     """q [tokens, q_heads, head_dim] (tokens may be strided), out the same, lse fp32 [tokens, q_heads]."""
-    seq = _sequences(c, cache, block_table, kv_len, q_start)
-    dtype, n = q.dtype, q.shape[0]
-    shape = (n, c.q_heads, c.head_dim)
-    _expect(q, "q", dtype, shape)
-    _expect(out, "out", dtype, shape)
-    if lse is not None:
-        _expect(lse, "lse", torch.float32, shape[:2])
+    d, cp, tp, ts, lp, sp, batch = _sequences(c, cache, block_table, kv_len, q_start)
+    dtype, n, H, D = q.dtype, q.shape[0], c.q_heads, c.head_dim
+    shape = (n, H, D)
+    if q.shape != shape or out.dtype is not dtype or out.shape != shape:
+        _refuse(((q, "q", dtype, shape), (out, "out", dtype, shape)))
+    if lse is not None and (lse.dtype is not torch.float32 or lse.shape != (n, H)):
+        _refuse(((lse, "lse", torch.float32, (n, H)),))
     if workspace_bytes is None:
         workspace_bytes = 0 if workspace is None or type(workspace) is int else \
             workspace.numel() * workspace.element_size()
-    qp, qs = _rows(q, "q")
-    _check(lib.mnb_attention_kv4(*seq, n, max_q, max_kv, _dtype_code(q), qp, qs, scale, 1 if causal else 0, window,
-                                 _addr(out, "out"), _addr(lse, "lse"), _addr(workspace, "workspace"), workspace_bytes,
-                                 _stream(stream)))
+    qp, qs = _rows3(q, H, D, "q")
+    st = lib.mnb_attention_kv4(d, cp, tp, ts, lp, sp, batch, n, max_q, max_kv, _dtype_code(q), qp, qs, scale,
+                               1 if causal else 0, window, _addr(out, "out"), _addr(lse, "lse"),
+                               _addr(workspace, "workspace"), workspace_bytes, _stream(stream))
+    if st:
+        _check(st)
 
 
 def mnb_unpack_debug(w: mnb_weight_desc, repacked: Ptr, codes: Ptr, w_f32: Ptr, stream=None) -> None:
