@@ -614,11 +614,11 @@ Plan plan_of(const AttentionArgs& a)
         want = a.v.batch == 1 ? 512 : 3072;
     } else {
         c.kind = 2;
-        // two column tiles a wave where that leaves a workgroup for every CU: 1000
-        // rows of 32 heads 45 us with two, XX with one; 2048 tokens by 4 heads
-        // of 8 groups 233 with two, XX with one
+        // two column tiles a wave where that leaves a workgroup for every CU (1000
+        // rows of 32 key heads: 90 us with two, 34 with one; 2048 and 1100 tokens of 8
+        // key heads by 4: 233 us with two, 306 with one) and the registers hold them
         const int64_t wgs = (rows + 255) / 256 * a.v.kv_heads * a.v.batch;
-        c.tiles = wide || wgs < 256 ? 1 : 2;
+        c.tiles = wide || a.v.groups > 2 || wgs < 256 ? 1 : 2;
         c.rows = kPromptWaves * 16 * c.tiles;
         least = 256;
         want = 256;

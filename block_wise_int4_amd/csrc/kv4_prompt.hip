@@ -115,7 +115,33 @@ __global__ __launch_bounds__(RW * 64, 2) void kv4_prompt_kernel(AttnParams p)
     constexpr int kTilesOfQuad = D == 64 ? 2 : 1;      // key tiles in a quad
     u4_t code[IT];
     uint32_t zw[IT][8 * NG];
+    constexpr bool LATE = NG >= 8;                     // too many words to hold for a stage: loaded at the unpack
+    __amdgpu_buffer_rsrc_t rs[IT];
 
+    // Zero points and scales that item it needs.
+    auto words_of = [&](int it, bool is_v, int qi) {
+        const int meta = 32 * D + (is_v ? 128 * NG : 0);
+        if (is_v) {
+#pragma unroll
+            for (int t = 0; t < 2; ++t)
+#pragma unroll
+                for (int i = 0; i < NG; ++i) {
+                    const u4_t r = __builtin_amdgcn_raw_buffer_load_b128(rs[it], 16 * NG * quarter + 16 * i, meta + t * 64 * NG, 0);
+                    zw[it][t * 4 * NG + 4 * i] = r.x;
+                    zw[it][t * 4 * NG + 4 * i + 1] = r.y;
+                    zw[it][t * 4 * NG + 4 * i + 2] = r.z;
+                    zw[it][t * 4 * NG + 4 * i + 3] = r.w;
+                }
+        } else {
+#pragma unroll
+            for (int t = 0; t < kTilesOfQuad; ++t) {
+                const int tt = D == 64 ? t : qi * 4 / NJ;      // key tile
+#pragma unroll
+                for (int g = 0; g < NG; ++g)
+                    zw[it][t * NG + g] = __builtin_amdgcn_raw_buffer_load_b32(rs[it], (col * NG + g) * 4, meta + tt * 64 * NG, 0);
+            }
+        }
+    };
     auto request = [&](int st) {
 #pragma unroll
         for (int it = 0; it < IT; ++it) {
@@ -127,30 +153,9 @@ __global__ __launch_bounds__(RW * 64, 2) void kv4_prompt_kernel(AttnParams p)
             int at = blk - page0;
             at = at < 0 ? 0 : at > 63 ? 63 : at;
             unsigned char* base = v.cache + (((int64_t)page_in(v, pages, at) * v.kv_heads + h) * nblk + (blk & (nblk - 1))) * block_bytes;
-            const __amdgpu_buffer_rsrc_t rs =
-                __builtin_amdgcn_make_buffer_rsrc(base, 0, there ? 32 * D + 256 * NG : 0, 0x00020000);
-            code[it] = __builtin_amdgcn_raw_buffer_load_b128(rs, lane * 16, (is_v ? 16 * D : 0) + qi * 1024, 0);
-            const int meta = 32 * D + (is_v ? 128 * NG : 0);
-            if (is_v) {
-#pragma unroll
-                for (int t = 0; t < 2; ++t)
-#pragma unroll
-                    for (int i = 0; i < NG; ++i) {
-                        const u4_t r = __builtin_amdgcn_raw_buffer_load_b128(rs, 16 * NG * quarter + 16 * i, meta + t * 64 * NG, 0);
-                        zw[it][t * 4 * NG + 4 * i] = r.x;
-                        zw[it][t * 4 * NG + 4 * i + 1] = r.y;
-                        zw[it][t * 4 * NG + 4 * i + 2] = r.z;
-                        zw[it][t * 4 * NG + 4 * i + 3] = r.w;
-                    }
-            } else {
-#pragma unroll
-                for (int t = 0; t < kTilesOfQuad; ++t) {
-                    const int tt = D == 64 ? t : qi * 4 / NJ;      // key tile
-#pragma unroll
-                    for (int g = 0; g < NG; ++g)
-                        zw[it][t * NG + g] = __builtin_amdgcn_raw_buffer_load_b32(rs, (col * NG + g) * 4, meta + tt * 64 * NG, 0);
-                }
-            }
+            rs[it] = __builtin_amdgcn_make_buffer_rsrc(base, 0, there ? 32 * D + 256 * NG : 0, 0x00020000);
+            code[it] = __builtin_amdgcn_raw_buffer_load_b128(rs[it], lane * 16, (is_v ? 16 * D : 0) + qi * 1024, 0);
+            if constexpr (!LATE) words_of(it, is_v, qi);
         }
     };
     auto unpack = [&](int buf) {
@@ -159,14 +164,15 @@ __global__ __launch_bounds__(RW * 64, 2) void kv4_prompt_kernel(AttnParams p)
         for (int it = 0; it < IT; ++it) {
             const int Q = wave + it * RW;
             const int qq = Q & 3, bi = qq / QB, qi = qq % QB;
+            if constexpr (LATE) words_of(it, Q >= 4, qi);
             if (Q < 4) {
 #pragma unroll
                 for (int w = 0; w < 4; ++w) {
                     const int W = qi * 4 + w, t = W / NJ, j = W % NJ;
-                    const uint32_t word = D == 64 ? zw[it][(w / 2) * NG + (w % 2) / JG] : 0u;
-                    // group of step j; the word's tile is t
-                    uint32_t m = word;
-                    if constexpr (D > 64) {
+                    uint32_t m;                // zero point of the lane's key in tile t, group of step j
+                    if constexpr (D == 64) {
+                        m = zw[it][(w / 2) * NG + (w % 2) / JG];
+                    } else {
                         m = zw[it][0];
 #pragma unroll
                         for (int g = 1; g < NG; ++g) m = j / JG == g ? zw[it][g] : m;
@@ -453,7 +459,7 @@ __global__ __launch_bounds__(RW * 64, 2) void kv4_prompt_kernel(AttnParams p)
 template <int D, int NG, bool F32> hipError_t launch_tiles(const AttnParams& p, const Plan& c, hipStream_t s)
 {
     const dim3 grid((unsigned)(p.v.kv_heads * c.splits * c.row_tiles), (unsigned)p.v.batch);
-    if constexpr (D < 256) {
+    if constexpr (D < 256 && NG <= 2) {
         if (c.tiles == 2) {
             kv4_prompt_kernel<D, NG, F32, 2, kPromptWaves><<<grid, dim3(kPromptWaves * 64), 0, s>>>(p);
             return hipGetLastError();
