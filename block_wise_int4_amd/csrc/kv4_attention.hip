@@ -168,15 +168,15 @@ __global__ __launch_bounds__(KW * 64, WPE) void kv4_attention_kernel(AttnParams 
         int r = row0 + n * 16 + col % R;
         r = r < rows ? r : rows - 1;
         const int token = r / p.gqa, head = h * p.gqa + r % p.gqa;
-        pos[n] = p.causal ? s.len - s.count + token : s.len - 1;
+        pos[n] = p.causal ? s.before + token : s.len - 1;
         qs[n] = load_query<NJ>(static_cast<const T*>(p.q) + (int64_t)(s.first + token) * p.q_stride + (int64_t)head * D +
                                    8 * quarter, qf[n]);
     }
     // every row of the workgroup sees the whole of a block below `whole`, from `open` on
     int whole = s.len, open = 0;
     if (p.causal) {
-        whole = s.len - s.count + row0 / p.gqa + 1;
-        if (p.window > 0) open = s.len - s.count + last_row / p.gqa - p.window + 1;
+        whole = s.before + row0 / p.gqa + 1;
+        if (p.window > 0) open = s.before + last_row / p.gqa - p.window + 1;
     }
 
     f4_t o[NR][NT];

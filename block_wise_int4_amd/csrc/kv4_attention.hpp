@@ -73,7 +73,8 @@ __device__ __forceinline__ uint32_t max_halves(uint32_t a, uint32_t b)
 
 // Length and new tokens of a sequence, within the bounds of the call.
 struct Sequence {
-    int len, first, count;            // keys; first row and number of new tokens
+    int len, first, count;            // keys; first row and number of new tokens that are computed
+    int before;                       // position of the first new token
 };
 __device__ __forceinline__ Sequence sequence_of(const KvView& v, int b, int max_q, int max_kv)
 {
@@ -87,6 +88,7 @@ __device__ __forceinline__ Sequence sequence_of(const KvView& v, int b, int max_
         first = v.q_start[b];
         end = v.q_start[b + 1];
     }
+    s.before = s.len - (end - first);
     first = first < 0 ? 0 : first;
     end = end > v.tokens ? v.tokens : end;
     int n = end - first;
@@ -101,10 +103,10 @@ __device__ __forceinline__ void key_range(const AttnParams& p, const Sequence& s
     lo = 0;
     hi = s.len;
     if (p.causal) {
-        const int end = s.len - s.count + i1 + 1;
+        const int end = s.before + i1 + 1;
         hi = end < hi ? end : hi;
         if (p.window > 0) {
-            const int from = s.len - s.count + i0 - p.window + 1;
+            const int from = s.before + i0 - p.window + 1;
             lo = from > 0 ? from : 0;
         }
     }

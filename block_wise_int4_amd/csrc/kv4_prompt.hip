@@ -83,7 +83,7 @@ __global__ __launch_bounds__(RW * 64, 2) void kv4_prompt_kernel(AttnParams p)
         r = live ? r : rows - 1;
         const int token = r / p.gqa, head = h * p.gqa + r % p.gqa;
         out_row[n] = live ? (int64_t)(s.first + token) * v.q_heads + head : -1;
-        pos[n] = p.causal ? s.len - s.count + token : s.len - 1;
+        pos[n] = p.causal ? s.before + token : s.len - 1;
         qs[n] = load_query<NJ>(static_cast<const T*>(p.q) + (int64_t)(s.first + token) * p.q_stride + (int64_t)head * D +
                                    8 * quarter, qf[n]);
     }
@@ -92,9 +92,9 @@ __global__ __launch_bounds__(RW * 64, 2) void kv4_prompt_kernel(AttnParams p)
     int whole = s.len, open = 0, none = s.len;
     if (p.causal) {
         const int wlast = wrow0 + NR * 16 <= rows ? wrow0 + NR * 16 - 1 : rows - 1;
-        whole = s.len - s.count + wrow0 / p.gqa + 1;
-        none = s.len - s.count + wlast / p.gqa + 1;
-        if (p.window > 0) open = s.len - s.count + wlast / p.gqa - p.window + 1;
+        whole = s.before + wrow0 / p.gqa + 1;
+        none = s.before + wlast / p.gqa + 1;
+        if (p.window > 0) open = s.before + wlast / p.gqa - p.window + 1;
     }
     whole = whole < to ? whole : to;           // past the split's end LDS holds zeros
 

@@ -84,6 +84,14 @@ mnb_status check_counts(int64_t batch, int64_t tokens)
     return MNB_OK;
 }
 
+// A workgroup of up to 256 threads each, in a grid of less than 2^32 threads.
+mnb_status check_tokens(int64_t tokens)
+{
+    if (tokens >= (int64_t(1) << 24))
+        return fail(MNB_ERR_UNSUPPORTED, "%lld tokens not supported (below 2^24)", (long long)tokens);
+    return MNB_OK;
+}
+
 mnb::KvView view_of(const mnb_kv4_desc* c, const void* cache, const int32_t* block_table, int64_t table_stride,
                     const int32_t* kv_len, const int32_t* q_start, int64_t batch, int64_t tokens)
 {
@@ -115,8 +123,8 @@ mnb_status check_bounds(const mnb_kv4_desc* c, int64_t batch, int64_t tokens, in
     if (batch > 65535) return fail(MNB_ERR_UNSUPPORTED, "batch %lld not supported (at most 65535)", (long long)batch);
     if (max_kv > (int64_t(1) << 30))
         return fail(MNB_ERR_UNSUPPORTED, "max_kv %lld not supported (at most 2^30)", (long long)max_kv);
-    if (max_q > kMaxInt / 2 / c->q_heads)
-        return fail(MNB_ERR_UNSUPPORTED, "max_q %lld times q_heads %d not supported (at most 2^30)", (long long)max_q,
+    if (max_q > kMaxInt / 4 / c->q_heads)
+        return fail(MNB_ERR_UNSUPPORTED, "max_q %lld times q_heads %d not supported (below 2^29)", (long long)max_q,
                     c->q_heads);
     return MNB_OK;
 }
@@ -222,8 +230,7 @@ mnb_status mnb_kv4_append(const mnb_kv4_desc* c, void* cache, const int32_t* blo
     MNB_TRY(check_stride(v_stride, kv_row, tokens, "v_stride"));
     if (q) MNB_TRY(check_stride(q_stride, q_row, tokens, "q_stride"));
     if (tokens == 0 || batch == 0) return ok("noop");
-    if (tokens > kMaxInt / (c->q_heads + 2 * c->kv_heads))
-        return fail(MNB_ERR_UNSUPPORTED, "tokens %lld times heads not supported (below 2^31)", (long long)tokens);
+    MNB_TRY(check_tokens(tokens));
     MNB_TRY(check_sequences(block_table, table_stride, kv_len, q_start, batch, tokens));
     const uintptr_t elem = dtype == MNB_F16 ? 2 : 4;
     MNB_TRY(check_ptr(k, elem, "k"));
@@ -260,8 +267,7 @@ mnb_status mnb_kv4_read(const mnb_kv4_desc* c, const void* cache, const int32_t*
     MNB_TRY(check_dtype(dtype));
     MNB_TRY(check_counts(batch, tokens));
     if (tokens == 0 || batch == 0 || (!k_out && !v_out)) return ok("noop");
-    if (tokens > kMaxInt / (2 * c->kv_heads))
-        return fail(MNB_ERR_UNSUPPORTED, "tokens %lld times heads not supported (below 2^31)", (long long)tokens);
+    MNB_TRY(check_tokens(tokens));
     MNB_TRY(check_sequences(block_table, table_stride, kv_len, q_start, batch, tokens));
     const uintptr_t elem = dtype == MNB_F16 ? 2 : 4;
     if (k_out) MNB_TRY(check_ptr(k_out, elem, "k_out"));

@@ -241,18 +241,29 @@ __global__ __launch_bounds__(1024) void rms_norm_kernel(NormParams p)
 }
 
 template <typename T, int OUT>
-hipError_t launch_out(const NormArgs& a, const NormParams& p, hipStream_t s)
+hipError_t launch_out(const NormArgs& a, NormParams p, hipStream_t s)
 {
     const int64_t nv = a.k / Vec<T>::N;
-    const dim3 grid((unsigned)a.m);
-    int threads = (int)(nv < 64 ? 64 : nv > 512 ? 512 : (nv + 63) / 64 * 64);
-    if (nv <= 512)
-        rms_norm_kernel<T, OUT, 1><<<grid, dim3(threads), 0, s>>>(p);
-    else if (nv <= 1024)
-        rms_norm_kernel<T, OUT, 2><<<grid, dim3(threads), 0, s>>>(p);
-    else
-        rms_norm_kernel<T, OUT, 4><<<grid, dim3(threads), 0, s>>>(p);
-    return hipGetLastError();
+    const int threads = (int)(nv < 64 ? 64 : nv > 512 ? 512 : (nv + 63) / 64 * 64);
+    constexpr int64_t kRows = 1 << 22;     // of a launch: a grid holds less than 2^32 threads
+    const int64_t out_elem = OUT == kNormValues ? (int64_t)sizeof(T) : OUT == kNormCodesF16 ? 2 : 1;
+    for (int64_t r0 = 0; r0 < a.m; r0 += kRows) {
+        const dim3 grid((unsigned)(a.m - r0 < kRows ? a.m - r0 : kRows));
+        if (nv <= 512)
+            rms_norm_kernel<T, OUT, 1><<<grid, dim3(threads), 0, s>>>(p);
+        else if (nv <= 1024)
+            rms_norm_kernel<T, OUT, 2><<<grid, dim3(threads), 0, s>>>(p);
+        else
+            rms_norm_kernel<T, OUT, 4><<<grid, dim3(threads), 0, s>>>(p);
+        const hipError_t e = hipGetLastError();
+        if (e != hipSuccess) return e;
+        p.x = static_cast<const T*>(p.x) + kRows * p.x_stride;
+        if (p.residual) p.residual = static_cast<const T*>(p.residual) + kRows * p.residual_stride;
+        if (p.residual_out) p.residual_out = static_cast<T*>(p.residual_out) + kRows * a.k;
+        p.out = static_cast<unsigned char*>(p.out) + kRows * a.k * out_elem;
+        if (p.scales) p.scales += kRows;
+    }
+    return hipSuccess;
 }
 
 template <typename T> hipError_t launch_type(const NormArgs& a, const NormParams& p, hipStream_t s)

@@ -448,7 +448,7 @@ size_t mnb_kv4_cache_bytes(const mnb_kv4_desc* c);
  * token whose position is negative, past the table or on a page outside
  * 0..num_pages-1 is not stored (padding may use page -1).  Two tokens of one
  * call must not share a place.  Rows past q_start[batch] are ignored but for
- * q_out, which gets them rotated by position 0. */
+ * q_out, which gets them rotated by position 0.  tokens < 2^24. */
 mnb_status mnb_kv4_append(const mnb_kv4_desc* c, void* cache, const int32_t* block_table, int64_t table_stride,
                           const int32_t* kv_len, const int32_t* q_start, int64_t batch, int64_t tokens,
                           int32_t dtype, const void* q, int64_t q_stride, const void* k, int64_t k_stride,
@@ -472,12 +472,14 @@ mnb_status mnb_kv4_read(const mnb_kv4_desc* c, const void* cache, const int32_t*
  * q [tokens, q_heads, head_dim], tokens q_stride elements apart; out the same,
  * dense; lse NULL or fp32 [tokens, q_heads], the natural logarithm of the
  * sum of exponentials.  max_q and max_kv bound the new tokens and the length of
- * every sequence (they shape the grid; tokens past max_q get no output, keys
- * past max_kv are not seen and positions count from min(kv_len, max_kv)).
- * Logits, sums and outputs are kept in fp32.
+ * every sequence: they shape the grid.  A sequence's tokens past its first max_q
+ * and rows of no sequence are not written; keys past max_kv are not seen, and
+ * positions count from min(kv_len, max_kv).  Logits, sums and outputs are kept in
+ * fp32; in fp16 calls the weights p times the value's scale are rounded to fp16
+ * once, as is the output.
  * workspace (256-byte aligned): mnb_attention_kv4_workspace_bytes of the same
  * arguments; contents need no initialisation.  batch <= 65535, max_kv <=
- * 2^30.  Deterministic. */
+ * 2^30, max_q * q_heads < 2^29.  Deterministic. */
 size_t mnb_attention_kv4_workspace_bytes(const mnb_kv4_desc* c, int64_t batch, int64_t tokens, int64_t max_q,
                                          int64_t max_kv);
 mnb_status mnb_attention_kv4(const mnb_kv4_desc* c, const void* cache, const int32_t* block_table,

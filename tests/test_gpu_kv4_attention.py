@@ -233,6 +233,26 @@ def test_keys_past_the_bound_are_not_seen(mnb):
     check(mnb, geo, cache, vmax, table, lens, [0, 2], q, 0.1, max_kv=77)
 
 
+@pytest.mark.parametrize("max_q", [1, 3, 40])
+def test_tokens_past_the_bound_are_not_written(mnb, max_q):
+    """More new tokens than max_q: the first max_q of each sequence as they would be, the rest untouched."""
+    rng = np.random.default_rng(940)
+    lens, new = [90, 61], [50, 2]
+    table, pages = sequences(rng, lens, 32)
+    geo = o.Geometry(2, 1, 64, 64, 32, pages)
+    cache, vmax = make_cache(rng, geo, table, lens)
+    q = rng.normal(size=(52, 2, 64)).astype(np.float16)
+    out, _ = attend(mnb, geo, cache, table, lens, [0, 50, 52], q, 0.1, max_q=max_q)
+    w, _, size, reach = o.attention(geo, cache, table, lens, [0, 50, 52], q, 0.1)
+    tol = o.attention_tolerance(size, reach, 90, 64, True, vmax)
+    got = G.host(out)
+    for t in range(52):
+        if t - (0 if t < 50 else 50) < max_q:
+            assert (np.abs(got[t] - w[t]) <= tol[t]).all(), t
+        else:
+            assert (got[t] == 7.0).all(), t
+
+
 def test_device_values_out_of_range_stay_inside(mnb):
     """Lengths past the table, pages outside the cache, offsets past the rows: finite memory use, no fault."""
     t = G.torch()

@@ -157,6 +157,27 @@ def test_large_row_count_and_offsets(mnb):
     assert not out[:-2].any()
 
 
+def test_more_rows_than_a_launch_takes(mnb):
+    # 2^22 + 3 rows of 16: a second launch takes the last three
+    t = G.torch()
+    m, k = (1 << 22) + 3, 16
+    rng = np.random.default_rng(10)
+    x = t.ones((m, k), dtype=t.float16, device="cuda")
+    r = t.zeros((m, k), dtype=t.float16, device="cuda")
+    rows = [0, 1 << 22, (1 << 22) + 2]
+    part, rpart = (rng.normal(size=(3, k)).astype(np.float16) for _ in range(2))
+    x[rows], r[rows] = _dev(part), _dev(rpart)
+    w = rng.normal(size=k).astype(np.float16)
+    out, ro, sc = t.empty((m, k), dtype=t.int8, device="cuda"), t.empty_like(x), t.empty(m, device="cuda")
+    mnb.mnb_rms_norm(x, _dev(w), out, EPS, residual=r, residual_out=ro, scales=sc)
+    h, _ = o.rms_norm(part, rpart, w, EPS)
+    assert (ro[rows].cpu().numpy() == h).all()
+    _check_codes(G.host(out[rows]), G.host(sc[rows]), h, w, k, "f16")
+    mnb.mnb_rms_norm(x, _dev(w), ro, EPS, residual=r)
+    _, y = o.rms_norm(part, rpart, w, EPS)
+    assert (np.abs(G.host(ro[rows]) - y) <= _value_tolerance(y, k, "f16")).all()
+
+
 @pytest.mark.parametrize("M", [1, 2, 16, 17, 48, 70])
 def test_codes_into_the_int4_product(mnb, M):
     """norm -> codes -> product, against the exact product of the codes the GPU wrote."""
