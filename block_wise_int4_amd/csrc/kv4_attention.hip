@@ -519,7 +519,6 @@ __global__ __launch_bounds__(KW * 64, WPE) void kv4_attention_kernel(AttnParams 
 // in 16-byte loads; the workgroup's 4 to 16 such groups take one split in as many
 // and meet in LDS.  The weights are formed once, one split to a thread.
 constexpr int kJoinThreads = 256;
-constexpr int kMaxSplits = 512;
 
 template <int D, bool F32>
 __global__ __launch_bounds__(kJoinThreads) void kv4_join_kernel(AttnParams p)
@@ -592,48 +591,6 @@ __global__ __launch_bounds__(kJoinThreads) void kv4_join_kernel(AttnParams p)
         static_cast<T*>(p.out)[row * D + tid] = (T)(y * inv);
     }
     if (p.lse && tid == 0) p.lse[row] = log_sum(m, sum);
-}
-
-Plan plan_of(const AttentionArgs& a)
-{
-    Plan c = {};
-    const int64_t rows = a.max_q * (a.v.q_heads / a.v.kv_heads);
-    const bool wide = a.v.head_dim == 256;
-    int64_t least, want;                       // keys that keep every wave busy; workgroups that fill the chip
-    if (rows <= (wide || a.v.groups > 2 ? 16 : 32)) {   // two column tiles where the registers hold them
-        // few rows: the waves of a workgroup cut the keys between them
-        c.group = rows <= 4 ? 4 : rows <= 8 ? 2 : rows <= 16 ? 1 : 0;
-        c.rows = c.group ? 16 / c.group : 32;
-        // up to 1024 keys one workgroup of 8 waves does without the join
-        c.kind = !wide && a.v.groups <= 2 && c.group && a.max_kv <= 1024 ? 0 : 1;
-        least = 256;
-        // one sequence: its pieces are alike, and two workgroups a CU in one round
-        // are best (131072 keys: 34 us with 512, 44 with 2048); several of unknown
-        // lengths: more and shorter pieces even them out (32 sequences of up to 8192 keys:
-        // 45 us with 512, 41 with 3072)
-        want = a.v.batch == 1 ? 512 : 3072;
-    } else {
-        c.kind = 2;
-        // two column tiles a wave where that leaves a workgroup for every CU (1000
-        // rows of 32 key heads: 90 us with two, 34 with one; 2048 and 1100 tokens of 8
-        // key heads by 4: 233 us with two, 306 with one) and the registers hold them
-        const int64_t wgs = (rows + 255) / 256 * a.v.kv_heads * a.v.batch;
-        c.tiles = wide || a.v.groups > 2 || wgs < 256 ? 1 : 2;
-        c.rows = kPromptWaves * 16 * c.tiles;
-        least = 256;
-        want = 256;
-    }
-    c.row_tiles = (int)((rows + c.rows - 1) / c.rows);
-    const int64_t units = (int64_t)c.row_tiles * a.v.kv_heads * a.v.batch;
-    const int64_t most = (a.max_kv + least - 1) / least;
-    int64_t splits = c.kind == 0 ? 1 : (want + units - 1) / units;
-    splits = splits > most ? most : splits;
-    splits = splits > kMaxSplits ? kMaxSplits : splits < 1 ? 1 : splits;
-    c.chunk = (int)(((a.max_kv + splits - 1) / splits + least - 1) / least * least);
-    if (c.chunk < least) c.chunk = (int)least;
-    c.splits = (int)((a.max_kv + c.chunk - 1) / c.chunk);
-    if (c.splits < 1) c.splits = 1;
-    return c;
 }
 
 template <int D, int NG, bool F32, int GRP, int NR, int KW>

@@ -4,6 +4,7 @@
 
 #include <type_traits>
 
+#include "kv4_plan.hpp"
 #include "mnb_device.hpp"
 #include "mnb_kv4.hpp"
 
@@ -34,18 +35,8 @@ struct AttnParams {
     int row_tiles, rows_per_wg;
 };
 
-// How a call is cut.
-struct Plan {
-    int kind;                         // 0: one workgroup a row set; 1: few rows; 2: many rows
-    int group;                        // few rows: column groups (4, 2, 1), 0 for two row tiles
-    int tiles;                        // many rows: column tiles of a wave
-    int rows;                         // rows per workgroup
-    int row_tiles, splits, chunk;
-};
-
 hipError_t launch_prompt(const AttnParams& p, const Plan& c, int f16, hipStream_t s);
 hipError_t launch_join(const AttnParams& p, int f16, hipStream_t s);
-constexpr int kPromptWaves = 8;
 
 typedef uint16_t us2_t __attribute__((ext_vector_type(2)));
 
