@@ -518,14 +518,14 @@ __global__ __launch_bounds__(KW * 64, WPE) void kv4_attention_kernel(AttnParams 
 // Joins the splits of one (token, head).  D / 4 lanes take one split's partial
 // in 16-byte loads; the workgroup's 4 to 16 such groups take one split in as many
 // and meet in LDS.  The weights are formed once, one split to a thread.
+constexpr int kJoinThreads = 256;
 
-template <int D, bool F32, int kJoinThreads>
+template <int D, bool F32>
 __global__ __launch_bounds__(kJoinThreads) void kv4_join_kernel(AttnParams p)
 {
-    constexpr int kPer = kJoinThreads == 64 ? 1 : kMaxSplits / kJoinThreads;   // splits of a thread
     typedef typename std::conditional<F32, float, _Float16>::type T;
     constexpr int LPR = D / 4, GR = kJoinThreads / LPR;
-    __shared__ float wgt[kPer * kJoinThreads];
+    __shared__ float wgt[kMaxSplits];
     __shared__ float red[2][kJoinThreads / 64];
     __shared__ __align__(16) float sums[GR][D];
     const KvView& v = p.v;
@@ -546,9 +546,9 @@ __global__ __launch_bounds__(kJoinThreads) void kv4_join_kernel(AttnParams p)
     const int64_t step = (int64_t)v.tokens * v.q_heads;
 
     const float* ml = p.part_ml + 2 * (s0 * step + row);
-    float M[kPer], L[kPer], m = kLow;
+    float M[kMaxSplits / kJoinThreads], L[kMaxSplits / kJoinThreads], m = kLow;
 #pragma unroll
-    for (int k = 0; k < kPer; ++k) {
+    for (int k = 0; k < kMaxSplits / kJoinThreads; ++k) {
         const int at = k * kJoinThreads + tid;
         M[k] = at < n ? ml[2 * at * step] : kLow;
         L[k] = at < n ? ml[2 * at * step + 1] : 0.0f;
@@ -562,7 +562,7 @@ __global__ __launch_bounds__(kJoinThreads) void kv4_join_kernel(AttnParams p)
     for (int k = 0; k < kJoinThreads / 64; ++k) m = fmaxf(m, red[0][k]);
     float sum = 0.0f;
 #pragma unroll
-    for (int k = 0; k < kPer; ++k) {
+    for (int k = 0; k < kMaxSplits / kJoinThreads; ++k) {
         const int at = k * kJoinThreads + tid;
         const float w = exp2f(M[k] - m);
         if (at < n) wgt[at] = w;
@@ -579,16 +579,16 @@ __global__ __launch_bounds__(kJoinThreads) void kv4_join_kernel(AttnParams p)
     const int g = tid / LPR, d = tid % LPR * 4;
     const float* o = p.part_o + (s0 * step + row) * D + d;
     f4_t a = {0.0f, 0.0f, 0.0f, 0.0f};
-#pragma unroll 8
+#pragma unroll 4
     for (int k = g; k < n; k += GR) a += *reinterpret_cast<const f4_t*>(o + k * step * D) * wgt[k];
     *reinterpret_cast<f4_t*>(&sums[g][d]) = a;
     __syncthreads();
-    for (int e = tid; e < D; e += kJoinThreads) {
+    if (tid < D) {
         float y = 0.0f;
 #pragma unroll
-        for (int k = 0; k < GR; ++k) y += sums[k][e];
+        for (int k = 0; k < GR; ++k) y += sums[k][tid];
         const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
-        static_cast<T*>(p.out)[row * D + e] = (T)(y * inv);
+        static_cast<T*>(p.out)[row * D + tid] = (T)(y * inv);
     }
     if (p.lse && tid == 0) p.lse[row] = log_sum(m, sum);
 }
@@ -648,15 +648,8 @@ hipError_t launch_few_rows(const AttnParams& p, const Plan& c, int f16, hipStrea
 template <int D> hipError_t launch_join_dim(const AttnParams& p, int f16, hipStream_t s)
 {
     const dim3 grid((unsigned)(p.max_q * p.v.q_heads), (unsigned)p.v.batch);
-    // up to 32 splits one wave joins a row without waiting for others (17 splits of
-    // 960 rows: XX us against YY)
-    if (p.splits <= 32) {
-        if (f16) kv4_join_kernel<D, false, 64><<<grid, dim3(64), 0, s>>>(p);
-        else kv4_join_kernel<D, true, 64><<<grid, dim3(64), 0, s>>>(p);
-    } else {
-        if (f16) kv4_join_kernel<D, false, 256><<<grid, dim3(256), 0, s>>>(p);
-        else kv4_join_kernel<D, true, 256><<<grid, dim3(256), 0, s>>>(p);
-    }
+    if (f16) kv4_join_kernel<D, false><<<grid, dim3(kJoinThreads), 0, s>>>(p);
+    else kv4_join_kernel<D, true><<<grid, dim3(kJoinThreads), 0, s>>>(p);
     return hipGetLastError();
 }
 
