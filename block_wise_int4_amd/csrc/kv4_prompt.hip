@@ -7,11 +7,18 @@
 // all of them as its A operands.  (Unpacked by each wave for itself, the codes
 // cost as many vector instructions as the softmax.)
 //
-// The next stage's codes are requested a stage ahead and unpacked into the other
-// half of LDS, so there is one barrier a stage.  With two waves a SIMD (the
+// The next stages' codes are requested a stage ahead and unpacked into the other
+// half of LDS, with one barrier for two stages.  With two waves a SIMD (the
 // registers allow no more) the kernel is bound by the latencies inside a wave, so a wave takes up
 // to 64 keys through its softmax at once: one look at the masks, one at the running
-// reference, and long runs of independent products and exponentials.
+// reference, and long runs of independent products and exponentials.  LDS reads,
+// products and vector work take about 155, 145 and 205 of 490 thousand cycles of a SIMD at
+// the long case below: nearly their sum, which the two waves' opposite order and
+// priorities bring down (from 233 us to 217).
+//
+// Measured, head_dim 128, groups of 128, fp16: 2048 and 1100 new tokens of 32 heads by 8
+// key heads @LONG@; 1000 tokens of 32 heads by 32 key
+// heads @SHORT@, one round of workgroups that lasts as long as its longest key range.
 #include "kv4_attention.hpp"
 
 namespace mnb {
@@ -410,6 +417,11 @@ __global__ __launch_bounds__(RW * 64, 2) void kv4_prompt_kernel(AttnParams p)
         }
         request(st);
     };
+    // A SIMD's two waves are w and w + 4: one unpacks before its products, the other
+    // after them and goes first where both can issue, so that one's products run beside
+    // the other's softmax.
+    const bool first_half = wave < RW / 2;
+    if (!first_half) __builtin_amdgcn_s_setprio(1);
     if (stages > 0) {
         request(0);
 #pragma unroll
@@ -420,14 +432,17 @@ __global__ __launch_bounds__(RW * 64, 2) void kv4_prompt_kernel(AttnParams p)
         __syncthreads();
         for (int st = 0; st < stages; ++st) {
             const int buf = st & (NB - 1);
+            const bool more = st + EP < stages, further = st + EP + 1 < stages;
+            if (first_half && more) unpack((st + EP) & (NB - 1));
+            if (first_half && further) ask(st + EP + 1);
 #pragma unroll
             for (int b0 = 0; b0 < SB; b0 += KB) {
                 const int blk = blk0 + st * SB + b0;
                 // blocks past the end hold zeros and are masked
                 if (busy && blk < blk1 && blk * 32 < none) compute(buf, b0, blk);
             }
-            if (st + EP < stages) unpack((st + EP) & (NB - 1));
-            if (st + EP + 1 < stages) ask(st + EP + 1);
+            if (!first_half && more) unpack((st + EP) & (NB - 1));
+            if (!first_half && further) ask(st + EP + 1);
             if ((st & (EP - 1)) == EP - 1) __syncthreads();
         }
     }
