@@ -515,11 +515,71 @@ __global__ __launch_bounds__(KW * 64, WPE) void kv4_attention_kernel(AttnParams 
     }
 }
 
-// Joins the splits of one (token, head).  D / 4 lanes take one split's partial
-// in 16-byte loads; the workgroup's 4 to 16 such groups take one split in as many
-// and meet in LDS.  The weights are formed once, one split to a thread.
-constexpr int kJoinThreads = 256;
+// The splits that wrote row h of token i: those with a key of its workgroup.
+// Returns how many, the first one in s0.
+__device__ __forceinline__ int splits_of(const AttnParams& p, const Sequence& s, int i, int h, int& s0)
+{
+    int lo, hi;
+    const int r = i * p.gqa + h % p.gqa;
+    const int rows = s.count * p.gqa;
+    const int r0 = r / p.rows_per_wg * p.rows_per_wg;
+    const int r1 = r0 + p.rows_per_wg <= rows ? r0 + p.rows_per_wg - 1 : rows - 1;
+    key_range(p, s, r0 / p.gqa, r1 / p.gqa, lo, hi);
+    s0 = lo / p.chunk;
+    return hi > lo ? (hi + p.chunk - 1) / p.chunk - s0 : 0;
+}
 
+constexpr int kJoinThreads = 256;
+constexpr int kWaveSplits = 16;       // most splits that a wave joins alone
+
+// Joins the splits of one (token, head), one wave to each: lane k forms split k's
+// weight, and D / 4 lanes take one split's partial in 16-byte loads.
+template <int D, bool F32>
+__global__ __launch_bounds__(kJoinThreads) void kv4_join_rows_kernel(AttnParams p)
+{
+    typedef typename std::conditional<F32, float, _Float16>::type T;
+    constexpr int LPR = D / 4, GR = 64 / LPR;
+    const KvView& v = p.v;
+    const int lane = threadIdx.x & 63;
+    const int at = uniform(blockIdx.x * (kJoinThreads / 64) + (threadIdx.x >> 6));
+    const int h = at % v.q_heads, i = at / v.q_heads;      // token of the sequence
+    const Sequence s = sequence_of(v, blockIdx.y, p.max_q, p.max_kv);
+    if (i >= s.count) return;
+    const int64_t row = (int64_t)(s.first + i) * v.q_heads + h;
+    int s0;
+    const int n = splits_of(p, s, i, h, s0);               // at most kWaveSplits
+    const int64_t step = (int64_t)v.tokens * v.q_heads;
+    const float* ml = p.part_ml + 2 * (s0 * step + row);
+    const float M = lane < n ? ml[2 * lane * step] : kLow;
+    const float L = lane < n ? ml[2 * lane * step + 1] : 0.0f;
+    float m = M;
+#pragma unroll
+    for (int off = 32; off > 0; off >>= 1) m = fmaxf(m, __shfl_xor(m, off));
+    const float w = exp2f(M - m);
+    float sum = L * w;
+#pragma unroll
+    for (int off = 32; off > 0; off >>= 1) sum += __shfl_xor(sum, off);
+
+    const int g = lane / LPR, d = lane % LPR * 4;
+    const float* o = p.part_o + (s0 * step + row) * D + d;
+    f4_t a = {0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll 4
+    for (int k0 = 0; k0 < n; k0 += GR) {
+        const int k = k0 + g;
+        const float wk = __shfl(w, k);
+        if (k < n) a += *reinterpret_cast<const f4_t*>(o + k * step * D) * wk;
+    }
+#pragma unroll
+    for (int off = LPR; off < 64; off <<= 1)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) a[e] += __shfl_xor(a[e], off);
+    const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
+    if (g == 0) store4(static_cast<T*>(p.out) + row * D + d, a, inv);
+    if (p.lse && lane == 0) p.lse[row] = log_sum(m, sum);
+}
+
+// The same with a workgroup to each: its 4 to 16 groups of D / 4 lanes take a split
+// each in turn and meet in LDS.  The weights are formed once, one split to a thread.
 template <int D, bool F32>
 __global__ __launch_bounds__(kJoinThreads) void kv4_join_kernel(AttnParams p)
 {
@@ -535,14 +595,8 @@ __global__ __launch_bounds__(kJoinThreads) void kv4_join_kernel(AttnParams p)
     const Sequence s = sequence_of(v, blockIdx.y, p.max_q, p.max_kv);
     if (i >= s.count) return;
     const int64_t row = (int64_t)(s.first + i) * v.q_heads + h;
-    // the splits that wrote this row: those with a key of its workgroup
-    int lo, hi;
-    const int r = i * p.gqa + h % p.gqa;
-    const int rows = s.count * p.gqa;
-    const int r0 = r / p.rows_per_wg * p.rows_per_wg;
-    const int r1 = r0 + p.rows_per_wg <= rows ? r0 + p.rows_per_wg - 1 : rows - 1;
-    key_range(p, s, r0 / p.gqa, r1 / p.gqa, lo, hi);
-    const int s0 = lo / p.chunk, n = hi > lo ? (hi + p.chunk - 1) / p.chunk - s0 : 0;
+    int s0;
+    const int n = splits_of(p, s, i, h, s0);
     const int64_t step = (int64_t)v.tokens * v.q_heads;
 
     const float* ml = p.part_ml + 2 * (s0 * step + row);
@@ -647,7 +701,17 @@ hipError_t launch_few_rows(const AttnParams& p, const Plan& c, int f16, hipStrea
 
 template <int D> hipError_t launch_join_dim(const AttnParams& p, int f16, hipStream_t s)
 {
-    const dim3 grid((unsigned)(p.max_q * p.v.q_heads), (unsigned)p.v.batch);
+    const unsigned rows = (unsigned)(p.max_q * p.v.q_heads), waves = kJoinThreads / 64;
+    // A wave a row up to 16 splits: 1200 rows of 8 splits 52 us with its attention kernel
+    // against 65, 9600 of 3 splits 89 against 102; past that the few rows there are leave
+    // the chip idle (16 splits of 128 rows and 64 of 32: 22.1 against 27.9, 32 against 39).
+    if (p.splits <= kWaveSplits) {
+        const dim3 grid((rows + waves - 1) / waves, (unsigned)p.v.batch);
+        if (f16) kv4_join_rows_kernel<D, false><<<grid, dim3(kJoinThreads), 0, s>>>(p);
+        else kv4_join_rows_kernel<D, true><<<grid, dim3(kJoinThreads), 0, s>>>(p);
+        return hipGetLastError();
+    }
+    const dim3 grid(rows, (unsigned)p.v.batch);
     if (f16) kv4_join_kernel<D, false><<<grid, dim3(kJoinThreads), 0, s>>>(p);
     else kv4_join_kernel<D, true><<<grid, dim3(kJoinThreads), 0, s>>>(p);
     return hipGetLastError();

@@ -24,14 +24,14 @@ inline Plan plan_of(const AttentionArgs& a)
     Plan c = {};
     const int64_t rows = a.max_q * (a.v.q_heads / a.v.kv_heads);
     const bool wide = a.v.head_dim == 256;
-    int64_t least, want;                       // keys that keep every wave busy; workgroups that fill the chip
+    // keys worth a split, in steps of grain; workgroups that fill the chip
+    int64_t least = 256, grain = 256, want;
     if (rows <= (wide || a.v.groups > 2 ? 16 : 32)) {   // two column tiles where the registers hold them
         // few rows: the waves of a workgroup cut the keys between them
         c.group = rows <= 4 ? 4 : rows <= 8 ? 2 : rows <= 16 ? 1 : 0;
         c.rows = c.group ? 16 / c.group : 32;
         // up to 1024 keys one workgroup of 8 waves does without the join
         c.kind = !wide && a.v.groups <= 2 && c.group && a.max_kv <= 1024 ? 0 : 1;
-        least = 256;
         // one sequence: its pieces are alike, and two workgroups a CU in one round
         // are best (131072 keys: 34 us with 512, 44 with 2048); several of unknown
         // lengths: more and shorter pieces even them out (32 sequences of up to 8192 keys:
@@ -45,17 +45,22 @@ inline Plan plan_of(const AttentionArgs& a)
         const int64_t wgs = (rows + 255) / 256 * a.v.kv_heads * a.v.batch;
         c.tiles = wide || a.v.groups > 2 || wgs < 256 ? 1 : 2;
         c.rows = kPromptWaves * 16 * c.tiles;
-        least = 256;
+        // one workgroup a CU, so splits that make a second round gain nothing (800 new
+        // tokens of 8000 keys, 200 workgroups: 196 us whole, 271 in two)
         want = 256;
+        // and many rows' partials cost as much as some hundred keys (300 tokens of 32 heads,
+        // no prefix: 14.8 us whole, 21 in two; 33 tokens with 1000 keys: 17 us in four, 23 in two)
+        least = a.max_q * a.v.q_heads * a.v.batch <= 4096 ? 256 : 512;
+        grain = 128;                           // a stage of the kernel, or more
     }
     c.row_tiles = (int)((rows + c.rows - 1) / c.rows);
     const int64_t units = (int64_t)c.row_tiles * a.v.kv_heads * a.v.batch;
     const int64_t most = (a.max_kv + least - 1) / least;
-    int64_t splits = c.kind == 0 ? 1 : (want + units - 1) / units;
+    int64_t splits = c.kind == 0 ? 1 : c.kind == 1 ? (want + units - 1) / units : want / units;
     splits = splits > most ? most : splits;
     splits = splits > kMaxSplits ? kMaxSplits : splits < 1 ? 1 : splits;
-    c.chunk = (int)(((a.max_kv + splits - 1) / splits + least - 1) / least * least);
-    if (c.chunk < least) c.chunk = (int)least;
+    c.chunk = (int)(((a.max_kv + splits - 1) / splits + grain - 1) / grain * grain);
+    if (c.chunk < grain) c.chunk = (int)grain;
     c.splits = (int)((a.max_kv + c.chunk - 1) / c.chunk);
     if (c.splits < 1) c.splits = 1;
     return c;

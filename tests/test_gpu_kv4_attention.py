@@ -110,6 +110,33 @@ def test_against_the_oracle(mnb, case, mask, dt):
           window=37 if mask == "window" else 0)
 
 
+SPLIT = [  # D, group, q heads, kv heads, new tokens, cached with them
+    (128, 128, 4, 2, [1, 1], [1500, 300]),           # few rows, up to 16 splits
+    (64, 64, 2, 1, [3], [4900]),                     # few rows, more
+    (256, 64, 4, 1, [1, 2, 0], [5100, 33, 0]),
+    (128, 64, 3, 1, [40, 2], [1300, 700]),           # many rows, up to 16
+    (64, 32, 2, 1, [35], [4500]),                    # many rows, more
+    (256, 128, 2, 1, [20], [4400]),
+    (128, 128, 8, 8, [520, 3], [1100, 1099]),        # so many that a split takes 512 keys
+]
+
+
+@pytest.mark.parametrize("dt", ["f16", "f32"])
+@pytest.mark.parametrize("mask", ["causal", "full", "window"])
+@pytest.mark.parametrize("case", SPLIT, ids=["-".join(map(str, c[:4] + (c[4][0], c[5][0]))) for c in SPLIT])
+def test_keys_shared_between_workgroups(mnb, case, mask, dt):
+    """Every form of the join: the splits of a row hold all, some or none of its keys."""
+    D, group, H, Hkv, new, lens = case
+    rng = np.random.default_rng((939, D, H, lens[0]))
+    table, pages = sequences(rng, lens, 64)
+    geo = o.Geometry(H, Hkv, D, group, 64, pages)
+    cache, vmax = make_cache(rng, geo, table, lens)
+    q_start = np.concatenate([[0], np.cumsum(new)])
+    q = (1.5 * rng.normal(size=(q_start[-1], H, D))).astype(np.float16 if dt == "f16" else np.float32)
+    check(mnb, geo, cache, vmax, table, lens, q_start, q, D ** -0.5, causal=mask != "full",
+          window=600 if mask == "window" else 0)
+
+
 @pytest.mark.parametrize("dt", ["f16", "f32"])
 def test_rows_that_see_nothing(mnb, dt):
     """Empty sequences, new tokens before position 0, and rows beside them that see keys."""
