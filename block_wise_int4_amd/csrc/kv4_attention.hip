@@ -35,6 +35,15 @@
 // Work split: the waves of a workgroup share the keys of one set of rows (joined
 // through LDS), and `splits` workgroups share a sequence's keys (joined by a second
 // kernel over fp32 partials), so that a few long sequences fill the chip.
+//
+// Measured, head_dim 128, fp16, 8 key heads by 4: 32 sequences of up to 8192 keys 42 us and
+// 5.5 for the join (182 MB: 4.3 TB/s without the join, where a large copy moves 5.15);
+// one of 131072 keys with groups of 64, 30.8 and 4.7 us (151 MB: 4.9 TB/s); one of 1000 keys
+// 10 us, without a join: launch, the chain to the first block, one round trip (a wave asks
+// for its 4 blocks at once), their softmax and the join in LDS.
+// 8 sequences of 5 new tokens, 3 heads to a key head, a window of 3000 keys, in fp32 at
+// head_dim 64, 12.0 and 4.5 us: bound by the latency of
+// the chain to the first block, two blocks' work a wave, and the second launch.
 #include "kv4_attention.hpp"
 
 namespace mnb {

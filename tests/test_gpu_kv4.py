@@ -179,6 +179,33 @@ def test_many_sequences_are_found(mnb):
     assert (cache.cpu().numpy() == want).all()
 
 
+@pytest.mark.parametrize("new", [[511], [512], [513], [700, 1, 600]])
+def test_prompts_longer_than_a_round_of_workgroups(mnb, new):
+    """Every token is taken once where runs of them go to one XCD, and those past the last whole round."""
+    t = G.torch()
+    rng = np.random.default_rng((926, sum(new)))
+    lens = np.array([n + 5 for n in new], np.int32)
+    table, pages = sequences(rng, [int(n) for n in lens], 32)
+    geo = o.Geometry(2, 1, 64, 64, 32, pages)
+    q_start = np.concatenate([[0], np.cumsum(new)]).astype(np.int32)
+    T = int(q_start[-1])
+    q, k, v = (rng.normal(size=(T, h, 64)).astype(np.float16) for h in (2, 1, 1))
+    want = np.zeros(geo.bytes, np.uint8)
+    o.append(geo, want, table, lens, q_start, k, v)
+    cache = dev(np.zeros(geo.bytes, np.uint8))
+    q_out = t.full((T, 2, 64), 9.0, dtype=t.float16, device="cuda")
+    seq = (dev(table), dev(lens), dev(q_start))
+    mnb.mnb_kv4_append(desc_of(mnb, geo), cache, dev(k), dev(v), *seq, q=dev(q), q_out=q_out)
+    assert (cache.cpu().numpy() == want).all() and (q_out.cpu().numpy() == q).all()
+    ko, vo = (t.full((T, 1, 64), 9.0, dtype=t.float16, device="cuda") for _ in range(2))
+    mnb.mnb_kv4_read(desc_of(mnb, geo), cache, *seq, ko, vo)
+    for b in range(len(new)):
+        K, V = o.gather(geo, want, table[b], 0, int(lens[b]))
+        rows = slice(q_start[b], q_start[b + 1])
+        assert (ko[rows, 0].cpu().numpy() == K[5:].astype(np.float16)).all()
+        assert (vo[rows, 0].cpu().numpy() == V[5:].astype(np.float16)).all()
+
+
 def test_pages_past_four_gigabytes(mnb):
     """A page whose offset passes 32 bits."""
     t = G.torch()
