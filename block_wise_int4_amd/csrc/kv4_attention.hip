@@ -36,8 +36,8 @@
 // through LDS), and `splits` workgroups share a sequence's keys (joined by a second
 // kernel over fp32 partials), so that a few long sequences fill the chip.
 //
-// Measured, head_dim 128, fp16, 8 key heads by 4: 32 sequences of up to 8192 keys 42 us and
-// 5.5 for the join (182 MB: 4.3 TB/s without the join, where a large copy moves 5.15);
+// Measured, head_dim 128, fp16, 8 key heads by 4: 32 sequences of up to 8192 keys 43.7 us and
+// 5.5 for the join (182 MB: 4.2 TB/s without the join, where a large copy moves 5.15);
 // one of 131072 keys with groups of 64, 30.8 and 4.7 us (151 MB: 4.9 TB/s); one of 1000 keys
 // 10 us, without a join: launch, the chain to the first block, one round trip (a wave asks
 // for its 4 blocks at once), their softmax and the join in LDS.

@@ -248,6 +248,8 @@ __global__ __launch_bounds__(1024) void rms_norm_kernel(NormParams p)
 template <typename T, int OUT>
 hipError_t launch_out(const NormArgs& a, NormParams p, hipStream_t s)
 {
+    // 16 bytes a thread of up to 512, of longer rows two or four times that; the registers
+    // of four hold 16384 fp16 or 8192 fp32 elements, and what is left is read twice
     const int64_t nv = a.k / Vec<T>::N;
     const int threads = (int)(nv < 64 ? 64 : nv > 512 ? 512 : (nv + 63) / 64 * 64);
     constexpr int64_t kRows = 1 << 22;     // of a launch: a grid holds less than 2^32 threads
