@@ -100,17 +100,19 @@ struct Place {
     int key;                  // token's place in its block
 };
 
-// Where a token of the workgroup is kept.  Page numbers and positions outside
-// their ranges give no page.
+// Where a token of the workgroup is kept.  Rows of no sequence have no position,
+// and page numbers and positions outside their ranges give no page.
 __device__ __forceinline__ Place place_of(const KvView& v, int token, int64_t block_bytes)
 {
     Place r{-1, nullptr, 0};
     int b = token, behind = 1;    // tokens of the sequence from this one on
     if (v.q_start) {
         b = find_sequence(v.q_start, v.batch, token, threadIdx.x & 63);
-        if (b < v.batch) behind = v.q_start[b + 1] - token;
+        if (b >= v.batch) return r;
+        const int first = v.q_start[b], end = v.q_start[b + 1];
+        if (token < first || token >= end) return r;   // before the first sequence, or offsets that decrease
+        behind = end - token;
     }
-    if (b >= v.batch) return r;
     r.pos = (int64_t)v.kv_len[b] - behind;
     if (r.pos < 0) return r;
     const int64_t page_at = r.pos >> v.page_shift;

@@ -433,6 +433,8 @@ size_t mnb_kv4_cache_bytes(const mnb_kv4_desc* c);
  *   kv_len [batch]: tokens of each sequence, the new ones included.
  *   q_start [batch + 1]: rows of the new tokens, q_start[b] .. q_start[b+1]-1 for
  *     sequence b, non-decreasing; NULL: one each, row b (then tokens == batch).
+ *     Rows before q_start[0] and from q_start[batch] on belong to no sequence, so
+ *     a part of a batch may be given by its offsets into the whole arrays.
  * A sequence with n new tokens has them at positions kv_len - n .. kv_len - 1. */
 
 /* Append: for each new token (row of q, k, v) the keys are rotated by their
@@ -447,8 +449,9 @@ size_t mnb_kv4_cache_bytes(const mnb_kv4_desc* c);
  * quantized from binary32.  A position past rope_rows uses the last row.  A
  * token whose position is negative, past the table or on a page outside
  * 0..num_pages-1 is not stored (padding may use page -1).  Two tokens of one
- * call must not share a place.  Rows past q_start[batch] are ignored but for
- * q_out, which gets them rotated by position 0.  tokens < 2^24. */
+ * call must not share a place.  Rows of no sequence are ignored but for q_out,
+ * which gets them rotated by position 0.  tokens < 2^24; tokens == 0 or batch ==
+ * 0 is a no-op. */
 mnb_status mnb_kv4_append(const mnb_kv4_desc* c, void* cache, const int32_t* block_table, int64_t table_stride,
                           const int32_t* kv_len, const int32_t* q_start, int64_t batch, int64_t tokens,
                           int32_t dtype, const void* q, int64_t q_stride, const void* k, int64_t k_stride,
@@ -457,8 +460,9 @@ mnb_status mnb_kv4_append(const mnb_kv4_desc* c, void* cache, const int32_t* blo
 
 /* Read: the stored keys and values of the same rows as values, k_out and v_out
  * [tokens, kv_heads, head_dim] of dtype (either may be NULL), each (c - z) * s
- * rounded once; zeros for a token that has no place.  With n = kv_len the whole
- * sequence is read. */
+ * rounded once; zeros for a token that has no place (rows of no sequence are
+ * such).  With n = kv_len the whole sequence is read.  tokens == 0 or batch == 0
+ * is a no-op. */
 mnb_status mnb_kv4_read(const mnb_kv4_desc* c, const void* cache, const int32_t* block_table, int64_t table_stride,
                         const int32_t* kv_len, const int32_t* q_start, int64_t batch, int64_t tokens,
                         int32_t dtype, void* k_out, void* v_out, void* stream);
