@@ -4,6 +4,7 @@
 
 #include <type_traits>
 
+#include "kv4_index.hpp"
 #include "kv4_plan.hpp"
 #include "mnb_device.hpp"
 #include "mnb_kv4.hpp"
@@ -60,32 +61,6 @@ __device__ __forceinline__ float top_exponent(uint32_t word) { return (float)((i
 __device__ __forceinline__ uint32_t max_halves(uint32_t a, uint32_t b)
 {
     return __builtin_bit_cast(uint32_t, __builtin_elementwise_max(__builtin_bit_cast(us2_t, a), __builtin_bit_cast(us2_t, b)));
-}
-
-// Length and new tokens of a sequence, within the bounds of the call.
-struct Sequence {
-    int len, first, count;            // keys; first row and number of new tokens that are computed
-    int before;                       // position of the first new token
-};
-__device__ __forceinline__ Sequence sequence_of(const KvView& v, int b, int max_q, int max_kv)
-{
-    Sequence s;
-    int64_t room = v.table_stride << v.page_shift;
-    int len = v.kv_len[b];
-    len = len < 0 ? 0 : len > max_kv ? max_kv : len;
-    s.len = (int64_t)len > room ? (int)room : len;
-    int first = b, end = b + 1;
-    if (v.q_start) {
-        first = v.q_start[b];
-        end = v.q_start[b + 1];
-    }
-    s.before = s.len - (end - first);
-    first = first < 0 ? 0 : first;
-    end = end > v.tokens ? v.tokens : end;
-    int n = end - first;
-    s.first = first;
-    s.count = n < 0 ? 0 : n > max_q ? max_q : n;
-    return s;
 }
 
 // The keys rows of tokens i0..i1 of a sequence can see: [lo, hi).

@@ -1,0 +1,39 @@
+// kv4_index.hpp -- which rows and keys belong to a sequence: arithmetic on
+// values of device memory, which may hold anything.  The same code on the host,
+// where it is tested over the values' whole range.
+#pragma once
+
+#include "mnb_kv4.hpp"
+
+namespace mnb {
+namespace kv4 {
+
+// Length and new tokens of a sequence, within the bounds of the call.
+struct Sequence {
+    int len, first, count;            // keys; first row and number of new tokens that are computed
+    int before;                       // position of the first new token
+};
+__host__ __device__ __forceinline__ Sequence sequence_of(const KvView& v, int b, int max_q, int max_kv)
+{
+    Sequence s;
+    // a cache without pages holds no keys (elsewhere a page out of range is read as page 0)
+    const int64_t room = v.num_pages > 0 ? v.table_stride << v.page_shift : 0;
+    int len = v.kv_len[b];
+    len = len < 0 ? 0 : len > max_kv ? max_kv : len;
+    s.len = (int64_t)len > room ? (int)room : len;
+    int first = b, end = b + 1;
+    if (v.q_start) {
+        first = v.q_start[b];
+        end = v.q_start[b + 1];
+    }
+    s.before = s.len - (end - first);
+    first = first < 0 ? 0 : first;
+    end = end > v.tokens ? v.tokens : end;
+    int n = end - first;
+    s.first = first;
+    s.count = n < 0 ? 0 : n > max_q ? max_q : n;
+    return s;
+}
+
+}  // namespace kv4
+}  // namespace mnb

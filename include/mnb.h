@@ -390,7 +390,8 @@ mnb_status mnb_gemm_accuracy4_codes(const mnb_weight_desc* w, const void* repack
 /* The 4-bit cache of one layer.  q_heads % kv_heads == 0 (query heads
  * h*q_heads/kv_heads .. share key head h); head_dim 64, 128 or 256; group_size
  * 32, 64 or 128 and at most head_dim; head_dim / group_size at most 8;
- * page_size 32, 64, 128 or 256 tokens (else MNB_ERR_UNSUPPORTED).
+ * page_size 32, 64, 128 or 256 tokens (else MNB_ERR_UNSUPPORTED).  A cache of
+ * num_pages 0 holds no token: nothing is stored, and rows see no key.
  *
  * A group of group_size consecutive values of one token and head is stored as
  * 4-bit codes c, an fp16 scale s and a zero point z in 0..15, and stands for

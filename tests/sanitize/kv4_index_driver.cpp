@@ -1,0 +1,51 @@
+// Host-side run, under AddressSanitizer and UndefinedBehaviorSanitizer, of the
+// arithmetic that the cache's and the attention's kernels do on lengths and
+// offsets from device memory: whatever these hold, rows and keys stay inside
+// the call's arrays.  Built as plain C++.
+#include <cstdio>
+#include <cstring>
+#include <vector>
+
+#include "kv4_index.hpp"
+
+using namespace mnb;
+
+static int failures = 0;
+static void expect(bool good, const char* what)
+{
+    if (!good && ++failures < 20) std::printf("FAIL %s\n", what);
+}
+
+static KvView view(const int32_t* kv_len, const int32_t* q_start, int batch, int tokens, int64_t table_stride, int num_pages)
+{
+    KvView v = {};
+    v.kv_len = kv_len;
+    v.q_start = q_start;
+    v.batch = batch;
+    v.tokens = tokens;
+    v.table_stride = table_stride;
+    v.page_shift = 5;
+    v.num_pages = num_pages;
+    return v;
+}
+
+// A cache without pages has no keys, whatever the lengths say.
+static void no_pages()
+{
+    const int32_t lens[] = {100, 1, INT32_MAX, 0, -3};
+    for (int b = 0; b < 5; ++b) {
+        const kv4::Sequence s = kv4::sequence_of(view(lens, nullptr, 5, 5, 40, 0), b, 1, 1000);
+        expect(s.len == 0 && s.first == b && s.count == 1 && s.before == -1, "no pages");
+        const kv4::Sequence one = kv4::sequence_of(view(lens, nullptr, 5, 5, 40, 1), b, 1, 1000);
+        expect(one.len == (lens[b] < 0 ? 0 : lens[b] < 1000 ? lens[b] : 1000), "a page");
+    }
+}
+
+int main(int argc, char** argv)
+{
+    struct { const char* name; void (*run)(); } parts[] = {{"no_pages", no_pages}};
+    for (auto& p : parts)
+        if (argc < 2 || !std::strcmp(argv[1], p.name)) p.run();
+    std::printf("%s: %d failures\n", failures ? "FAILED" : "ok", failures);
+    return failures ? 1 : 0;
+}
