@@ -41,9 +41,37 @@ static void no_pages()
     }
 }
 
+// Offsets of any two values: rows inside the call's, none where the offsets
+// decrease, positions by the formula as far as 32 bits hold them.
+static void offsets()
+{
+    const int32_t v[] = {INT32_MIN, INT32_MIN + 1, INT32_MIN + 7, -(1 << 30), -100, -1, 0, 1, 5, 60, 99, 100, 101, 1 << 30,
+                         INT32_MAX - 1, INT32_MAX};
+    const int32_t lens[] = {INT32_MIN, -1, 0, 1, 77, 1 << 30, INT32_MAX};
+    for (int32_t len : lens)
+        for (int32_t first : v)
+            for (int32_t end : v)
+                for (int max_q : {1, 40, (1 << 29) - 1})
+                    for (int max_kv : {0, 50, 1 << 30}) {
+                        const int32_t q_start[] = {first, end};
+                        const int tokens = 100;
+                        const kv4::Sequence s = kv4::sequence_of(view(&len, q_start, 1, tokens, 1 << 26, 9), 0, max_q, max_kv);
+                        expect(s.len >= 0 && s.len <= max_kv, "length");
+                        expect(s.count >= 0 && s.count <= max_q, "count");
+                        expect(s.count == 0 || (s.first >= 0 && s.first + s.count <= tokens), "rows");
+                        expect(first < end || s.count == 0, "decreasing offsets");
+                        expect(s.before >= -(1 << 30) && s.before <= s.len, "position");
+                        if (first >= 0 && end >= first && end <= tokens) {
+                            expect(s.before == s.len - (end - first), "the formula");
+                            expect(s.count == (end - first < max_q ? end - first : max_q), "all rows");
+                            expect(s.count == 0 || s.first == first, "first row");
+                        }
+                    }
+}
+
 int main(int argc, char** argv)
 {
-    struct { const char* name; void (*run)(); } parts[] = {{"no_pages", no_pages}};
+    struct { const char* name; void (*run)(); } parts[] = {{"no_pages", no_pages}, {"offsets", offsets}};
     for (auto& p : parts)
         if (argc < 2 || !std::strcmp(argv[1], p.name)) p.run();
     std::printf("%s: %d failures\n", failures ? "FAILED" : "ok", failures);

@@ -4,8 +4,8 @@ import pytest
 
 from oracle import decoder as o
 from tests import gpu_util as G
-from tests.test_gpu_kv4 import desc_of, dev
-from tests.test_gpu_kv4_attention import attend
+from tests.test_gpu_kv4 import desc_of, dev, sequences
+from tests.test_gpu_kv4_attention import attend, make_cache
 
 pytestmark = pytest.mark.gpu
 
@@ -26,3 +26,32 @@ def test_a_cache_without_pages_holds_no_keys(mnb, new, max_kv, dt):
     q = rng.normal(size=(2 * new, 2, 64)).astype(np.float16 if dt == "f16" else np.float32)
     out, lse = attend(mnb, geo, np.zeros(256, np.uint8), table, [60, 90], [0, new, 2 * new], q, 0.1, max_kv=max_kv)
     assert (G.host(out) == 0).all() and np.isneginf(G.host(lse)).all()
+
+
+@pytest.mark.parametrize("new,max_kv", [(2, 120), (2, 5000), (40, 120), (40, 5000)])
+@pytest.mark.parametrize("rest", [[(1 << 31) - 1, -(1 << 31)], [-(1 << 31), -(1 << 31)], [(1 << 31) - 1, -7],
+                                  [(1 << 31) - 1, (1 << 31) - 1]])
+def test_offsets_of_any_value_stay_inside(mnb, rest, new, max_kv):
+    """Offsets that decrease or lie far outside the rows: the sequence before them is as it should be, and rows of no
+    sequence and what lies about the outputs stay as they were."""
+    t = G.torch()
+    rng = np.random.default_rng(981)
+    lens = [100, 120, 60]
+    table, pages = sequences(rng, lens, 32)
+    geo = o.Geometry(4, 2, 128, 64, 32, pages)
+    cache, vmax = make_cache(rng, geo, table, lens)
+    T = new + 3
+    q = rng.normal(size=(T, 4, 128)).astype(np.float16)
+    start = np.array([0, new] + rest, np.int64)
+    d = desc_of(mnb, geo)
+    n = mnb.mnb_attention_kv4_workspace_bytes(d, 3, T, new, max_kv)
+    ws = t.empty(max(n, 16), dtype=t.uint8, device="cuda")
+    buf = t.full((3, T, 4, 128), 7.0, dtype=t.float16, device="cuda")
+    mnb.mnb_attention_kv4(d, dev(cache), dev(q), dev(table), dev(np.array(lens, np.int32)), dev(start.astype(np.int32)), new,
+                          max_kv, buf[1], 0.1, workspace=ws, workspace_bytes=n)
+    w, _, size, reach = o.attention(geo, cache, table, lens[:1], [0, new], q, 0.1)
+    got = G.host(buf)
+    assert (np.abs(got[1, :new] - w[:new]) <= o.attention_tolerance(size, reach, 120, 128, True, vmax)[:new]).all()
+    assert (got[[0, 2]] == 7.0).all()
+    if rest[0] < 0:                                    # no offsets past the first sequence lead to a row
+        assert (got[1, new:] == 7.0).all()
