@@ -24,6 +24,7 @@
 // groups of 64, 52 us (append, 204 MB: 3.9 TB/s, where a large copy moves 5.15; the values'
 // single bytes are four stores a lane) and 18.9 us (read); one token of each of 16
 // sequences 4.6 and 3.2 us, the chain's latency.
+#include "kv4_index.hpp"
 #include "mnb_device.hpp"
 #include "mnb_kv4.hpp"
 
@@ -70,16 +71,13 @@ __device__ __forceinline__ void store8(float* p, const float* f)
 // whose tokens all come before it (batch when the token is past the last).
 __device__ __forceinline__ int find_sequence(const int32_t* q_start, int batch, int token, int lane)
 {
-    int lo = 0, n = batch;
-    while (n > 0) {
-        const int step = (n + 63) / 64;
-        const int at = lo + (lane + 1) * step;       // ends of sequences lo .. at - 1
-        const bool before = at <= lo + n && q_start[at <= batch ? at : batch] <= token;
-        const int left = lo + n;
-        lo += __builtin_popcountll(__builtin_amdgcn_ballot_w64(before)) * step;
-        n = left - lo < step - 1 ? left - lo : step - 1;
+    kv4::Search s = kv4::search_of(batch);
+    while (s.n > 0) {
+        const uint32_t at = s.at(lane);
+        const bool before = s.holds(at) && q_start[at] <= token;
+        s.keep(__builtin_popcountll(__builtin_amdgcn_ballot_w64(before)));
     }
-    return uniform(lo);
+    return uniform((int)s.lo);
 }
 
 // The token of a workgroup.  A token's codes are single bytes and words of lines that

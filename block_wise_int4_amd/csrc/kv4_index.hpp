@@ -38,5 +38,25 @@ __host__ __device__ __forceinline__ Sequence sequence_of(const KvView& v, int b,
     return s;
 }
 
+// A round of a wave's search among `batch` ends of sequences: lane i looks at
+// the end of sequence at(i) - 1 if the range holds it, and keep() takes the number of lanes
+// whose end is not past the token.  Unsigned: 64 steps may pass 2^31.
+struct Search {
+    uint32_t lo, n, step;             // ends of sequences lo .. lo + n - 1 are open
+    __host__ __device__ __forceinline__ uint32_t at(int lane) const { return lo + (uint32_t)(lane + 1) * step; }
+    __host__ __device__ __forceinline__ bool holds(uint32_t at) const { return at <= lo + n; }
+    __host__ __device__ __forceinline__ void keep(int lanes)
+    {
+        const uint32_t left = lo + n;
+        lo += (uint32_t)lanes * step;
+        n = left - lo < step - 1 ? left - lo : step - 1;
+        step = (n + 63) / 64;
+    }
+};
+__host__ __device__ __forceinline__ Search search_of(int batch)
+{
+    return Search{0, (uint32_t)batch, ((uint32_t)batch + 63) / 64};
+}
+
 }  // namespace kv4
 }  // namespace mnb

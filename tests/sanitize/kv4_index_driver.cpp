@@ -69,9 +69,37 @@ static void offsets()
                     }
 }
 
+// The search for a token's sequence by 64 lanes, for batches up to the largest:
+// every offset looked at is one of the batch's, and the sequence is found.
+static void search()
+{
+    for (int batch : {1, 2, 63, 64, 65, 700, 4096, 4097, 1 << 24, INT32_MAX - 65, INT32_MAX - 64, INT32_MAX - 2, INT32_MAX - 1})
+        for (int per : {1, 3, 200, 1 << 28})                       // sequences to a token
+            for (int64_t token : {(int64_t)0, (int64_t)1, (int64_t)5, (int64_t)batch / per / 2, (int64_t)batch / per - 1,
+                                  (int64_t)batch / per, (int64_t)batch / per + 1}) {
+                if (token < 0) continue;
+                auto q_start = [&](uint32_t i) {
+                    expect(i >= 1 && i <= (uint32_t)batch, "an offset of the batch");
+                    return (int64_t)(i / (uint32_t)per);
+                };
+                kv4::Search s = kv4::search_of(batch);
+                int rounds = 0;
+                while (s.n > 0 && ++rounds < 20) {
+                    int lanes = 0;
+                    for (int lane = 0; lane < 64; ++lane) {
+                        const uint32_t at = s.at(lane);
+                        lanes += s.holds(at) && q_start(at) <= token;
+                    }
+                    s.keep(lanes);
+                }
+                const int64_t ends = (token + 1) * per - 1;        // of i / per <= token
+                expect(rounds <= 6 && s.lo == (uint32_t)(ends < batch ? ends : batch), "the sequence");
+            }
+}
+
 int main(int argc, char** argv)
 {
-    struct { const char* name; void (*run)(); } parts[] = {{"no_pages", no_pages}, {"offsets", offsets}};
+    struct { const char* name; void (*run)(); } parts[] = {{"no_pages", no_pages}, {"offsets", offsets}, {"search", search}};
     for (auto& p : parts)
         if (argc < 2 || !std::strcmp(argv[1], p.name)) p.run();
     std::printf("%s: %d failures\n", failures ? "FAILED" : "ok", failures);
