@@ -155,7 +155,7 @@ __global__ __launch_bounds__(KW * 64, WPE) void kv4_attention_kernel(AttnParams 
     if (row0 >= rows) return;                  // the whole workgroup
     const int last_row = row0 + kRows <= rows ? row0 + kRows - 1 : rows - 1;
     int lo, hi;
-    key_range(p, s, row0 / p.gqa, last_row / p.gqa, lo, hi);
+    key_range(p.causal, p.window, s, row0 / p.gqa, last_row / p.gqa, lo, hi);
     // this split's part, in blocks
     const int from = lo > c0 ? lo : c0, to = hi < c1 ? hi : c1;
     const bool any = from < to;
@@ -533,7 +533,7 @@ __device__ __forceinline__ int splits_of(const AttnParams& p, const Sequence& s,
     const int rows = s.count * p.gqa;
     const int r0 = r / p.rows_per_wg * p.rows_per_wg;
     const int r1 = r0 + p.rows_per_wg <= rows ? r0 + p.rows_per_wg - 1 : rows - 1;
-    key_range(p, s, r0 / p.gqa, r1 / p.gqa, lo, hi);
+    key_range(p.causal, p.window, s, r0 / p.gqa, r1 / p.gqa, lo, hi);
     s0 = lo / p.chunk;
     return hi > lo ? (hi + p.chunk - 1) / p.chunk - s0 : 0;
 }
@@ -759,7 +759,7 @@ hipError_t launch_kv4_attention(const AttentionArgs& a, hipStream_t stream, cons
     p.part_ml = p.part_o ? p.part_o + (int64_t)c.splits * a.v.tokens * a.v.q_heads * a.v.head_dim : nullptr;
     p.scale_log2 = a.scale * 1.4426950408889634f;
     p.causal = a.causal;
-    p.window = (int)(a.window > 0x7fffffff ? 0 : a.window);
+    p.window = kv4::window_of(a.window, a.max_kv);
     p.max_q = (int)a.max_q;
     p.max_kv = (int)a.max_kv;
     p.gqa = a.v.q_heads / a.v.kv_heads;

@@ -29,7 +29,7 @@ struct AttnParams {
     float* part_ml;                   // [splits][tokens * q_heads][2]: M, sum
     float scale_log2;
     int causal;
-    int window;                       // 0: none
+    int window;                       // 0: none; else below max_kv
     int max_q, max_kv;
     int gqa;                          // query heads per key head
     int splits, chunk;                // keys per split, a multiple of 32
@@ -61,22 +61,6 @@ __device__ __forceinline__ float top_exponent(uint32_t word) { return (float)((i
 __device__ __forceinline__ uint32_t max_halves(uint32_t a, uint32_t b)
 {
     return __builtin_bit_cast(uint32_t, __builtin_elementwise_max(__builtin_bit_cast(us2_t, a), __builtin_bit_cast(us2_t, b)));
-}
-
-// The keys rows of tokens i0..i1 of a sequence can see: [lo, hi).
-__device__ __forceinline__ void key_range(const AttnParams& p, const Sequence& s, int i0, int i1, int& lo, int& hi)
-{
-    lo = 0;
-    hi = s.len;
-    if (p.causal) {
-        const int end = s.before + i1 + 1;
-        hi = end < hi ? end : hi;
-        if (p.window > 0) {
-            const int from = s.before + i0 - p.window + 1;
-            lo = from > 0 ? from : 0;
-        }
-    }
-    hi = hi < lo ? lo : hi;
 }
 
 // The queries of a lane's row as the B operand of the first product: dims 32 j +

@@ -38,6 +38,29 @@ __host__ __device__ __forceinline__ Sequence sequence_of(const KvView& v, int b,
     return s;
 }
 
+// The window as the kernels take it: one that no position of max_kv keys passes is none.
+__host__ __device__ __forceinline__ int window_of(int64_t window, int64_t max_kv)
+{
+    return window < max_kv ? (int)window : 0;
+}
+
+// The keys rows of tokens i0..i1 of a sequence can see: [lo, hi).  A window below 2^30
+// and positions from -2^30 on keep the differences in 32 bits.
+__host__ __device__ __forceinline__ void key_range(int causal, int window, const Sequence& s, int i0, int i1, int& lo, int& hi)
+{
+    lo = 0;
+    hi = s.len;
+    if (causal) {
+        const int end = s.before + i1 + 1;
+        hi = end < hi ? end : hi;
+        if (window > 0) {
+            const int from = s.before + i0 - window + 1;
+            lo = from > 0 ? from : 0;
+        }
+    }
+    hi = hi < lo ? lo : hi;
+}
+
 // A round of a wave's search among `batch` ends of sequences: lane i looks at
 // the end of sequence at(i) - 1 if the range holds it, and keep() takes the number of lanes
 // whose end is not past the token.  Unsigned: 64 steps may pass 2^31.

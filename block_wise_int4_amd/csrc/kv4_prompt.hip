@@ -63,7 +63,7 @@ __global__ __launch_bounds__(RW * 64, 2) void kv4_prompt_kernel(AttnParams p)
     if (row0 >= rows) return;                          // the whole workgroup
     const int last_row = row0 + kRows <= rows ? row0 + kRows - 1 : rows - 1;
     int lo, hi;
-    key_range(p, s, row0 / p.gqa, last_row / p.gqa, lo, hi);
+    key_range(p.causal, p.window, s, row0 / p.gqa, last_row / p.gqa, lo, hi);
     const int c0 = split * p.chunk, c1 = c0 + p.chunk;
     const int from = lo > c0 ? lo : c0, to = hi < c1 ? hi : c1;
     const bool any = from < to;

@@ -97,9 +97,36 @@ static void search()
             }
 }
 
+// The keys of rows under a window of any width, against the definition.
+static void windows()
+{
+    const int64_t widths[] = {0, 1, 2, 31, 32, 1000, (1 << 30) - 1, 1 << 30, INT32_MAX - 1000, INT32_MAX - 1, INT32_MAX,
+                              (int64_t)INT32_MAX + 1, INT64_MAX};
+    const int32_t lens[] = {0, 1, 5, 33, 100, 1 << 30, INT32_MAX};
+    for (int32_t len : lens)
+        for (int32_t tokens : {1, 3, 20, 1000, INT32_MAX})
+            for (int max_kv : {0, 1, 33, 1 << 30})
+                for (int64_t width : widths)
+                    for (int i0 : {0, 1, 19, 511, (1 << 29) - 2})
+                        for (int i1 : {i0, i0 + 1, (1 << 29) - 1}) {
+                            const int32_t q_start[] = {0, tokens};
+                            const KvView v = view(&len, q_start, 1, tokens, 1 << 26, 9);
+                            const kv4::Sequence s = kv4::sequence_of(v, 0, (1 << 29) - 1, max_kv);
+                            if (i1 >= s.count) continue;
+                            const int window = kv4::window_of(width, max_kv);
+                            int lo, hi;
+                            kv4::key_range(1, window, s, i0, i1, lo, hi);
+                            const int64_t first = (int64_t)s.len - tokens;
+                            int64_t from = 0, to = first + i1 + 1;     // of every row i0..i1 together
+                            if (width > 0 && first + i0 + 1 > width) from = first + i0 + 1 - width;
+                            to = to > s.len ? s.len : to;
+                            expect(lo <= hi && (lo == hi ? to <= from : lo == from && hi == to), "keys of the rows");
+                        }
+}
+
 int main(int argc, char** argv)
 {
-    struct { const char* name; void (*run)(); } parts[] = {{"no_pages", no_pages}, {"offsets", offsets}, {"search", search}};
+    struct { const char* name; void (*run)(); } parts[] = {{"no_pages", no_pages}, {"offsets", offsets}, {"search", search}, {"windows", windows}};
     for (auto& p : parts)
         if (argc < 2 || !std::strcmp(argv[1], p.name)) p.run();
     std::printf("%s: %d failures\n", failures ? "FAILED" : "ok", failures);

@@ -1,4 +1,4 @@
-"""Lengths, offsets and pages of any value: the attention stays inside the arrays that the call describes."""
+"""Lengths, offsets, pages and windows of any value: the attention stays inside the arrays that the call describes."""
 import numpy as np
 import pytest
 
@@ -55,3 +55,22 @@ def test_offsets_of_any_value_stay_inside(mnb, rest, new, max_kv):
     assert (got[[0, 2]] == 7.0).all()
     if rest[0] < 0:                                    # no offsets past the first sequence lead to a row
         assert (got[1, new:] == 7.0).all()
+
+
+@pytest.mark.parametrize("dt", ["f16", "f32"])
+@pytest.mark.parametrize("window", [(1 << 31) - 1, (1 << 31) - 5, (1 << 31) + 7, 1 << 62])
+@pytest.mark.parametrize("new", [6, 20, 50])
+def test_a_window_wider_than_any_sequence(mnb, new, window, dt):
+    """New tokens before position 0 beside ones that see keys: the same bits as without a window."""
+    t = G.torch()
+    rng = np.random.default_rng((973, new))
+    lens = [5, 120]
+    table, pages = sequences(rng, lens, 32)
+    geo = o.Geometry(2, 1, 128, 128, 32, pages)
+    cache, _ = make_cache(rng, geo, table, lens)
+    q = rng.normal(size=(new + 3, 2, 128)).astype(np.float16 if dt == "f16" else np.float32)
+    q_start = [0, new, new + 3]
+    a, la = attend(mnb, geo, cache, table, lens, q_start, q, 0.1)
+    b, lb = attend(mnb, geo, cache, table, lens, q_start, q, 0.1, window=window)
+    assert t.equal(a, b) and t.equal(la, lb)
+    assert a[new - 1].any() and not a[0].any()

@@ -24,7 +24,7 @@ def driver(tmp_path_factory):
     return exe
 
 
-@pytest.mark.parametrize("part", ["no_pages", "offsets", "search"])
+@pytest.mark.parametrize("part", ["no_pages", "offsets", "search", "windows"])
 def test_stays_in_range(driver, part):
     r = subprocess.run([driver, part], capture_output=True, text=True, env=ENV, timeout=300)
     assert r.returncode == 0 and r.stdout.strip().endswith("ok: 0 failures"), r.stdout[-2000:] + r.stderr[-3000:]
