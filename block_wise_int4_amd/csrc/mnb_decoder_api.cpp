@@ -36,6 +36,11 @@ mnb_status check_stride(int64_t stride, int64_t row, int64_t rows, const char* n
     return MNB_OK;
 }
 
+int64_t page_bytes(const mnb_kv4_desc* c)
+{
+    return (int64_t)c->kv_heads * (c->page_size / mnb::kKvBlock) * mnb::kv_block_bytes(c->head_dim, c->head_dim / c->group_size);
+}
+
 mnb_status check_kv_desc(const mnb_kv4_desc* c)
 {
     if (!c) return fail(MNB_ERR_INVALID_ARGUMENT, "cache descriptor is NULL");
@@ -56,6 +61,7 @@ mnb_status check_kv_desc(const mnb_kv4_desc* c)
         return fail(MNB_ERR_UNSUPPORTED, "group_size %d exceeds head_dim %d", c->group_size, c->head_dim);
     if (c->page_size != 32 && c->page_size != 64 && c->page_size != 128 && c->page_size != 256)
         return fail(MNB_ERR_UNSUPPORTED, "page_size %d not supported (32, 64, 128 or 256)", c->page_size);
+    if (c->num_pages > INT64_MAX / page_bytes(c)) return fail(MNB_ERR_INVALID_ARGUMENT, "cache size overflows");
     return MNB_OK;
 }
 
@@ -187,18 +193,12 @@ mnb_status mnb_rms_norm(const void* x, int64_t x_stride, const void* residual, i
 size_t mnb_kv4_cache_bytes(const mnb_kv4_desc* c)
 {
     if (check_kv_desc(c) != MNB_OK) return 0;
-    const int64_t page = (int64_t)c->kv_heads * (c->page_size / mnb::kKvBlock) *
-                         mnb::kv_block_bytes(c->head_dim, c->head_dim / c->group_size);
-    if (c->num_pages > 0 && page > INT64_MAX / c->num_pages) {
-        fail(MNB_ERR_INVALID_ARGUMENT, "cache size overflows");
-        return 0;
-    }
     if (c->num_pages == 0) {
         fail(MNB_ERR_INVALID_ARGUMENT, "the cache has no pages");
         return 0;
     }
     ok("");
-    return (size_t)(page * c->num_pages);
+    return (size_t)(page_bytes(c) * c->num_pages);
 }
 
 mnb_status mnb_kv4_append(const mnb_kv4_desc* c, void* cache, const int32_t* block_table, int64_t table_stride,
