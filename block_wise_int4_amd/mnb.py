@@ -410,8 +410,9 @@ def _sequences(c, cache, table, kv_len, q_start):
     d = ctypes.byref(c)
     if cache.numel() * cache.element_size() < lib.mnb_kv4_cache_bytes(d):
         raise ValueError("cache: %d bytes expected" % mnb_kv4_cache_bytes(c))
-    tp, ts = _rows2(table, "block_table")
-    return d, _addr(cache, "cache"), tp, ts, _addr(kv_len, "kv_len"), _addr(q_start, "q_start"), batch
+    # a row's length is its pitch: of a slice of a wider table the kernels would take the entries beside it
+    return d, _addr(cache, "cache"), _addr(table, "block_table"), table.shape[1], _addr(kv_len, "kv_len"), \
+        _addr(q_start, "q_start"), batch
 
 
 def mnb_kv4_append(c: mnb_kv4_desc, cache, k, v, block_table, kv_len, q_start=None, cos=None, sin=None,

@@ -429,8 +429,8 @@ typedef struct {
 size_t mnb_kv4_cache_bytes(const mnb_kv4_desc* c);
 
 /* The sequences of a call, in device memory (int32, 4-byte aligned):
- *   block_table [batch, table_stride]: pages of each sequence, in order; only
- *     entries of pages that hold tokens are used.
+ *   block_table [batch, table_stride], dense: pages of each sequence, in order;
+ *     only entries of pages that hold tokens are used, any of a row may be read.
  *   kv_len [batch]: tokens of each sequence, the new ones included.
  *   q_start [batch + 1]: rows of the new tokens, q_start[b] .. q_start[b+1]-1 for
  *     sequence b, non-decreasing; NULL: one each, row b (then tokens == batch).
