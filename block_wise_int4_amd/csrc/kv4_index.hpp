@@ -21,20 +21,21 @@ __host__ __device__ __forceinline__ Sequence sequence_of(const KvView& v, int b,
     int len = v.kv_len[b];
     len = len < 0 ? 0 : len > max_kv ? max_kv : len;
     s.len = (int64_t)len > room ? (int)room : len;
-    int64_t first = b, end = (int64_t)b + 1;
+    int first = b, end = b + 1;
     if (v.q_start) {
         first = v.q_start[b];
         end = v.q_start[b + 1];
     }
-    // in 64 bits: the difference of two offsets need not fit 32.  Positions are below
-    // zero however far they are, so they stop at -2^30: max_q is less than that
-    const int64_t before = s.len - (end - first);
-    s.before = before < -(1 << 30) ? -(1 << 30) : before > s.len ? s.len : (int)before;
+    // offsets from 0 on have a difference that fits, and one that decreases means no tokens.
+    // Positions are below zero however far they are, so they stop at -2^30: max_q is less than that
     first = first < 0 ? 0 : first;
+    end = end < first ? first : end;
+    const int before = s.len - (end - first);
+    s.before = before < -(1 << 30) ? -(1 << 30) : before;
     end = end > v.tokens ? v.tokens : end;
-    const int64_t n = end - first;
-    s.count = n <= 0 ? 0 : n > max_q ? max_q : (int)n;
-    s.first = s.count > 0 ? (int)first : 0;
+    const int n = end - first;
+    s.count = n <= 0 ? 0 : n > max_q ? max_q : n;
+    s.first = first;
     return s;
 }
 
