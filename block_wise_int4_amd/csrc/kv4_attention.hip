@@ -266,48 +266,49 @@ __global__ __launch_bounds__(KW * 64, WPE) void kv4_attention_kernel(AttnParams 
 #pragma unroll
                 for (int k = 0; k < 2 * I; ++k) x[n][k / I][k % I] *= qs[n];
         }
-        // ---- masks, and the running reference: the largest logit plus the exponent of its value scale ----
+        // ---- masks: a hidden key's logit is -infinity ----
         const bool edge = blk * 32 + 32 > whole || blk * 32 < open;
         uint32_t seen[NR];                     // bit t I + i: the row sees the key
-        float mxs[NR];
-        if (edge) {                            // key by key: a hidden key's scale is not looked at
+        if (edge) {
 #pragma unroll
             for (int n = 0; n < NR; ++n) {
                 seen[n] = 0;
-                mxs[n] = -__builtin_inff();
                 const int below = p.causal && p.window > 0 ? pos[n] - p.window : -1;
 #pragma unroll
                 for (int t = 0; t < 2; ++t)
 #pragma unroll
                     for (int i = 0; i < I; ++i) {
                         const int key = blk * 32 + t * 16 + mine + i;
-                        uint32_t w = vwd[t][i * NG];
-#pragma unroll
-                        for (int g = 1; g < NG; ++g) w = max_halves(w, vwd[t][i * NG + g]);
                         if (key <= pos[n] && key > below && key < s.len)
                             seen[n] |= 1u << (I * t + i);
                         else
                             x[n][t][i] = -__builtin_inff();
-                        mxs[n] = fmaxf(mxs[n], x[n][t][i] + top_exponent(w));
                     }
             }
-        } else {
-            uint32_t w = vwd[0][0];
-#pragma unroll
-            for (int k = 1; k < 2 * I * NG; ++k) w = max_halves(w, vwd[k / (I * NG)][k % (I * NG)]);
-            const float top = top_exponent(w);
-#pragma unroll
-            for (int n = 0; n < NR; ++n) {
-                float m = x[n][0][0];
-#pragma unroll
-                for (int k = 1; k < 2 * I; ++k) m = fmaxf(m, x[n][k / I][k % I]);
-                mxs[n] = m + top;
-            }
         }
+        // ---- the running reference: looked at key by key where the largest logit and the
+        // largest scale, of whichever keys, would pass it ----
+        uint32_t most = vwd[0][0];
+#pragma unroll
+        for (int k = 1; k < 2 * I * NG; ++k) most = max_halves(most, vwd[k / (I * NG)][k % (I * NG)]);
+        const float top = top_exponent(most);
 #pragma unroll
         for (int n = 0; n < NR; ++n) {
-            float mx = mxs[n];
-            if (__builtin_amdgcn_ballot_w64(mx > M[n] + kRaise)) {
+            float mx = x[n][0][0];
+#pragma unroll
+            for (int k = 1; k < 2 * I; ++k) mx = fmaxf(mx, x[n][k / I][k % I]);
+            if (__builtin_amdgcn_ballot_w64(mx - M[n] > kRaise - top)) {
+                mx = -__builtin_inff();        // of a key: its logit plus its own scale's exponent
+#pragma unroll
+                for (int t = 0; t < 2; ++t)
+#pragma unroll
+                    for (int i = 0; i < I; ++i) {
+                        uint32_t w = vwd[t][i * NG];
+#pragma unroll
+                        for (int g = 1; g < NG; ++g) w = max_halves(w, vwd[t][i * NG + g]);
+                        mx = fmaxf(mx, x[n][t][i] + (float)((w >> 10) & 31u));
+                    }
+                mx -= 14.0f;                   // as top_exponent
                 mx = fmaxf(mx, __shfl_xor(mx, 16));
                 mx = fmaxf(mx, __shfl_xor(mx, 32));
                 const float next = fmaxf(M[n], mx - kBelow);

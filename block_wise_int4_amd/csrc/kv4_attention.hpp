@@ -13,11 +13,14 @@ namespace mnb {
 namespace kv4 {
 
 constexpr float kLow = -1e30f;        // "no key yet": finite, so differences stay numbers
-// The running reference M of a row is raised when a logit plus the exponent of
-// its value scale passes M + kRaise, to kBelow under that: p s' stays below
-// 2^kRaise (fp16 ends at 2^16) and the largest one is at least 2^(kBelow - 1),
-// 2^23 above fp16's smallest normal value.
-constexpr float kRaise = 14.0f, kBelow = 10.0f;
+// The running reference M of a row is looked at when a logit plus the exponent of
+// a value scale may pass M + kRaise, and is then taken to kBelow under the largest sum of
+// a key's logit and the exponent of its own scale (the largest of its groups), if that is
+// higher.  So p s' stays below 2^kRaise (fp16 ends at 2^16), and the largest p s' of the row
+// is at least 2^(kBelow - 1), 2^23 above fp16's smallest normal value: a term keeps its bits
+// unless it is that much smaller than the row's largest.  Of a key with groups of far
+// different scales, the small groups' dims may lose theirs.
+constexpr float kRaise = 15.9f, kBelow = 10.0f;
 
 struct AttnParams {
     KvView v;

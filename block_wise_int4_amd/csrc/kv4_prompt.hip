@@ -320,44 +320,51 @@ __global__ __launch_bounds__(RW * 64, 2) void kv4_prompt_kernel(AttnParams p)
             raise |= mx[n] + top > kRaise || (M[n] == kLow && mx[n] > -__builtin_inff());
         }
         if (__builtin_amdgcn_ballot_w64(raise)) {
-            if (edge) {                        // key by key: a hidden key's scale is not looked at
+            // key by key: a logit plus the exponent of its own scale, so that the largest
+            // product of a row sets its reference.  All rows that have risen since move
+            // together: a third as many looks as with those past kRaise alone (2048 and 1100
+            // tokens of 32 heads by 8: 215 us against 230)
 #pragma unroll
-                for (int n = 0; n < NR; ++n) mx[n] = -__builtin_inff();
-                for (int k = 0; k < 8 * KB; ++k) {
-                    uint32_t most = 0;         // an fp32 scale's exponent, as top_exponent has it
+            for (int n = 0; n < NR; ++n) mx[n] = -__builtin_inff();
+            int own = 4 * quarter;             // opaque: else the scales read here stay in registers until the
+            asm volatile("" : "+v"(own));      // products (37 spilled at head_dim 256, groups of 64, fp32)
 #pragma unroll
-                    for (int g = 0; g < NG; ++g) {
-                        const uint32_t w = __builtin_bit_cast(uint32_t, vs[buf][b0 + (k >> 3)][g][((k >> 2) & 1) * 16 + 4 * quarter + (k & 3)]);
-                        most = w > most ? w : most;
-                    }
-                    const float e = fminf(fmaxf((float)((int)(most >> 23) - 126), -14.0f), 17.0f);
+            for (int t = 0; t < 2 * KB; ++t) {
+                u4_t most = {0, 0, 0, 0};      // fp32 scales: their exponents with a bias of 126
 #pragma unroll
-                    for (int n = 0; n < NR; ++n) {
-                        float yk = y[n][0];
-#pragma unroll
-                        for (int q = 1; q < 8 * KB; ++q) yk = k == q ? y[n][q] : yk;
-                        mx[n] = fmaxf(mx[n], yk + e);
-                    }
+                for (int g = 0; g < NG; ++g) {
+                    const f4_t v4 = *reinterpret_cast<const f4_t*>(&vs[buf][b0 + t / 2][g][t % 2 * 16 + own]);
+                    most = __builtin_elementwise_max(most, __builtin_bit_cast(u4_t, v4));
                 }
-            } else {
 #pragma unroll
-                for (int n = 0; n < NR; ++n) mx[n] += top;
+                for (int i = 0; i < 4; ++i) {
+                    const float e = __builtin_amdgcn_fmed3f((float)(most[i] >> 23), 112.0f, 143.0f);
+#pragma unroll
+                    for (int n = 0; n < NR; ++n) mx[n] = fmaxf(mx[n], y[n][4 * t + i] + e);
+                }
             }
+            bool move = false;
 #pragma unroll
             for (int n = 0; n < NR; ++n) {
                 mx[n] = fmaxf(mx[n], __shfl_xor(mx[n], 16));
-                mx[n] = fmaxf(mx[n], __shfl_xor(mx[n], 32));
-                const bool first = M[n] == kLow;
-                const bool move = first ? mx[n] > -__builtin_inff() : mx[n] > kRaise;
-                const float next = move ? Mu[n] + mx[n] - kBelow : Mu[n];
-                const float alpha = first ? 1.0f : exp2f(Mu[n] - next);   // nothing was summed before the first
-                const float by = next - Mu[n];
-                M[n] = move ? next : M[n];
-                l[n] *= alpha;
+                mx[n] = fmaxf(mx[n], __shfl_xor(mx[n], 32)) - 126.0f;   // as top_exponent
+                move |= mx[n] > (M[n] == kLow ? -__builtin_inff() : kBelow);
+            }
+            if (__builtin_amdgcn_ballot_w64(move)) {
 #pragma unroll
-                for (int t = 0; t < NT; ++t) o[n][t] *= alpha;
+                for (int n = 0; n < NR; ++n) {
+                    const bool first = M[n] == kLow;
+                    const bool up = mx[n] > (first ? -__builtin_inff() : kBelow);
+                    const float next = up ? Mu[n] + mx[n] - kBelow : Mu[n];
+                    const float alpha = first ? 1.0f : exp2f(Mu[n] - next);   // nothing was summed before the first
+                    const float by = next - Mu[n];
+                    M[n] = up ? next : M[n];
+                    l[n] *= alpha;
 #pragma unroll
-                for (int k = 0; k < 8 * KB; ++k) y[n][k] -= by;
+                    for (int t = 0; t < NT; ++t) o[n][t] *= alpha;
+#pragma unroll
+                    for (int k = 0; k < 8 * KB; ++k) y[n][k] -= by;
+                }
             }
         }
         // ---- p ----

@@ -1,0 +1,100 @@
+"""The attention's range: value scales far apart."""
+import numpy as np
+import pytest
+
+from oracle import decoder as o
+from tests import gpu_util as G
+from tests.test_gpu_kv4 import dev, sequences
+from tests.test_gpu_kv4_attention import attend, make_cache
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module")
+def mnb():
+    from block_wise_int4_amd import mnb as m
+    return m
+
+
+def peak_of(geo, cache, table_row, n, q, scale, first):
+    """Largest weight times value scale, over the keys a row sees and their groups, [T, H]: rows at positions first + t."""
+    T, H, _ = q.shape
+    per = geo.q_heads // geo.kv_heads
+    out = np.zeros((T, H))
+    for h in range(geo.kv_heads):
+        K, _ = o.gather(geo, cache, table_row, h, n)
+        s = np.zeros(n)
+        for j in range(n):
+            at = geo.base(int(table_row[j // geo.page]), h, j % geo.page) + 32 * geo.D + 128 * geo.G + 4 * geo.G * (j % 32)
+            s[j] = (cache[at:at + 4 * geo.G].copy().view("<u4") & 0xFFFF).astype(np.uint16).view(np.float16).max()
+        for g in range(h * per, (h + 1) * per):
+            for t in range(T):
+                m = first + t + 1
+                x = scale * (K[:m] @ q[t, g].astype(np.float64))
+                p = np.exp(x - x.max())
+                out[t, g] = (p * s[:m]).max() / p.sum()
+    return out
+
+
+def tolerance(size, reach, keys, D, f16, peak):
+    """As the oracle's bound, but what a product p s' loses below fp16's normal range (2^-25 a key, codes up to 15) set
+    beside the row's own largest product: the running reference keeps that at 2^9 or above.  fp32 calls: p s' in
+    two fp16 parts, 2^-22 relative."""
+    tol = o.attention_tolerance(size, reach, keys, D, f16, 0.0) + keys * 15 * 2.0 ** -34 * peak[..., None]
+    return tol + (0 if f16 else size * 2.0 ** -22)
+
+
+@pytest.mark.parametrize("dt", ["f16", "f32"])
+@pytest.mark.parametrize("group", [128, 64, 32])
+@pytest.mark.parametrize("new", [1, 6, 20, 40])
+@pytest.mark.parametrize("others", [-4, 8])
+def test_keys_with_nearly_all_the_weight_and_small_values(mnb, others, new, group, dt):
+    """In blocks that every row sees whole, beside keys of far larger value scales: exact to their own size."""
+    rng = np.random.default_rng((970, new, group, others + 50))
+    past, D, H = 96, 128, 2
+    n = past + new
+    table, pages = sequences(rng, [n], 32)
+    geo = o.Geometry(H, 1, D, group, 32, pages)
+    cache, _ = make_cache(rng, geo, table, [n], k_scale=0.05)
+    NG, u = D // group, rng.choice([-1.0, 1.0], D)
+    for j in range(n):                                # the others' value scales
+        at = geo.base(int(table[0, j // 32]), 0, j % 32) + 32 * D + 128 * NG + 4 * NG * (j % 32)
+        cache[at:at + 4 * NG] = np.full(NG, int(np.float16(2.0 ** others).view(np.uint16)) | (8 << 16), "<u4").view(np.uint8)
+    for star, ks in ((40, 1.0), (41, 0.995), (73, 0.99)):     # alike, so that no weight is a power of two of another
+        small = (2.0 ** -20 * rng.uniform(1, 2, NG)).astype(np.float16)
+        o.store(geo, cache, int(table[0, star // 32]), 0, star % 32, False, (8 + 7 * u).astype(int), np.full(NG, ks, np.float16),
+                np.full(NG, 8))
+        o.store(geo, cache, int(table[0, star // 32]), 0, star % 32, True, rng.integers(0, 16, D), small, np.full(NG, 7))
+    q = (0.5 * rng.normal(size=(new, H, D)) + u).astype(np.float16 if dt == "f16" else np.float32)
+    w, _, size, reach = o.attention(geo, cache, table, [n], [0, new], q, D ** -0.5)
+    assert np.abs(w).max() < 2.0 ** -15               # the small keys' values
+    tol = tolerance(size, reach, n, D, dt == "f16", peak_of(geo, cache, table[0], n, q, D ** -0.5, past))
+    err = np.abs(G.host(attend(mnb, geo, cache, table, [n], [0, new], q, D ** -0.5)[0]) - w)
+    assert (err <= tol).all(), "worst %.3g of the bound" % float((err / tol).max())
+
+
+@pytest.mark.parametrize("dt", ["f16", "f32"])
+@pytest.mark.parametrize("rise", [0, 1])
+@pytest.mark.parametrize("new", [1, 7, 30, 60])
+def test_value_scales_of_every_size(mnb, new, rise, dt):
+    """Value scales over fp16's whole range, with level logits or ones that rise along the keys, bounded by each row's own
+    largest product."""
+    rng = np.random.default_rng((971, new, rise))
+    n, D = 260, 128
+    table, pages = sequences(rng, [n], 64)
+    geo = o.Geometry(2, 1, D, 64, 64, pages)
+    cache, _ = make_cache(rng, geo, table, [n], k_scale=0.2)
+    meta = cache.reshape(-1, geo.B)[:, 32 * D:].copy().view("<u4")
+    for j in range(n):
+        row, at = int(table[0, j // 64]) * 2 + j % 64 // 32, j % 32 * 2
+        s = np.float16(2.0) ** rng.integers(-24, 9, 2).astype(np.float16)
+        ks = np.float16(0.05 + rise * 0.8 * j / n)
+        for g in range(2):
+            meta[row, at + g] = (int(meta[row, at + g]) & 0xFFFF0000) | int(ks.view(np.uint16))
+            meta[row, 64 + at + g] = (int(meta[row, 64 + at + g]) & 0xFFFF0000) | int(s[g].view(np.uint16))
+    cache.reshape(-1, geo.B)[:, 32 * D:] = meta.view(np.uint8)
+    q = (1.5 * rng.normal(size=(new, 2, D))).astype(np.float16 if dt == "f16" else np.float32)
+    w, _, size, reach = o.attention(geo, cache, table, [n], [0, new], q, D ** -0.5)
+    tol = tolerance(size, reach, n, D, dt == "f16", peak_of(geo, cache, table[0], n, q, D ** -0.5, n - new))
+    err = np.abs(G.host(attend(mnb, geo, cache, table, [n], [0, new], q, D ** -0.5)[0]) - w)
+    assert (err <= tol).all(), "worst %.3g of the bound" % float((err / tol).max())
