@@ -12,7 +12,7 @@
 namespace mnb {
 namespace kv4 {
 
-constexpr float kLow = -1e30f;        // "no key yet": finite, so differences stay numbers
+constexpr float kLow = -3.402823466e38f;   // "no key yet": below any logit, finite, so that differences are numbers
 // The running reference M of a row is looked at when a logit plus the exponent of
 // a value scale may pass M + kRaise, and is then taken to kBelow under the largest sum of
 // a key's logit and the exponent of its own scale (the largest of its groups), if that is

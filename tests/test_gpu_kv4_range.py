@@ -1,4 +1,4 @@
-"""The attention's range: value scales far apart."""
+"""The attention's range: value scales far apart, logits far below zero."""
 import numpy as np
 import pytest
 
@@ -98,3 +98,27 @@ def test_value_scales_of_every_size(mnb, new, rise, dt):
     tol = tolerance(size, reach, n, D, dt == "f16", peak_of(geo, cache, table[0], n, q, D ** -0.5, n - new))
     err = np.abs(G.host(attend(mnb, geo, cache, table, [n], [0, new], q, D ** -0.5)[0]) - w)
     assert (err <= tol).all(), "worst %.3g of the bound" % float((err / tol).max())
+
+
+@pytest.mark.parametrize("new", [1, 8, 16, 40])
+@pytest.mark.parametrize("split", [False, True])
+def test_logits_far_below_zero(mnb, new, split):
+    """fp32 queries whose logits are all one large negative number: equal weights, not a row that sees nothing."""
+    rng = np.random.default_rng(972)
+    n, D = 300, 128
+    table, pages = sequences(rng, [n], 32)
+    geo = o.Geometry(1, 1, D, 128, 32, pages)
+    cache, _ = make_cache(rng, geo, table, [n])
+    for j in range(n):
+        o.store(geo, cache, int(table[0, j // 32]), 0, j % 32, False, np.full(D, 15), np.ones(1, np.float16), np.zeros(1, int))
+    V = o.gather(geo, cache, table[0], 0, n)[1]
+    q = np.full((new, 1, D), -1e31, np.float32)
+    got, lse = attend(mnb, geo, cache, table, [n], [0, new], q, 0.125, max_kv=3000 if split else n)
+    got, lse = G.host(got), G.host(lse)
+    x = -0.125 * 15 * D * float(np.float32(1e31))
+    for t in range(new):
+        seen = V[:n - new + t + 1]
+        # equal logits, so equal weights; the sums in fp32, the weights times the scales in two fp16 parts
+        tol = np.abs(seen).mean(0) * ((n + 64) * o.EPS32 + 2.0 ** -22) + 2.0 ** -30
+        assert (np.abs(got[t, 0] - seen.mean(0)) <= tol).all(), t
+        assert abs(lse[t, 0] - x) <= abs(x) * (D + 16) * o.EPS32, t
