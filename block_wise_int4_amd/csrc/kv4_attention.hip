@@ -758,7 +758,7 @@ hipError_t launch_kv4_attention(const AttentionArgs& a, hipStream_t stream, cons
     p.lse = a.lse;
     p.part_o = static_cast<float*>(a.workspace);
     p.part_ml = p.part_o ? p.part_o + (int64_t)c.splits * a.v.tokens * a.v.q_heads * a.v.head_dim : nullptr;
-    p.scale_log2 = a.scale * 1.4426950408889634f;
+    p.scale_log2 = a.scale * kLog2E;
     p.causal = a.causal;
     p.window = kv4::window_of(a.window, a.max_kv);
     p.max_q = (int)a.max_q;

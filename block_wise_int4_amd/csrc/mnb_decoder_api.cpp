@@ -304,7 +304,8 @@ mnb_status mnb_attention_kv4(const mnb_kv4_desc* c, const void* cache, const int
     if (causal != 0 && causal != 1) return fail(MNB_ERR_INVALID_ARGUMENT, "causal must be 0 or 1 (got %d)", causal);
     if (window < 0) return fail(MNB_ERR_INVALID_ARGUMENT, "window must be >= 0 (got %lld)", (long long)window);
     if (window > 0 && !causal) return fail(MNB_ERR_INVALID_ARGUMENT, "a window needs causal = 1");
-    if (!std::isfinite(scale)) return fail(MNB_ERR_INVALID_ARGUMENT, "scale must be finite");
+    if (!std::isfinite(scale * mnb::kLog2E))
+        return fail(MNB_ERR_INVALID_ARGUMENT, "scale must be finite, and times log2(e) too");
     MNB_TRY(check_stride(q_stride, (int64_t)c->q_heads * c->head_dim, tokens, "q_stride"));
     if (tokens == 0 || batch == 0 || max_q == 0) return ok("noop");
     MNB_TRY(check_sequences(block_table, table_stride, kv_len, q_start, batch, tokens));

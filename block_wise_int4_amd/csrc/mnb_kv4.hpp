@@ -72,6 +72,7 @@ struct ReadArgs {
 hipError_t launch_kv4_read(const ReadArgs& a, hipStream_t stream, const char** variant);
 
 // ---- attention ----
+constexpr float kLog2E = 1.4426950408889634f;   // the kernels' logits are in units of log2
 struct AttentionArgs {
     KvView v;
     const void* q;

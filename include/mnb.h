@@ -487,7 +487,7 @@ mnb_status mnb_kv4_read(const mnb_kv4_desc* c, const void* cache, const int32_t*
  * its row over all keys and groups is held to 2^-34 of that.
  * workspace (256-byte aligned): mnb_attention_kv4_workspace_bytes of the same
  * arguments; contents need no initialisation.  batch <= 65535, max_kv <=
- * 2^30, max_q * q_heads < 2^29.  Deterministic. */
+ * 2^30, max_q * q_heads < 2^29, scale finite (times log2(e) too).  Deterministic. */
 size_t mnb_attention_kv4_workspace_bytes(const mnb_kv4_desc* c, int64_t batch, int64_t tokens, int64_t max_q,
                                          int64_t max_kv);
 mnb_status mnb_attention_kv4(const mnb_kv4_desc* c, const void* cache, const int32_t* block_table,

@@ -15,3 +15,8 @@ def test_a_cache_whose_size_overflows_is_refused_by_every_call():
     with pytest.raises(mnb.MnbError):
         mnb.mnb_kv4_cache_bytes(big)
     assert mnb.mnb_attention_kv4_workspace_bytes(big, 1, 1, 1, 100) == 0 and "overflow" in mnb.mnb_last_error()
+
+
+@pytest.mark.parametrize("scale", [2.4e38, -2.4e38, 3.4e38])
+def test_a_scale_that_overflows_in_the_units_of_log2_is_refused(scale):
+    _refused(INVALID, attend, scale=scale)
