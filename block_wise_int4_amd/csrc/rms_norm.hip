@@ -8,9 +8,9 @@
 //   q = 127 h w / max|h w|,
 // so the sum of squares and the maximum are found together, by one reduction
 // of the workgroup, and the codes do not depend on how the sum was rounded.
-// h * w is exact in fp32 for fp16 operands; the quotient is formed in fp64,
-// so a code is off only where the exact quotient is a tie to within 2^-50 (fp32
-// operands: 2^-23).
+// h * w is exact in fp32 for fp16 operands; the quotient is formed in fp64 and is
+// off by at most 2^-45 at 127, so a code is off only where the exact quotient is a tie to
+// within that (fp32 operands, whose h w and maximum are rounded: to within 2 x 127 x 2^-24).
 //
 // Bound by memory for many rows, by one round trip and the launch for few.  Measured:
 // 8192 rows of 4096 with a residual, fp16, 45.6 us for 268 MB (5.9 TB/s; a large copy moves
@@ -80,12 +80,15 @@ template <typename T> __device__ __forceinline__ u4_t pack_vec(const float* f)
     }
 }
 
-// round half away from zero of 127 hw / max, as factor = 127 / max in fp64
+// the larger one, or NaN if either is
+__device__ __forceinline__ float max_of(float a, float b) { return __builtin_elementwise_maximum(a, b); }
+
+// round half away from zero of 127 hw / max, as factor = 127 / max in fp64: at
+// most 127 in magnitude, since no |hw| is above the row's largest
 __device__ __forceinline__ int code_of(float hw, double factor)
 {
     const double t = (double)hw * factor;
-    const int q = (int)(t + __builtin_copysign(0.5, t));
-    return q > 127 ? 127 : (q < -127 ? -127 : q);
+    return (int)(t + __builtin_copysign(0.5, t));
 }
 
 template <typename T, int OUT, int NV>
@@ -144,7 +147,7 @@ __global__ __launch_bounds__(1024) void rms_norm_kernel(NormParams p)
             float f[VE];
             unpack_vec<T>(wr, f);
 #pragma unroll
-            for (int i = 0; i < VE; ++i) mx = fmaxf(mx, fabsf(h[i] * f[i]));
+            for (int i = 0; i < VE; ++i) mx = max_of(mx, fabsf(h[i] * f[i]));
         }
     };
     // the sums replace x in its registers, rounded as they are stored
@@ -166,7 +169,7 @@ __global__ __launch_bounds__(1024) void rms_norm_kernel(NormParams p)
 #pragma unroll
     for (int off = 32; off > 0; off >>= 1) {
         ss += __shfl_xor(ss, off);
-        if constexpr (OUT != kNormValues) mx = fmaxf(mx, __shfl_xor(mx, off));
+        if constexpr (OUT != kNormValues) mx = max_of(mx, __shfl_xor(mx, off));
     }
     const int waves = nt >> 6;
     if (waves > 1) {
@@ -179,10 +182,12 @@ __global__ __launch_bounds__(1024) void rms_norm_kernel(NormParams p)
         mx = 0.0f;
         for (int i = 0; i < waves; ++i) {
             ss += red[0][i];
-            mx = fmaxf(mx, red[1][i]);
+            mx = max_of(mx, red[1][i]);
         }
     }
     const float rs = 1.0f / sqrtf(__builtin_fmaf(ss, p.inv_k, p.eps));
+    // no NaN and no infinity among the row's products (mx holds either)
+    const bool fine = uniform(mx < __builtin_inff());
     const double factor = OUT != kNormValues && mx > 0.0f ? 127.0 / (double)mx : 0.0;
 
     auto store_vec = [&](int v, const float* h, const u4_t& wr) {
@@ -197,7 +202,11 @@ __global__ __launch_bounds__(1024) void rms_norm_kernel(NormParams p)
         } else {
             int q[VE];
 #pragma unroll
-            for (int i = 0; i < VE; ++i) q[i] = code_of(h[i] * f[i], factor);
+            for (int i = 0; i < VE; ++i) q[i] = 0;
+            if (fine) {
+#pragma unroll
+                for (int i = 0; i < VE; ++i) q[i] = code_of(h[i] * f[i], factor);
+            }
             if constexpr (OUT == kNormCodesF16) {
                 typedef uint32_t out_t __attribute__((ext_vector_type(VE / 2), aligned(2), may_alias));
                 out_t o;
@@ -238,11 +247,12 @@ __global__ __launch_bounds__(1024) void rms_norm_kernel(NormParams p)
         if constexpr (OUT == kNormValues)
             static_cast<T*>(p.out)[e] = (T)(th * rs * tw);
         else if constexpr (OUT == kNormCodesF16)
-            static_cast<_Float16*>(p.out)[e] = (_Float16)(float)code_of(th * tw, factor);
+            static_cast<_Float16*>(p.out)[e] = (_Float16)(float)(fine ? code_of(th * tw, factor) : 0);
         else
-            static_cast<int8_t*>(p.out)[e] = (int8_t)code_of(th * tw, factor);
+            static_cast<int8_t*>(p.out)[e] = (int8_t)(fine ? code_of(th * tw, factor) : 0);
     }
-    if (OUT != kNormValues && tid == 0) p.scales[row] = mx * rs / 127.0f;
+    if (OUT != kNormValues && tid == 0)
+        p.scales[row] = mx == 0.0f ? 0.0f : fine ? mx * rs / 127.0f : __builtin_nanf("");
 }
 
 template <typename T, int OUT>

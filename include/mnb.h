@@ -368,8 +368,10 @@ mnb_status mnb_gemm_accuracy4_noalloc(const mnb_weight_desc* w, const void* repa
  *   MNB_NORM_CODES_I8   the same codes as int8 [m, k]; scales fp32 [m]:
  *     s = max|y| / 127 and q = y / s to the nearest integer, halves away from
  *     zero, formed as 127 h w / max|h w| (the norm's factor cancels) in 64
- *     bits from the product h w in binary32.  A row of zeros has s = 0 and
- *     codes 0; a row that holds a NaN or an infinity has s = NaN.
+ *     bits from the product h w in binary32.  A row whose products are all 0
+ *     has s = 0 and codes 0, with eps = 0 too; a row with a product that is
+ *     NaN or infinite (from x, residual or weight, 0 times infinity included)
+ *     has s = NaN and codes 0.
  *     MNB_NORM_CODES_F16 is what mnb_gemm_accuracy4_codes takes.
  * Sums are kept in fp32.  residual_out may be x or residual themselves where
  * their stride is k.  m <= 2^31-1, 1 <= k <= 2^31-16; m == 0 is a no-op. */

@@ -1,0 +1,66 @@
+"""RMS norm at the ends of its range: rows of zeros without eps, infinities and NaN the weight hides."""
+import numpy as np
+import pytest
+
+from tests import gpu_util as G
+from tests.test_gpu_norm import _dev, _inputs
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module")
+def mnb():
+    from block_wise_int4_amd import mnb as m
+    return m
+
+
+def codes_of(mnb, x, w, eps, kind, residual=None):
+    t = G.torch()
+    out, sc = t.full(x.shape, 99, dtype=kind, device="cuda"), t.full((x.shape[0],), -1.0, device="cuda")
+    mnb.mnb_rms_norm(_dev(x), _dev(w), out, eps, residual=None if residual is None else _dev(residual), scales=sc)
+    return G.host(out), G.host(sc)
+
+
+def kinds():
+    t = G.torch()
+    return t.float16, t.int8
+
+
+SIZES = [64, 67, 4099, 40003]       # within one vector a thread, past the vectors, several, past the registers
+
+
+@pytest.mark.parametrize("dt", ["f16", "f32"])
+@pytest.mark.parametrize("k", SIZES)
+def test_a_row_of_zeros_without_eps_has_scale_zero(mnb, k, dt):
+    x, _, w = _inputs(3, k, dt, 20)
+    x[1] = 0
+    for kind in kinds():
+        q, s = codes_of(mnb, x, w, 0.0, kind)
+        assert s[1] == 0 and (q[1] == 0).all()
+        assert (s[[0, 2]] > 0).all() and np.isfinite(s).all()
+
+
+@pytest.mark.parametrize("dt", ["f16", "f32"])
+@pytest.mark.parametrize("k", SIZES)
+@pytest.mark.parametrize("value", [np.inf, -np.inf, np.nan])
+def test_a_bad_value_under_a_zero_weight_still_marks_its_row(mnb, value, k, dt):
+    x, r, w = _inputs(4, k, dt, 21)
+    for at in (3, k - 1):
+        y, u = x.copy(), w.copy()
+        y[2, at], u[at] = value, 0
+        for kind in kinds():
+            q, s = codes_of(mnb, y, u, 1e-5, kind, r)
+            assert np.isnan(s[2]) and (q[2] == 0).all() and np.isfinite(s[[0, 1, 3]]).all(), (at, s)
+
+
+@pytest.mark.parametrize("dt", ["f16", "f32"])
+@pytest.mark.parametrize("k", SIZES)
+def test_a_bad_weight_marks_every_row(mnb, k, dt):
+    x, r, w = _inputs(3, k, dt, 22)
+    x[1], r[1] = 0, 0                                  # 0 times NaN is NaN too
+    for at, value in ((5, np.nan), (k - 1, np.nan), (7, np.inf)):
+        u = w.copy()
+        u[at] = value
+        for kind in kinds():
+            _, s = codes_of(mnb, x, u, 1e-5, kind, r)
+            assert np.isnan(s).all(), (at, value, s)
