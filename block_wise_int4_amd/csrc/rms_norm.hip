@@ -185,7 +185,41 @@ __global__ __launch_bounds__(1024) void rms_norm_kernel(NormParams p)
             mx = max_of(mx, red[1][i]);
         }
     }
-    const float rs = 1.0f / sqrtf(__builtin_fmaf(ss, p.inv_k, p.eps));
+    float var = __builtin_fmaf(ss, p.inv_k, p.eps), pre = 1.0f;
+    if constexpr (sizeof(T) == 4) {
+        // squares past either end of binary32 are summed again from elements scaled by a power of
+        // two (the same choice in every thread: they hold the same sum)
+        if (uniform(!(var <= 0x1p127f) || var < 0x1p-100f)) {
+            pre = var < 1.0f ? 0x1p90f : 0x1p-90f;
+            ss = tid < tail ? th * pre * (th * pre) : 0.0f;
+            auto add = [&](const float* h) {
+#pragma unroll
+                for (int i = 0; i < VE; ++i) ss = __builtin_fmaf(h[i] * pre, h[i] * pre, ss);
+            };
+#pragma unroll
+            for (int u = 0; u < NV; ++u) {
+                if (tid + u * nt < nv) {
+                    float h[VE];
+                    unpack_vec<T>(xv[u], h);
+                    add(h);
+                }
+            }
+            for (int v = tid + NV * nt; v < nv; v += nt) {
+                float h[VE];
+                sum_vec(load(x, v), r ? load(r, v) : u4_t{0, 0, 0, 0}, h);
+                add(h);
+            }
+#pragma unroll
+            for (int off = 32; off > 0; off >>= 1) ss += __shfl_xor(ss, off);
+            __shared__ float again[16];
+            if ((tid & 63) == 0) again[tid >> 6] = ss;
+            __syncthreads();
+            ss = 0.0f;
+            for (int i = 0; i < waves; ++i) ss += again[i];
+            var = __builtin_fmaf(ss, p.inv_k, p.eps * pre * pre);
+        }
+    }
+    const float rs = 1.0f / sqrtf(var);            // of pre h
     // no NaN and no infinity among the row's products (mx holds either)
     const bool fine = uniform(mx < __builtin_inff());
     const double factor = OUT != kNormValues && mx > 0.0f ? 127.0 / (double)mx : 0.0;
@@ -197,7 +231,7 @@ __global__ __launch_bounds__(1024) void rms_norm_kernel(NormParams p)
         const int64_t e = row * K + (int64_t)v * VE;
         if constexpr (OUT == kNormValues) {
 #pragma unroll
-            for (int i = 0; i < VE; ++i) f[i] = h[i] * rs * f[i];
+            for (int i = 0; i < VE; ++i) f[i] = h[i] * pre * rs * f[i];
             *reinterpret_cast<raw_t*>(static_cast<T*>(p.out) + e) = pack_vec<T>(f);
         } else {
             int q[VE];
@@ -245,14 +279,14 @@ __global__ __launch_bounds__(1024) void rms_norm_kernel(NormParams p)
         if (ro) ro[te] = (T)th;
         const int64_t e = row * K + te;
         if constexpr (OUT == kNormValues)
-            static_cast<T*>(p.out)[e] = (T)(th * rs * tw);
+            static_cast<T*>(p.out)[e] = (T)(th * pre * rs * tw);
         else if constexpr (OUT == kNormCodesF16)
             static_cast<_Float16*>(p.out)[e] = (_Float16)(float)(fine ? code_of(th * tw, factor) : 0);
         else
             static_cast<int8_t*>(p.out)[e] = (int8_t)(fine ? code_of(th * tw, factor) : 0);
     }
     if (OUT != kNormValues && tid == 0)
-        p.scales[row] = mx == 0.0f ? 0.0f : fine ? mx * rs / 127.0f : __builtin_nanf("");
+        p.scales[row] = mx == 0.0f ? 0.0f : fine ? mx * pre * rs / 127.0f : __builtin_nanf("");
 }
 
 template <typename T, int OUT>

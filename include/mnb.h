@@ -373,7 +373,8 @@ mnb_status mnb_gemm_accuracy4_noalloc(const mnb_weight_desc* w, const void* repa
  *     NaN or infinite (from x, residual or weight, 0 times infinity included)
  *     has s = NaN and codes 0.
  *     MNB_NORM_CODES_F16 is what mnb_gemm_accuracy4_codes takes.
- * Sums are kept in fp32.  residual_out may be x or residual themselves where
+ * Sums are kept in fp32, of fp32 rows whose squares pass its range scaled by a
+ * power of two.  residual_out may be x or residual themselves where
  * their stride is k.  m <= 2^31-1, 1 <= k <= 2^31-16; m == 0 is a no-op. */
 typedef enum { MNB_NORM_VALUES = 0, MNB_NORM_CODES_F16 = 1, MNB_NORM_CODES_I8 = 2 } mnb_norm_out;
 mnb_status mnb_rms_norm(const void* x, int64_t x_stride, const void* residual, int64_t residual_stride,

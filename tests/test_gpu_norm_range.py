@@ -1,9 +1,11 @@
-"""RMS norm at the ends of its range: rows of zeros without eps, infinities and NaN the weight hides."""
+"""RMS norm at the ends of its range: rows of zeros without eps, infinities and NaN the weight hides, squares past
+binary32."""
 import numpy as np
 import pytest
 
+from oracle import decoder as o
 from tests import gpu_util as G
-from tests.test_gpu_norm import _dev, _inputs
+from tests.test_gpu_norm import _dev, _inputs, _value_tolerance
 
 pytestmark = pytest.mark.gpu
 
@@ -64,3 +66,24 @@ def test_a_bad_weight_marks_every_row(mnb, k, dt):
         for kind in kinds():
             _, s = codes_of(mnb, x, u, 1e-5, kind, r)
             assert np.isnan(s).all(), (at, value, s)
+
+
+@pytest.mark.parametrize("k", SIZES)
+@pytest.mark.parametrize("size,eps", [(1e19, 1e-5), (1e25, 1e-5), (1e36, 0.0), (1e-21, 0.0), (1e-30, 0.0), (1e-30, 1e-58),
+                                      (1e-24, 1e-45)])
+def test_squares_past_binary32(mnb, size, eps, k):
+    """fp32 rows whose squares overflow or vanish, beside rows of usual size."""
+    t = G.torch()
+    x, _, w = _inputs(3, k, "f32", 23)
+    x[1] = np.clip(x[1], -3, 3) * np.float32(size)
+    eps = float(np.float32(eps))                       # as the call receives it
+    _, y = o.rms_norm(x, None, w, eps)
+    out = t.empty((3, k), device="cuda")
+    mnb.mnb_rms_norm(_dev(x), _dev(w), out, eps)
+    assert (np.abs(G.host(out) - y) <= _value_tolerance(y, k, "f32")).all()
+    s, q = o.norm_codes(x, w, eps)
+    for kind in kinds():
+        c, got = codes_of(mnb, x, w, eps, kind)
+        assert (np.abs(got - s) <= s * (0.5 * (k + 2) + 10) * o.EPS32).all()
+        # the products h w are rounded to binary32, whose least normal value is 2^-126
+        assert (np.abs(c - q) <= 0.5 + 2 * 127 * o.EPS32 + 1e-12).all()
