@@ -15,11 +15,13 @@ from typing import Optional, Union
 
 try:                       # device memory and streams; the host-only calls work without it
     import torch
-    # the current stream's handle without building a stream object (2.8 us a call)
+except ImportError:
+    torch = None
+try:                       # the current stream's handle without building a stream object (2.8 us a call)
     from torch._C import _cuda_getCurrentRawStream as _raw_stream, _cuda_getDevice as _current_device
     from torch.cuda import is_initialized as _initialized
-except ImportError:
-    torch = _raw_stream = None
+except ImportError:        # private names: without them torch's public call gives the stream
+    _raw_stream = None
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(HERE, "lib", "libmnb.so")
@@ -173,8 +175,7 @@ def _stream(stream):
     if stream is None:
         if _raw_stream is not None and _initialized():
             return _raw_stream(_current_device())
-        import torch as _t
-        stream = _t.cuda.current_stream()
+        stream = torch.cuda.current_stream()
     if isinstance(stream, int):
         return ctypes.c_void_p(stream)
     return ctypes.c_void_p(stream.cuda_stream)
