@@ -48,7 +48,7 @@ mnb_status fail(mnb_status s, const char* fmt, ...)
 mnb_status ok(const char* variant)
 {
     g_error[0] = 0;
-    g_variant = variant ? variant : "";
+    if (variant) g_variant = variant;
     return MNB_OK;
 }
 

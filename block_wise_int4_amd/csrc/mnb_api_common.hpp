@@ -12,7 +12,8 @@ namespace api {
 
 // Records the reason ("mnb: ...") for this thread and returns s.
 mnb_status fail(mnb_status s, const char* fmt, ...) __attribute__((format(printf, 2, 3)));
-// Clears the thread's error and records the variant it enqueued.
+// Clears the thread's error and records the variant it enqueued; NULL, for a
+// query that enqueues nothing, keeps the last one.
 mnb_status ok(const char* variant);
 mnb_status check_ptr(const void* p, uintptr_t align, const char* name);
 // A gfx950 device must be current.

@@ -197,7 +197,7 @@ size_t mnb_kv4_cache_bytes(const mnb_kv4_desc* c)
         fail(MNB_ERR_INVALID_ARGUMENT, "the cache has no pages");
         return 0;
     }
-    ok("");
+    ok(nullptr);
     return (size_t)(page_bytes(c) * c->num_pages);
 }
 
@@ -288,7 +288,7 @@ size_t mnb_attention_kv4_workspace_bytes(const mnb_kv4_desc* c, int64_t batch, i
                                          int64_t max_kv)
 {
     if (check_bounds(c, batch, tokens, max_q, max_kv) != MNB_OK) return 0;
-    ok("");
+    ok(nullptr);
     if (batch == 0 || tokens == 0 || max_q == 0) return 0;
     return mnb::kv4_attention_workspace(plan_args(c, batch, tokens, max_q, max_kv));
 }

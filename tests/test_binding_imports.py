@@ -37,3 +37,19 @@ class S:
 torch.cuda.current_stream = lambda: S
 assert mnb._stream(None).value == 12 and mnb._stream(S).value == 12 and mnb._stream(7).value == 7
 """)
+
+
+def test_size_queries_keep_the_last_variant():
+    """The last call that enqueued work, or was a no-op, is still named after a query."""
+    _run("""
+import ctypes
+from block_wise_int4_amd import mnb
+from tests.test_decoder_abi import desc, norm
+assert norm(m=0) == 0 and mnb.mnb_last_variant() == "noop"
+assert mnb.mnb_kv4_cache_bytes(desc()) > 0 and mnb.mnb_last_variant() == "noop"
+assert mnb.mnb_attention_kv4_workspace_bytes(desc(), 1, 1, 1, 100000) > 0 and mnb.mnb_last_variant() == "noop"
+assert mnb.mnb_attention_kv4_workspace_bytes(desc(), 0, 0, 0, 0) == 0 and mnb.mnb_last_variant() == "noop"
+assert norm(m=-1) != 0 and mnb.mnb_last_error()
+mnb.mnb_kv4_cache_bytes(desc())
+assert mnb.mnb_last_error() == "" and mnb.mnb_last_variant() == "noop"
+""")
