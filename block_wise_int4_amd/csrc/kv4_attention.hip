@@ -117,9 +117,9 @@ template <int GRP, typename F> __device__ __forceinline__ void for_copies(F f)
 
 // GRP column groups (4: up to 4 rows, 2: up to 8, 1: up to 16 NR).  KW waves
 // share the keys; PF blocks of a wave are in registers, all but the one in work
-// still on their way.  WPE: waves per SIMD that the registers are held to.
-template <int D, int NG, bool F32, int GRP, int NR, int KW, int PF, int WPE>
-__global__ __launch_bounds__(KW * 64, WPE) void kv4_attention_kernel(AttnParams p)
+// still on their way.
+template <int D, int NG, bool F32, int GRP, int NR, int KW, int PF>
+__global__ __launch_bounds__(KW * 64) void kv4_attention_kernel(AttnParams p)
 {
     static_assert(GRP == 1 || NR == 1, "copies of the rows need one column tile");
     typedef typename std::conditional<F32, float, _Float16>::type T;
@@ -663,10 +663,8 @@ hipError_t launch_rows(const AttnParams& p, const Plan& c, hipStream_t s)
     const dim3 grid((unsigned)(p.v.kv_heads * c.splits * c.row_tiles), (unsigned)p.v.batch);
     // as many register sets as the registers hold without spilling
     constexpr bool big = D == 256 || (NR == 2 && F32) || (D == 128 && NG == 4 && (F32 || GRP == 1));
-    constexpr bool lean = NR == 1 && KW == 4 && D == 128 && NG == 1 && !F32;
-    constexpr int PF = KW == 8 ? 4 - 2 * (D == 128 && F32) : big ? 1 : D == 128 && (F32 || NR == 2 || (lean && GRP < 4)) ? 2 : 3;
-    constexpr int WPE = lean ? 3 : 1;
-    kv4_attention_kernel<D, NG, F32, GRP, NR, KW, PF, WPE><<<grid, dim3(KW * 64), 0, s>>>(p);
+    constexpr int PF = KW == 8 ? 4 - 2 * (D == 128 && F32) : big ? 1 : D == 128 && (F32 || NR == 2) ? 2 : 3;
+    kv4_attention_kernel<D, NG, F32, GRP, NR, KW, PF><<<grid, dim3(KW * 64), 0, s>>>(p);
     return hipGetLastError();
 }
 
