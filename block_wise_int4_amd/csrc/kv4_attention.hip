@@ -117,9 +117,11 @@ template <int GRP, typename F> __device__ __forceinline__ void for_copies(F f)
 
 // GRP column groups (4: up to 4 rows, 2: up to 8, 1: up to 16 NR).  KW waves
 // share the keys; PF blocks of a wave are in registers, all but the one in work
-// still on their way.
+// still on their way.  Head size 256 with up to 4 rows is held to two waves a SIMD: with groups of
+// 32 in fp32 it passes 256 registers by 4 otherwise (8 sequences of 4000 keys 27.1 us, 31.8 with
+// one wave; the others fit as they are).
 template <int D, int NG, bool F32, int GRP, int NR, int KW, int PF>
-__global__ __launch_bounds__(KW * 64) void kv4_attention_kernel(AttnParams p)
+__global__ __launch_bounds__(KW * 64, D == 256 && GRP == 4 ? 2 : 1) void kv4_attention_kernel(AttnParams p)
 {
     static_assert(GRP == 1 || NR == 1, "copies of the rows need one column tile");
     typedef typename std::conditional<F32, float, _Float16>::type T;
@@ -266,9 +268,25 @@ __global__ __launch_bounds__(KW * 64) void kv4_attention_kernel(AttnParams p)
 #pragma unroll
                 for (int k = 0; k < 2 * I; ++k) x[n][k / I][k % I] *= qs[n];
         }
-        // ---- masks: a hidden key's logit is -infinity ----
+        // ---- masks, and what the running reference must not fall too far below: of each key its
+        // logit plus the exponent of its value scale, or, where no key is hidden, the largest of
+        // either as a bound ----
         const bool edge = blk * 32 + 32 > whole || blk * 32 < open;
         uint32_t seen[NR];                     // bit t I + i: the row sees the key
+        float mxs[NR];
+        auto largest = [&](int n) {
+            float mx = -__builtin_inff();
+#pragma unroll
+            for (int t = 0; t < 2; ++t)
+#pragma unroll
+                for (int i = 0; i < I; ++i) {
+                    uint32_t w = vwd[t][i * NG];
+#pragma unroll
+                    for (int g = 1; g < NG; ++g) w = max_halves(w, vwd[t][i * NG + g]);
+                    mx = fmaxf(mx, x[n][t][i] + top_exponent(w));
+                }
+            return mx;
+        };
         if (edge) {
 #pragma unroll
             for (int n = 0; n < NR; ++n) {
@@ -282,36 +300,30 @@ __global__ __launch_bounds__(KW * 64) void kv4_attention_kernel(AttnParams p)
                         if (key <= pos[n] && key > below && key < s.len)
                             seen[n] |= 1u << (I * t + i);
                         else
-                            x[n][t][i] = -__builtin_inff();
+                            x[n][t][i] = -__builtin_inff();    // whatever its scale is
                     }
+                mxs[n] = largest(n);
+            }
+        } else {
+            uint32_t w = vwd[0][0];
+#pragma unroll
+            for (int k = 1; k < 2 * I * NG; ++k) w = max_halves(w, vwd[k / (I * NG)][k % (I * NG)]);
+            const float top = top_exponent(w);
+#pragma unroll
+            for (int n = 0; n < NR; ++n) {
+                float m = x[n][0][0];
+#pragma unroll
+                for (int k = 1; k < 2 * I; ++k) m = fmaxf(m, x[n][k / I][k % I]);
+                mxs[n] = m + top;
             }
         }
-        // ---- the running reference: looked at key by key where the largest logit and the
-        // largest scale, of whichever keys, would pass it ----
-        uint32_t most = vwd[0][0];
-#pragma unroll
-        for (int k = 1; k < 2 * I * NG; ++k) most = max_halves(most, vwd[k / (I * NG)][k % (I * NG)]);
-        const float top = top_exponent(most);
 #pragma unroll
         for (int n = 0; n < NR; ++n) {
-            float mx = x[n][0][0];
-#pragma unroll
-            for (int k = 1; k < 2 * I; ++k) mx = fmaxf(mx, x[n][k / I][k % I]);
-            if (__builtin_amdgcn_ballot_w64(mx - M[n] > kRaise - top)) {
-                mx = -__builtin_inff();        // of a key: its logit plus its own scale's exponent
-#pragma unroll
-                for (int t = 0; t < 2; ++t)
-#pragma unroll
-                    for (int i = 0; i < I; ++i) {
-                        uint32_t w = vwd[t][i * NG];
-#pragma unroll
-                        for (int g = 1; g < NG; ++g) w = max_halves(w, vwd[t][i * NG + g]);
-                        mx = fmaxf(mx, x[n][t][i] + (float)((w >> 10) & 31u));
-                    }
-                mx -= 14.0f;                   // as top_exponent
-                mx = fmaxf(mx, __shfl_xor(mx, 16));
-                mx = fmaxf(mx, __shfl_xor(mx, 32));
-                const float next = fmaxf(M[n], mx - kBelow);
+            if (__builtin_amdgcn_ballot_w64(mxs[n] - M[n] > kRaise)) {
+                const float mx = of_quarters(edge ? mxs[n] : largest(n));
+                // by the row's own visible keys alone: neither the rows beside it nor hidden keys
+                // decide a bit of it
+                const float next = mx - M[n] > kRaise ? mx - kBelow : M[n];
                 const float alpha = exp2f(M[n] - next);
                 M[n] = next;
                 l[n] *= alpha;

@@ -13,13 +13,12 @@ namespace mnb {
 namespace kv4 {
 
 constexpr float kLow = -3.402823466e38f;   // "no key yet": below any logit, finite, so that differences are numbers
-// The running reference M of a row is looked at when a logit plus the exponent of
-// a value scale may pass M + kRaise, and is then taken to kBelow under the largest sum of
-// a key's logit and the exponent of its own scale (the largest of its groups), if that is
-// higher.  So p s' stays below 2^kRaise (fp16 ends at 2^16), and the largest p s' of the row
-// is at least 2^(kBelow - 1), 2^23 above fp16's smallest normal value: a term keeps its bits
-// unless it is that much smaller than the row's largest.  Of a key with groups of far
-// different scales, the small groups' dims may lose theirs.
+// The running reference M of a row is raised when the logit of a key plus the exponent
+// of its value scale (the largest of its groups) passes M + kRaise, to kBelow under the
+// largest such sum.  So p s' stays below 2^kRaise (fp16 ends at 2^16), and the largest
+// p s' of the row is at least 2^(kBelow - 1), 2^23 above fp16's smallest normal value: a term
+// keeps its bits unless it is that much smaller than the row's largest.  Of a key with
+// groups of far different scales, the small groups' dims may lose theirs.
 constexpr float kRaise = 15.9f, kBelow = 10.0f;
 
 struct AttnParams {
@@ -59,6 +58,19 @@ __device__ __forceinline__ float scale_of(uint32_t m) { return (float)__builtin_
 // e with s < 2^e of an fp16 scale (low half of a word): -14 for zero and
 // subnormals, 17 for infinity and NaN
 __device__ __forceinline__ float top_exponent(uint32_t word) { return (float)((int)((word >> 10) & 31u) - 14); }
+
+// the largest of a column's four lanes (16 and 32 apart), without a trip through LDS
+__device__ __forceinline__ float of_quarters(float x)
+{
+    uint32_t u = __builtin_bit_cast(uint32_t, x);
+    const auto a = __builtin_amdgcn_permlane16_swap(u, u, false, false);
+    uint32_t lo = a[0], hi = a[1];             // an element by itself: a bit cast of a[1] takes a[0]
+    u = __builtin_bit_cast(uint32_t, fmaxf(__builtin_bit_cast(float, lo), __builtin_bit_cast(float, hi)));
+    const auto b = __builtin_amdgcn_permlane32_swap(u, u, false, false);
+    lo = b[0];
+    hi = b[1];
+    return fmaxf(__builtin_bit_cast(float, lo), __builtin_bit_cast(float, hi));
+}
 
 // the larger of both halves each: of two words, the larger scale in the low half
 __device__ __forceinline__ uint32_t max_halves(uint32_t a, uint32_t b)

@@ -307,64 +307,53 @@ __global__ __launch_bounds__(RW * 64, 2) void kv4_prompt_kernel(AttnParams p)
                 }
             }
         }
-        // ---- the running reference ----
-        float top = vtop[buf][b0];
-        if (KB > 1) top = fmaxf(top, vtop[buf][b0 + KB - 1]);
-        float mx[NR];
-        bool raise = false;
+        // ---- the running reference, of 16 rows at a time ----
+        float top[KB];
+#pragma unroll
+        for (int k = 0; k < KB; ++k) top[k] = vtop[buf][b0 + k];
 #pragma unroll
         for (int n = 0; n < NR; ++n) {
-            mx[n] = y[n][0];
+            float mx = -__builtin_inff();
 #pragma unroll
-            for (int k = 1; k < 8 * KB; ++k) mx[n] = fmaxf(mx[n], y[n][k]);
-            raise |= mx[n] + top > kRaise || (M[n] == kLow && mx[n] > -__builtin_inff());
-        }
-        if (__builtin_amdgcn_ballot_w64(raise)) {
-            // key by key: a logit plus the exponent of its own scale, so that the largest
-            // product of a row sets its reference.  All rows that have risen since move
-            // together: a third as many looks as with those past kRaise alone (2048 and 1100
-            // tokens of 32 heads by 8: 215 us against 230)
+            for (int kb = 0; kb < KB; ++kb) {
+                float m = y[n][8 * kb];
 #pragma unroll
-            for (int n = 0; n < NR; ++n) mx[n] = -__builtin_inff();
-            int own = 4 * quarter;             // opaque: else the scales read here stay in registers until the
-            asm volatile("" : "+v"(own));      // products (37 spilled at head_dim 256, groups of 64, fp32)
-#pragma unroll
-            for (int t = 0; t < 2 * KB; ++t) {
-                u4_t most = {0, 0, 0, 0};      // fp32 scales: their exponents with a bias of 126
-#pragma unroll
-                for (int g = 0; g < NG; ++g) {
-                    const f4_t v4 = *reinterpret_cast<const f4_t*>(&vs[buf][b0 + t / 2][g][t % 2 * 16 + own]);
-                    most = __builtin_elementwise_max(most, __builtin_bit_cast(u4_t, v4));
-                }
-#pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    const float e = __builtin_amdgcn_fmed3f((float)(most[i] >> 23), 112.0f, 143.0f);
-#pragma unroll
-                    for (int n = 0; n < NR; ++n) mx[n] = fmaxf(mx[n], y[n][4 * t + i] + e);
-                }
+                for (int k = 1; k < 8; ++k) m = fmaxf(m, y[n][8 * kb + k]);
+                mx = fmaxf(mx, m + top[kb]);
             }
-            bool move = false;
+            const bool first = M[n] == kLow;
+            if (__builtin_amdgcn_ballot_w64(mx > (first ? -__builtin_inff() : kRaise))) {
+                // key by key: a logit plus the exponent of its own scale, so that the largest
+                // product of a row sets its reference
+                mx = -__builtin_inff();
+                int own = 4 * quarter;         // opaque: else the scales read here stay in registers until the
+                asm volatile("" : "+v"(own));  // products (37 spilled at head_dim 256, groups of 64, fp32)
 #pragma unroll
-            for (int n = 0; n < NR; ++n) {
-                mx[n] = fmaxf(mx[n], __shfl_xor(mx[n], 16));
-                mx[n] = fmaxf(mx[n], __shfl_xor(mx[n], 32)) - 126.0f;   // as top_exponent
-                move |= mx[n] > (M[n] == kLow ? -__builtin_inff() : kBelow);
-            }
-            if (__builtin_amdgcn_ballot_w64(move)) {
+                for (int t = 0; t < 2 * KB; ++t) {
+                    u4_t most = {0, 0, 0, 0};  // fp32 scales: their exponents with a bias of 126
 #pragma unroll
-                for (int n = 0; n < NR; ++n) {
-                    const bool first = M[n] == kLow;
-                    const bool up = mx[n] > (first ? -__builtin_inff() : kBelow);
-                    const float next = up ? Mu[n] + mx[n] - kBelow : Mu[n];
-                    const float alpha = first ? 1.0f : exp2f(Mu[n] - next);   // nothing was summed before the first
-                    const float by = next - Mu[n];
-                    M[n] = up ? next : M[n];
-                    l[n] *= alpha;
+                    for (int g = 0; g < NG; ++g) {
+                        const f4_t v4 = *reinterpret_cast<const f4_t*>(&vs[buf][b0 + t / 2][g][t % 2 * 16 + own]);
+                        most = __builtin_elementwise_max(most, __builtin_bit_cast(u4_t, v4));
+                    }
 #pragma unroll
-                    for (int t = 0; t < NT; ++t) o[n][t] *= alpha;
-#pragma unroll
-                    for (int k = 0; k < 8 * KB; ++k) y[n][k] -= by;
+                    for (int i = 0; i < 4; ++i)
+                        mx = fmaxf(mx, y[n][4 * t + i] + __builtin_amdgcn_fmed3f((float)(most[i] >> 23), 112.0f, 143.0f));
                 }
+                mx = of_quarters(mx) - 126.0f;                     // as top_exponent
+                // a row moves by its own visible keys alone: neither the rows beside it nor hidden
+                // keys, whose scales are in top, decide a bit of it
+                const bool up = mx > (first ? -__builtin_inff() : kRaise);
+                if (!__builtin_amdgcn_ballot_w64(up)) continue;
+                const float next = up ? Mu[n] + mx - kBelow : Mu[n];
+                const float alpha = first ? 1.0f : exp2f(Mu[n] - next);   // nothing was summed before the first
+                const float by = next - Mu[n];
+                M[n] = up ? next : M[n];
+                l[n] *= alpha;
+#pragma unroll
+                for (int t = 0; t < NT; ++t) o[n][t] *= alpha;
+#pragma unroll
+                for (int k = 0; k < 8 * KB; ++k) y[n][k] -= by;
             }
         }
         // ---- p ----

@@ -122,3 +122,44 @@ def test_logits_far_below_zero(mnb, new, split):
         tol = np.abs(seen).mean(0) * ((n + 64) * o.EPS32 + 2.0 ** -22) + 2.0 ** -30
         assert (np.abs(got[t, 0] - seen.mean(0)) <= tol).all(), t
         assert abs(lse[t, 0] - x) <= abs(x) * (D + 16) * o.EPS32, t
+
+
+@pytest.mark.parametrize("dt", ["f16", "f32"])
+@pytest.mark.parametrize("split", [False, True])
+@pytest.mark.parametrize("new", [1, 3, 8, 16, 40, 150])
+def test_a_row_s_bits_come_from_its_own_keys(mnb, new, split, dt):
+    """Neither what lies in places without a token, nor keys that a row does not see, nor the rows beside it decide a
+    bit of it."""
+    t = G.torch()
+    rng = np.random.default_rng((974, new))
+    past, D, H = 100, 128, 2
+    n = past + new
+    table, pages = sequences(rng, [n], 32)
+    geo = o.Geometry(H, 1, D, 64, 32, pages)
+    cache, _ = make_cache(rng, geo, table, [n], k_scale=0.5)     # logits over a wide range: references move often
+    q = (2.0 * rng.normal(size=(new, H, D))).astype(np.float16 if dt == "f16" else np.float32)
+    kw = dict(max_kv=3000 if split else n)
+    want, _ = attend(mnb, geo, cache, table, [n], [0, new], q, D ** -0.5, **kw)
+    words = np.array([0x00080000, 0x00087BFF, 0x00087C00, 0x00087E00, 0xFFFFFFFF], np.uint32)
+    for word in words:                                # places after the last token, keys and values
+        other = cache.copy()
+        for j in range(n, -(-n // 32) * 32):
+            at = geo.base(int(table[0, j // 32]), 0, j % 32) + 32 * D + 8 * (j % 32)
+            other[at:at + 8] = other[at + 256:at + 264] = np.array([word, word], "<u4").view(np.uint8)
+        got, _ = attend(mnb, geo, other, table, [n], [0, new], q, D ** -0.5, **kw)
+        assert t.equal(got, want), hex(word)
+    if new == 1:
+        return
+    for word in words:                                # the last key, which only the last token sees
+        other = cache.copy()
+        at = geo.base(int(table[0, (n - 1) // 32]), 0, (n - 1) % 32) + 32 * D + 8 * ((n - 1) % 32)
+        other[at:at + 8] = other[at + 256:at + 264] = np.array([word, word], "<u4").view(np.uint8)
+        got, _ = attend(mnb, geo, other, table, [n], [0, new], q, D ** -0.5, **kw)
+        assert t.equal(got[:-1], want[:-1]), hex(word)
+    for value in (np.inf, np.nan, 3e4, 0.0):          # one row of queries
+        other = q.copy()
+        other[new // 2, 1] = value
+        got, _ = attend(mnb, geo, cache, table, [n], [0, new], other, D ** -0.5, **kw)
+        keep = t.ones((new, H), dtype=t.bool, device="cuda")
+        keep[new // 2, 1] = False
+        assert t.equal(got[keep], want[keep]), value
