@@ -7,10 +7,11 @@
 //
 // A code minus its zero point is an integer of at most 15 in magnitude: exact
 // in fp16.  So the products run on the fp16 matrix cores on exact operands: q as
-// it is (fp32 queries as a (hi, lo) pair of fp16), scales applied in fp32 to the
-// logits, and the value's scale multiplied into p before p is rounded to fp16.
+// it is (fp32 queries as a (hi, lo) pair of fp16, 22 bits), scales applied in fp32 to
+// the logits, and the value's scale multiplied into p before p is rounded to fp16.
 // That rounding (2^-12 on average over many keys) and the output's are the only
-// ones to 16 bits; in fp32 calls p too is a (hi, lo) pair.
+// ones to 16 bits; in fp32 calls p too is a (hi, lo) pair: the matrix cores' fp32 products
+// run at a sixteenth of their fp16 rate, and two parts cost twice the products.
 //
 // Layout.  A wave computes S^T = K Q^T on v_mfma_f32_16x16x32_f16: 16 keys by
 // 16 columns, the key codes of a lane being one word per 32 dims.  The result
@@ -28,21 +29,22 @@
 // the end, they would cost 14 instructions a block less, but the difference of
 // the two sums loses what a row of equal codes and zero points leaves.)
 //
-// The running reference M of a column is common to its four lanes and is raised
-// only when some lane's logit passes it by 2^14 (a branch of the whole wave),
-// so the usual block needs no exchange between lanes.
+// The running reference M of a column is common to its four lanes and is looked at
+// only when some lane's logit and value scale may pass it by 2^kRaise (a branch of the whole
+// wave), so the usual block needs no exchange between lanes.
 //
 // Work split: the waves of a workgroup share the keys of one set of rows (joined
 // through LDS), and `splits` workgroups share a sequence's keys (joined by a second
 // kernel over fp32 partials), so that a few long sequences fill the chip.
 //
-// Measured, head_dim 128, fp16, 8 key heads by 4: 32 sequences of up to 8192 keys 43.7 us and
-// 5.5 for the join (182 MB: 4.2 TB/s without the join, where a large copy moves 5.15);
-// one of 131072 keys with groups of 64, 30.8 and 4.7 us (151 MB: 4.9 TB/s); one of 1000 keys
-// 10 us, without a join: launch, the chain to the first block, one round trip (a wave asks
-// for its 4 blocks at once), their softmax and the join in LDS.
+// Measured, head_dim 128, fp16, 8 key heads by 4: 32 sequences of up to 8192 keys 42.6 us and
+// 5.1 for the join (182 MB asked for and counted from memory: 4.3 TB/s without the join, where a large
+// copy moves 5.15); one of 131072 keys with groups of 64, 31.3 and 4.7 us (151 MB: 4.8 TB/s); one of
+// 1000 keys 9.8 us, without a join: launch, the chain to the first block, a wave's 4 blocks one
+// after the other (their loads are asked for at once) and the join in LDS, on 8 workgroups: a
+// wave waits 37% of its cycles for data and 25% for an issue slot.
 // 8 sequences of 5 new tokens, 3 heads to a key head, a window of 3000 keys, in fp32 at
-// head_dim 64, 12.0 and 4.5 us: bound by the latency of
+// head_dim 64, 12.0 and 4.6 us: bound by the latency of
 // the chain to the first block, two blocks' work a wave, and the second launch.
 #include "kv4_attention.hpp"
 

@@ -12,14 +12,18 @@
 // registers allow no more) the kernel is bound by the latencies inside a wave, so a wave takes up
 // to 64 keys through its softmax at once: one look at the masks, one at the running
 // reference, and long runs of independent products and exponentials.  LDS reads,
-// products and vector work take about 155, 145 and 205 of 490 thousand cycles of a SIMD at
+// products and vector work take about 155, 145 and 200 of 485 thousand cycles of a SIMD at
 // the long case below: nearly their sum, which the two waves' opposite order and
-// priorities bring down (from 233 us to 217).
+// priorities bring down (from 233 us to 217 when they came in).
 //
 // Measured, head_dim 128, groups of 128, fp16: 2048 and 1100 new tokens of 32 heads by 8
 // key heads 214 us (150 GFLOP: 700 TFLOP/s, where a large fp16 product
 // of the library reaches 1139); 1000 tokens of 32 heads by 32 key
-// heads 32 us, one round of workgroups that lasts as long as its longest key range.
+// heads 33 us, one round of workgroups that lasts as long as its longest key range.  Two more
+// fp32 parts of q and p: 337 us for the first.  Head size 256 has one column tile a wave: 200
+// us with groups of 128 for 1024 and 640 tokens of 16 heads by 4 after a prefix, 388 with groups of
+// 32, whose zero points and scales are loaded late, 469 in fp32 (which holds 6 registers in memory
+// until after the loop; head size 64 in groups of 32 holds two words of a stage there).
 #include "kv4_attention.hpp"
 
 namespace mnb {

@@ -485,9 +485,9 @@ mnb_status mnb_kv4_read(const mnb_kv4_desc* c, const void* cache, const int32_t*
  * positions count from min(kv_len, max_kv).  Logits, sums and outputs are kept in
  * fp32.  The products run on fp16 operands: a weight p times the value's scale
  * is rounded to fp16 once in fp16 calls (as is the output), and in fp32 calls it is
- * the sum of two fp16 parts, 22 bits, as is each element of a query (below 2^-24 of
- * its row's largest with fewer).  A product 2^23 or more below the largest of
- * its row over all keys and groups is held to 2^-34 of that.
+ * the sum of two fp16 parts, 22 bits, as is each element of a query (to 2^-39 of
+ * its row's largest where that is more).  Such a product is also held to no less than
+ * 2^-34 of the largest of its row over all keys and groups.
  * workspace (256-byte aligned): mnb_attention_kv4_workspace_bytes of the same
  * arguments; contents need no initialisation.  batch <= 65535, max_kv <=
  * 2^30, max_q * q_heads < 2^29, scale finite (times log2(e) too).  Deterministic. */
