@@ -8,9 +8,9 @@
 //   q = 127 h w / max|h w|,
 // so the sum of squares and the maximum are found together, by one reduction
 // of the workgroup, and the codes do not depend on how the sum was rounded.
-// h * w is exact in fp32 for fp16 operands; the quotient is formed in fp64 and is
-// off by at most 2^-45 at 127, so a code is off only where the exact quotient is a tie to
-// within that (fp32 operands, whose h w and maximum are rounded: to within 2 x 127 x 2^-24).
+// h * w is exact in fp32 for fp16 operands and in fp64 for fp32 ones; the quotient is formed
+// in fp64 and is off by at most 2^-45 at 127, so a code is off only where the exact quotient is
+// a tie to within that.
 //
 // Bound by memory for many rows, by one round trip and the launch for few.  Measured:
 // 8192 rows of 4096 with a residual, fp16, 46.2 us for 268 MB (5.8 TB/s; a large copy moves
@@ -21,6 +21,8 @@
 // before the reduction's barrier and read once.  Loads and stores are 16 bytes
 // whatever the row's alignment (unaligned access is native here); the last
 // K mod 8 (4) elements go one to a thread.
+#include <type_traits>
+
 #include "mnb_device.hpp"
 #include "mnb_kv4.hpp"
 
@@ -81,13 +83,13 @@ template <typename T> __device__ __forceinline__ u4_t pack_vec(const float* f)
 }
 
 // the larger one, or NaN if either is
-__device__ __forceinline__ float max_of(float a, float b) { return __builtin_elementwise_maximum(a, b); }
+template <typename P> __device__ __forceinline__ P max_of(P a, P b) { return __builtin_elementwise_maximum(a, b); }
 
 // round half away from zero of 127 hw / max, as factor = 127 / max in fp64: at
 // most 127 in magnitude, since no |hw| is above the row's largest
-__device__ __forceinline__ int code_of(float hw, double factor)
+__device__ __forceinline__ int code_of(double hw, double factor)
 {
-    const double t = (double)hw * factor;
+    const double t = hw * factor;
     return (int)(t + __builtin_copysign(0.5, t));
 }
 
@@ -96,7 +98,9 @@ __global__ __launch_bounds__(1024) void rms_norm_kernel(NormParams p)
 {
     constexpr int VE = Vec<T>::N;
     typedef typename Vec<T>::raw raw_t;
-    __shared__ float red[2][16];
+    typedef typename std::conditional<sizeof(T) == 2, float, double>::type prod_t;   // holds h w exactly
+    __shared__ float red[16];
+    __shared__ prod_t red_mx[16];
 
     const int tid = threadIdx.x, nt = blockDim.x;
     const int64_t row = blockIdx.x;
@@ -130,7 +134,8 @@ __global__ __launch_bounds__(1024) void rms_norm_kernel(NormParams p)
             wv[u] = load(w, v);
         }
     }
-    float ss = 0.0f, mx = 0.0f;
+    float ss = 0.0f;
+    prod_t mx = 0;                    // largest |h w|
     float th = 0.0f, tw = 0.0f;       // the thread's element past the vectors
     const int te = nv * VE + tid;
     if (tid < tail) {
@@ -138,7 +143,7 @@ __global__ __launch_bounds__(1024) void rms_norm_kernel(NormParams p)
         if (r) th = (float)(T)(th + (float)r[te]);
         tw = (float)w[te];
         ss = th * th;
-        mx = fabsf(th * tw);
+        mx = __builtin_elementwise_abs((prod_t)th * tw);
     }
     auto add_vec = [&](const float* h, const u4_t& wr) {
 #pragma unroll
@@ -147,7 +152,7 @@ __global__ __launch_bounds__(1024) void rms_norm_kernel(NormParams p)
             float f[VE];
             unpack_vec<T>(wr, f);
 #pragma unroll
-            for (int i = 0; i < VE; ++i) mx = max_of(mx, fabsf(h[i] * f[i]));
+            for (int i = 0; i < VE; ++i) mx = max_of(mx, __builtin_elementwise_abs((prod_t)h[i] * f[i]));
         }
     };
     // the sums replace x in its registers, rounded as they are stored
@@ -174,15 +179,15 @@ __global__ __launch_bounds__(1024) void rms_norm_kernel(NormParams p)
     const int waves = nt >> 6;
     if (waves > 1) {
         if ((tid & 63) == 0) {
-            red[0][tid >> 6] = ss;
-            red[1][tid >> 6] = mx;
+            red[tid >> 6] = ss;
+            red_mx[tid >> 6] = mx;
         }
         __syncthreads();
         ss = 0.0f;
-        mx = 0.0f;
+        mx = 0;
         for (int i = 0; i < waves; ++i) {
-            ss += red[0][i];
-            mx = max_of(mx, red[1][i]);
+            ss += red[i];
+            mx = max_of(mx, red_mx[i]);
         }
     }
     float var = __builtin_fmaf(ss, p.inv_k, p.eps), pre = 1.0f;
@@ -221,8 +226,8 @@ __global__ __launch_bounds__(1024) void rms_norm_kernel(NormParams p)
     }
     const float rs = 1.0f / sqrtf(var);            // of pre h
     // no NaN and no infinity among the row's products (mx holds either)
-    const bool fine = uniform(mx < __builtin_inff());
-    const double factor = OUT != kNormValues && mx > 0.0f ? 127.0 / (double)mx : 0.0;
+    const bool fine = uniform(mx < (prod_t)__builtin_inff());
+    const double factor = OUT != kNormValues && mx > 0 ? 127.0 / (double)mx : 0.0;
 
     auto store_vec = [&](int v, const float* h, const u4_t& wr) {
         if (ro) *reinterpret_cast<raw_t*>(ro + (int64_t)v * VE) = pack_vec<T>(h);
@@ -239,7 +244,7 @@ __global__ __launch_bounds__(1024) void rms_norm_kernel(NormParams p)
             for (int i = 0; i < VE; ++i) q[i] = 0;
             if (fine) {
 #pragma unroll
-                for (int i = 0; i < VE; ++i) q[i] = code_of(h[i] * f[i], factor);
+                for (int i = 0; i < VE; ++i) q[i] = code_of((prod_t)h[i] * f[i], factor);
             }
             if constexpr (OUT == kNormCodesF16) {
                 typedef uint32_t out_t __attribute__((ext_vector_type(VE / 2), aligned(2), may_alias));
@@ -281,12 +286,12 @@ __global__ __launch_bounds__(1024) void rms_norm_kernel(NormParams p)
         if constexpr (OUT == kNormValues)
             static_cast<T*>(p.out)[e] = (T)(th * pre * rs * tw);
         else if constexpr (OUT == kNormCodesF16)
-            static_cast<_Float16*>(p.out)[e] = (_Float16)(float)(fine ? code_of(th * tw, factor) : 0);
+            static_cast<_Float16*>(p.out)[e] = (_Float16)(float)(fine ? code_of((prod_t)th * tw, factor) : 0);
         else
-            static_cast<int8_t*>(p.out)[e] = (int8_t)(fine ? code_of(th * tw, factor) : 0);
+            static_cast<int8_t*>(p.out)[e] = (int8_t)(fine ? code_of((prod_t)th * tw, factor) : 0);
     }
     if (OUT != kNormValues && tid == 0)
-        p.scales[row] = mx == 0.0f ? 0.0f : fine ? mx * pre * rs / 127.0f : __builtin_nanf("");
+        p.scales[row] = mx == 0 ? 0.0f : fine ? (float)(mx * pre * rs / 127) : __builtin_nanf("");
 }
 
 template <typename T, int OUT>

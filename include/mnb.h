@@ -368,7 +368,7 @@ mnb_status mnb_gemm_accuracy4_noalloc(const mnb_weight_desc* w, const void* repa
  *   MNB_NORM_CODES_I8   the same codes as int8 [m, k]; scales fp32 [m]:
  *     s = max|y| / 127 and q = y / s to the nearest integer, halves away from
  *     zero, formed as 127 h w / max|h w| (the norm's factor cancels) in 64
- *     bits from the product h w in binary32.  A row whose products are all 0
+ *     bits from the exact products.  A row whose products are all 0
  *     has s = 0 and codes 0, with eps = 0 too; a row with a product that is
  *     NaN or infinite (from x, residual or weight, 0 times infinity included)
  *     has s = NaN and codes 0.

@@ -1,5 +1,5 @@
 """RMS norm at the ends of its range: rows of zeros without eps, infinities and NaN the weight hides, squares past
-binary32."""
+binary32, quotients that only the exact products place on their side of a tie."""
 import numpy as np
 import pytest
 
@@ -87,3 +87,24 @@ def test_squares_past_binary32(mnb, size, eps, k):
         assert (np.abs(got - s) <= s * (0.5 * (k + 2) + 10) * o.EPS32).all()
         # the products h w are rounded to binary32, whose least normal value is 2^-126
         assert (np.abs(c - q) <= 0.5 + 2 * 127 * o.EPS32 + 1e-12).all()
+
+
+@pytest.mark.parametrize("k", SIZES)
+def test_quotients_beside_ties(mnb, k):
+    """fp32 elements whose quotients lie within 4e-6 of a tie: the products in 64 bits decide."""
+    rng = np.random.default_rng((24, k))
+    x = rng.normal(size=(1, k)).astype(np.float32)
+    x[0, 0] = np.float32(3.3)
+    w = np.ones(k, np.float32)
+    w[0] = np.float32(1.7)
+    top = float(x[0, 0]) * float(w[0])                 # exact in 64 bits, not in 32
+    want = rng.integers(-126, 126, k) + 0.5
+    w[1:] = (want[1:] * top / 127.0 / x[0, 1:].astype(np.float64)).astype(np.float32)
+    q = 127.0 * (x[0].astype(np.float64) * w.astype(np.float64)) / top
+    near = np.abs(np.abs(q) % 1 - 0.5)
+    assert 126.999 < np.abs(q).max() < 127.001 and np.median(near[1:]) < 4e-6
+    sure = near > 1e-10
+    want = np.trunc(q + np.copysign(0.5, q))
+    for kind in kinds():
+        c, s = codes_of(mnb, x, w, 1e-5, kind)
+        assert (c[0, sure] == want[sure]).all(), int((c[0, sure] != want[sure]).sum())
