@@ -119,11 +119,11 @@ template <int GRP, typename F> __device__ __forceinline__ void for_copies(F f)
 
 // GRP column groups (4: up to 4 rows, 2: up to 8, 1: up to 16 NR).  KW waves
 // share the keys; PF blocks of a wave are in registers, all but the one in work
-// still on their way.  Head size 256 with up to 4 rows is held to two waves a SIMD: with groups of
-// 32 in fp32 it passes 256 registers by 4 otherwise (8 sequences of 4000 keys 27.1 us, 31.8 with
-// one wave; the others fit as they are).
+// still on their way.  Head size 256 is held to two waves a SIMD where that costs no more than 2
+// registers in memory: with groups of 32 in fp32 and up to 4 rows (8 sequences of 4000 keys 26.6 us,
+// 31.8 with one wave), and with larger groups.
 template <int D, int NG, bool F32, int GRP, int NR, int KW, int PF>
-__global__ __launch_bounds__(KW * 64, D == 256 && GRP == 4 ? 2 : 1) void kv4_attention_kernel(AttnParams p)
+__global__ __launch_bounds__(KW * 64, D == 256 && (GRP == 4 || NG <= 4) ? 2 : 1) void kv4_attention_kernel(AttnParams p)
 {
     static_assert(GRP == 1 || NR == 1, "copies of the rows need one column tile");
     typedef typename std::conditional<F32, float, _Float16>::type T;
@@ -228,8 +228,10 @@ __global__ __launch_bounds__(KW * 64, D == 256 && GRP == 4 ? 2 : 1) void kv4_att
             words<I * NG>(slot + (t * 16 + mine) * NG, kwd[t]);
             words<I * NG>(slot + (32 + t * 16 + mine) * NG, vwd[t]);
         }
-        // ---- logits ----
-        float x[NR][2][I];
+        // ---- logits less M ----
+        float x[NR][2][I], Mu[NR];
+#pragma unroll
+        for (int n = 0; n < NR; ++n) Mu[n] = M[n] == kLow ? 0.0f : M[n];
 #pragma unroll
         for (int t = 0; t < 2; ++t) {
 #pragma unroll
@@ -260,7 +262,9 @@ __global__ __launch_bounds__(KW * 64, D == 256 && GRP == 4 ? 2 : 1) void kv4_att
                             dot = (copy & 2) ? e1 : e0;
                         }
                         const float ks = scale_of(kwd[t][i * NG + g]) * p.scale_log2;
-                        x[n][t][i] = g == 0 ? dot * ks : __builtin_fmaf(dot, ks, x[n][t][i]);
+                        // fp32 queries come back to their scale last, with M
+                        const float add = g == 0 ? (F32 ? 0.0f : -Mu[n]) : x[n][t][i];
+                        x[n][t][i] = __builtin_fmaf(dot, ks, add);
                     }
             }
         }
@@ -268,7 +272,7 @@ __global__ __launch_bounds__(KW * 64, D == 256 && GRP == 4 ? 2 : 1) void kv4_att
 #pragma unroll
             for (int n = 0; n < NR; ++n)
 #pragma unroll
-                for (int k = 0; k < 2 * I; ++k) x[n][k / I][k % I] *= qs[n];
+                for (int k = 0; k < 2 * I; ++k) x[n][k / I][k % I] = __builtin_fmaf(x[n][k / I][k % I], qs[n], -Mu[n]);
         }
         // ---- masks, and what the running reference must not fall too far below: of each key its
         // logit plus the exponent of its value scale, or, where no key is hidden, the largest of
@@ -321,16 +325,21 @@ __global__ __launch_bounds__(KW * 64, D == 256 && GRP == 4 ? 2 : 1) void kv4_att
         }
 #pragma unroll
         for (int n = 0; n < NR; ++n) {
-            if (__builtin_amdgcn_ballot_w64(mxs[n] - M[n] > kRaise)) {
+            const bool first = M[n] == kLow;
+            if (__builtin_amdgcn_ballot_w64(mxs[n] > (first ? -__builtin_inff() : kRaise))) {
                 const float mx = of_quarters(edge ? mxs[n] : largest(n));
                 // by the row's own visible keys alone: neither the rows beside it nor hidden keys
                 // decide a bit of it
-                const float next = mx - M[n] > kRaise ? mx - kBelow : M[n];
-                const float alpha = exp2f(M[n] - next);
-                M[n] = next;
+                const bool up = mx > (first ? -__builtin_inff() : kRaise);
+                const float next = up ? Mu[n] + mx - kBelow : Mu[n];
+                const float alpha = first ? 1.0f : exp2f(Mu[n] - next);   // nothing was summed before the first
+                const float by = next - Mu[n];
+                M[n] = up ? next : M[n];
                 l[n] *= alpha;
 #pragma unroll
                 for (int t = 0; t < NT; ++t) o[n][t] *= alpha;
+#pragma unroll
+                for (int k = 0; k < 2 * I; ++k) x[n][k / I][k % I] -= by;
             }
         }
         // ---- p ----
@@ -339,7 +348,7 @@ __global__ __launch_bounds__(KW * 64, D == 256 && GRP == 4 ? 2 : 1) void kv4_att
 #pragma unroll
             for (int k = 0; k < 2 * I; ++k) {
                 float& e = x[n][k / I][k % I];
-                e = __builtin_amdgcn_exp2f(e - M[n]);
+                e = __builtin_amdgcn_exp2f(e);
                 l[n] += e;
             }
         // ---- O^T += V^T (p s')^T, group by group ----

@@ -1,4 +1,4 @@
-"""The attention's range: value scales far apart, logits far below zero."""
+"""The attention's range: value scales far apart, logits far below zero, large logits close together."""
 import numpy as np
 import pytest
 
@@ -163,3 +163,37 @@ def test_a_row_s_bits_come_from_its_own_keys(mnb, new, split, dt):
         keep = t.ones((new, H), dtype=t.bool, device="cuda")
         keep[new // 2, 1] = False
         assert t.equal(got[keep], want[keep]), value
+
+
+@pytest.mark.parametrize("dt", ["f16", "f32"])
+@pytest.mark.parametrize("size", [2 ** 20, 2 ** 22, 2 ** 24, 2 ** 26])
+@pytest.mark.parametrize("new", [1, 6, 16, 30, 40])
+def test_large_logits_that_differ_little(mnb, new, size, dt):
+    """Logits of `size` (in units of log2) apart by a few units, beside value scales just below a power of two: whatever is
+    left of the differences, the outputs are means of the values."""
+    rng = np.random.default_rng((975, new, size))
+    D, n, half = 128, 500, 64
+    table, pages = sequences(rng, [n], 32)
+    geo = o.Geometry(1, 1, D, D, 32, pages)
+    cache, _ = make_cache(rng, geo, table, [n])
+    u = rng.choice([-1, 1], half)
+    V = np.zeros((n, D))
+    for j in range(n):
+        codes = np.concatenate([8 + 4 * u, rng.integers(0, 16, half)])
+        o.store(geo, cache, int(table[0, j // 32]), 0, j % 32, False, codes, np.full(1, 8, np.float16), np.full(1, 8))
+        s = np.float16(0.9995 * 2.0 ** rng.integers(-3, 4))
+        vc = rng.integers(0, 16, D)
+        o.store(geo, cache, int(table[0, j // 32]), 0, j % 32, True, vc, np.full(1, s, np.float16), np.full(1, 8))
+        V[j] = (vc - 8.0) * float(s)
+    scale = size * np.log(2.0) / (half * 4 * 8 * 6e4)
+    q = np.zeros((new, 1, D), np.float16 if dt == "f16" else np.float32)
+    q[:, 0, :half] = 6e4 * u
+    # codes less 8 have a deviation of 4.6: logits apart by about 6
+    q[:, 0, half:] = rng.normal(size=(new, half)) * 6 / (scale * 1.44 * 8 * 4.6 * 8)
+    out, lse = attend(mnb, geo, cache, table, [n], [0, new], q, scale)
+    got, lse = G.host(out)[:, 0], G.host(lse)
+    assert np.isfinite(got).all() and np.isfinite(lse).all()
+    lo, hi = np.minimum.accumulate(V, 0)[n - new:], np.maximum.accumulate(V, 0)[n - new:]
+    slack = 2.0 ** -9 * np.maximum(np.abs(lo), np.abs(hi))     # p s' and the output rounded to fp16, sums in fp32
+    assert (got >= lo - slack).all() and (got <= hi + slack).all()
+    assert (np.abs(lse / np.log(2.0) - size) <= 64 + size * 2.0 ** -15).all()
