@@ -23,8 +23,8 @@
 // Measured, head_dim 128, fp16, 32 heads by 8: 9665 prompt tokens with
 // groups of 64, 52 us (append, 209 MB, and 216 counted in memory, so the L2 joins the parts of
 // lines: 4.0 TB/s, where a large copy moves 5.15; the values' single bytes are four stores a
-// lane) and 18.9 us (read, 51 MB: 2.7 TB/s; a lane loads eight single bytes for its values and
-// uses one nibble of each); one token of each of 16 sequences 4.6 and 3.3 us, the chain's latency.
+// lane) and 18.8 us (read, 51 MB: 2.7 TB/s; a lane loads eight single bytes for its values and
+// uses one nibble of each); one token of each of 16 sequences 4.6 and 3.2 us, the chain's latency.
 #include "kv4_index.hpp"
 #include "mnb_device.hpp"
 #include "mnb_kv4.hpp"

@@ -37,9 +37,9 @@
 // through LDS), and `splits` workgroups share a sequence's keys (joined by a second
 // kernel over fp32 partials), so that a few long sequences fill the chip.
 //
-// Measured, head_dim 128, fp16, 8 key heads by 4: 32 sequences of up to 8192 keys 43.2 us and
-// 5.2 for the join (182 MB asked for and counted from memory: 4.2 TB/s without the join, where a large
-// copy moves 5.15); one of 131072 keys with groups of 64, 31.2 and 4.7 us (151 MB: 4.8 TB/s); one of
+// Measured, head_dim 128, fp16, 8 key heads by 4: 32 sequences of up to 8192 keys 44.4 us and
+// 5.3 for the join (182 MB asked for and counted from memory: 4.1 TB/s without the join, where a large
+// copy moves 5.15); one of 131072 keys with groups of 64, 30.7 and 4.7 us (151 MB: 4.9 TB/s); one of
 // 1000 keys 9.9 us, without a join: launch, the chain to the first block, a wave's 4 blocks one
 // after the other (their loads are asked for at once) and the join in LDS, on 8 workgroups: a
 // wave waits 37% of its cycles for data and 25% for an issue slot.

@@ -13,9 +13,9 @@
 // a tie to within that.
 //
 // Bound by memory for many rows, by one round trip and the launch for few.  Measured:
-// 8192 rows of 4096 with a residual, fp16, 45.9 us for 268 MB (5.9 TB/s; a large copy moves
-// 5.15), fp32 92 us; 1023 rows of 11008 to fp16 codes, fp32, 32.5 us for 158 MB (4.9 TB/s), to
-// int8 codes 33 us for 146; 1 row 2.3 us, 16 rows to codes 3.6 us.
+// 8192 rows of 4096 with a residual, fp16, 45.8 us for 268 MB (5.9 TB/s; a large copy moves
+// 5.15), fp32 92 us; 1023 rows of 11008 to fp16 codes, fp32, 32.7 us for 158 MB (4.8 TB/s), to
+// int8 codes 33 us for 146; 1 row 2.3 us, 16 rows to codes 3.4 us.
 //
 // One workgroup holds one row in registers: every input byte is requested
 // before the reduction's barrier and read once.  Loads and stores are 16 bytes
