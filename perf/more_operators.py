@@ -21,38 +21,38 @@ DEV = "cuda"
 def listed():
     return [
         # a chat with one user whose request has an adapter: latency
-        dict(name="adapters, one token", op="adapters", batch=1, new=1, k=4096, n=4096, rank=16, count=8, mixed=False,
+        dict(name="adapters: one token", op="adapters", batch=1, new=1, k=4096, n=4096, rank=16, count=8, mixed=False,
              wide=0, base=True, dtype="f16"),
         # one new token of each of 32 requests, most with an adapter of their own; q is a slice of the fused q, k, v
-        dict(name="adapters, 32 requests", op="adapters", batch=32, new=1, k=4096, n=4096, rank=16, count=24,
+        dict(name="adapters: 32 requests", op="adapters", batch=32, new=1, k=4096, n=4096, rank=16, count=24,
              mixed=False, wide=2048, base=True, dtype="f16"),
         # drafts of 20 requests to verify, a feed-forward layer's way down, adapters of different ranks
-        dict(name="adapters, 20 requests of 5 rows", op="adapters", batch=20, new=5, k=11008, n=4096, rank=64, count=12,
+        dict(name="adapters: 20 requests of 5 rows", op="adapters", batch=20, new=5, k=11008, n=4096, rank=64, count=12,
              mixed=True, wide=0, base=True, dtype="f16"),
         # prompts of five requests, of uneven length, in one call
-        dict(name="adapters, prompts", op="adapters", batch=5, new=2500, k=4096, n=11008, rank=32, count=4, mixed=False,
+        dict(name="adapters: prompts", op="adapters", batch=5, new=2500, k=4096, n=11008, rank=32, count=4, mixed=False,
              wide=0, base=True, dtype="f16"),
         # fp32 activations, odd sizes, the adapters' part by itself
-        dict(name="adapters, fp32, odd sizes", op="adapters", batch=7, new=150, k=2050, n=1001, rank=12, count=5,
+        dict(name="adapters: fp32 and odd sizes", op="adapters", batch=7, new=150, k=2050, n=1001, rank=12, count=5,
              mixed=True, wide=3, base=False, dtype="f32"),
         # a long chat of one user, one token
-        dict(name="sinks, one sequence", op="sinks", batch=1, new=1, kv=30000, window=4096, sinks=4, q_heads=32,
+        dict(name="sinks: one sequence", op="sinks", batch=1, new=1, kv=30000, window=4096, sinks=4, q_heads=32,
              kv_heads=8, dim=128, group=128, page=64, dtype="f16"),
         # a serving batch of long chats
-        dict(name="sinks, batch of 32", op="sinks", batch=32, new=1, kv=16384, window=4096, sinks=4, q_heads=32,
+        dict(name="sinks: batch of 32", op="sinks", batch=32, new=1, kv=16384, window=4096, sinks=4, q_heads=32,
              kv_heads=8, dim=128, group=128, page=64, dtype="f16"),
         # speculative verify in fp32, small heads, fine groups, a whole instruction kept visible
-        dict(name="sinks, verify fp32", op="sinks", batch=8, new=5, kv=4100, window=1000, sinks=100, q_heads=24,
+        dict(name="sinks: verify fp32", op="sinks", batch=8, new=5, kv=4100, window=1000, sinks=100, q_heads=24,
              kv_heads=8, dim=64, group=32, page=32, dtype="f32"),
         # chunks of a document behind what is cached of it
-        dict(name="sinks, prompt chunks", op="sinks", batch=2, new=2048, kv=8192, window=2048, sinks=16, q_heads=32,
+        dict(name="sinks: prompt chunks", op="sinks", batch=2, new=2048, kv=8192, window=2048, sinks=16, q_heads=32,
              kv_heads=8, dim=128, group=128, page=64, dtype="f16"),
         # four drafts of one request
-        dict(name="verify, one sequence", op="verify", batch=1, new=5, vocab=32000, draft=True, top=0, dtype="f32"),
+        dict(name="verify: one sequence", op="verify", batch=1, new=5, vocab=32000, draft=True, top=0, dtype="f32"),
         # seven drafts of each of 32 requests, a large vocabulary
-        dict(name="verify, 32 sequences", op="verify", batch=32, new=8, vocab=128000, draft=True, top=0, dtype="f32"),
+        dict(name="verify: 32 sequences", op="verify", batch=32, new=8, vocab=128000, draft=True, top=0, dtype="f32"),
         # drafts that were looked up, not drawn; 50 tokens are left to choose from; an odd vocabulary
-        dict(name="verify, certain drafts", op="verify", batch=16, new=6, vocab=50257, draft=False, top=50, dtype="f16"),
+        dict(name="verify: certain drafts", op="verify", batch=16, new=6, vocab=50257, draft=False, top=50, dtype="f16"),
     ]
 
 
