@@ -122,8 +122,11 @@ template <int GRP, typename F> __device__ __forceinline__ void for_copies(F f)
 // still on their way.  Head size 256 is held to two waves a SIMD where that costs no more than 2
 // registers in memory: with groups of 32 in fp32 and up to 4 rows (8 sequences of 4000 keys 26.6 us,
 // 31.8 with one wave), and with larger groups.
-template <int D, int NG, bool F32, int GRP, int NR, int KW, int PF>
-__global__ __launch_bounds__(KW * 64, D == 256 && (GRP == 4 || NG <= 4) ? 2 : 1) void kv4_attention_kernel(AttnParams p)
+// GAP: the call with first tokens that stay visible; the call without keeps its own
+// instances, some of which have no register left for the gap (with groups of 64 in fp32 and more than 8
+// rows at head size 256, 17 would be in memory).
+template <int D, int NG, bool F32, int GRP, int NR, int KW, int PF, bool GAP>
+__global__ __launch_bounds__(KW * 64, D == 256 && (GRP == 4 || NG <= 4) && !(GAP && F32 && NG == 4 && GRP == 1) ? 2 : 1) void kv4_attention_kernel(AttnParams p)
 {
     static_assert(GRP == 1 || NR == 1, "copies of the rows need one column tile");
     typedef typename std::conditional<F32, float, _Float16>::type T;
@@ -151,21 +154,21 @@ __global__ __launch_bounds__(KW * 64, D == 256 && (GRP == 4 || NG <= 4) ? 2 : 1)
     const int32_t* table = v.table + (int64_t)b * v.table_stride;
     const int c0 = split * p.chunk, c1 = c0 + p.chunk;
     int pages = 0;
-    if (p.window == 0) pages = pages_from(v, table, (c0 >> 5) + kw, KW, lane);
+    if (!GAP && p.window == 0) pages = pages_from(v, Span{}, table, (c0 >> 5) + kw, KW, lane);
 
     const Sequence s = sequence_of(v, b, p.max_q, p.max_kv);
     const int rows = s.count * p.gqa;
     const int row0 = tile * kRows;
     if (row0 >= rows) return;                  // the whole workgroup
     const int last_row = row0 + kRows <= rows ? row0 + kRows - 1 : rows - 1;
-    int lo, hi;
-    key_range(p.causal, p.window, s, row0 / p.gqa, last_row / p.gqa, lo, hi);
+    const Span span = span_of(p.causal, p.window, GAP ? p.sinks : -1, s, row0 / p.gqa, last_row / p.gqa);
     // this split's part, in blocks
-    const int from = lo > c0 ? lo : c0, to = hi < c1 ? hi : c1;
+    const int from = span.lo > c0 ? span.lo : c0, to = span.hi < c1 ? span.hi : c1;
     const bool any = from < to;
     if (p.splits > 1 && !any) return;          // the join reads only splits with keys
     const int blk0 = from >> 5, blk1 = any ? (to + 31) >> 5 : blk0;
-    if (p.window > 0) pages = pages_from(v, table, blk0 + kw, KW, lane);
+    if (GAP || p.window > 0) pages = pages_from(v, span, table, blk0 + kw, KW, lane);
+    auto real = [&](int blk) { return GAP ? span.at(blk) : blk; };   // a block of the count in the sequence
 
     const int nblk = 1 << (v.page_shift - 5);
     const int64_t block_bytes = kv_block_bytes(D, NG);
@@ -298,12 +301,16 @@ __global__ __launch_bounds__(KW * 64, D == 256 && (GRP == 4 || NG <= 4) ? 2 : 1)
             for (int n = 0; n < NR; ++n) {
                 seen[n] = 0;
                 const int below = p.causal && p.window > 0 ? pos[n] - p.window : -1;
+                // keys from the first tokens' end to the window are hidden too
+                const uint32_t hidden = below >= p.sinks ? below - p.sinks + 1 : 0;
+                const int most = pos[n] < s.len ? pos[n] : s.len - 1, at = blk * 32 + mine;
 #pragma unroll
                 for (int t = 0; t < 2; ++t)
 #pragma unroll
                     for (int i = 0; i < I; ++i) {
                         const int key = blk * 32 + t * 16 + mine + i;
-                        if (key <= pos[n] && key > below && key < s.len)
+                        if (GAP ? t * 16 + i <= most - at && (uint32_t)(at - p.sinks) + (t * 16 + i) >= hidden
+                                : key <= pos[n] && key > below && key < s.len)
                             seen[n] |= 1u << (I * t + i);
                         else
                             x[n][t][i] = -__builtin_inff();    // whatever its scale is
@@ -443,29 +450,29 @@ __global__ __launch_bounds__(KW * 64, D == 256 && (GRP == 4 || NG <= 4) ? 2 : 1)
         RawBlock<D, NG> set[PF];
 #pragma unroll
         for (int i = 0; i < PF; ++i)
-            load_block<D, NG>(block_at(page_in(v, pages, i), blk + i * KW), blk + i * KW < blk1, lane, set[i]);
+            load_block<D, NG>(block_at(page_in(v, pages, i), real(blk + i * KW)), blk + i * KW < blk1, lane, set[i]);
         // whole turns of the sets, then what is left: no branch between a load and
         // its use but the refill's, whose load is waited for where it is made
         const int steps = (blk1 - blk + KW - 1) / KW;
         int at = PF;                           // lane of `pages` with the next load's page
         for (int turn = 0; turn < steps / PF; ++turn) {
             if (at > 64 - PF) {
-                pages = pages_from(v, table, blk + PF * KW, KW, lane);
+                pages = pages_from(v, span, table, blk + PF * KW, KW, lane);
                 at = 0;
                 asm volatile("" : "+v"(pages));
             }
 #pragma unroll
             for (int i = 0; i < PF; ++i) {
-                compute(set[i], blk);
+                compute(set[i], real(blk));
                 const int next = blk + PF * KW;
-                load_block<D, NG>(block_at(page_in(v, pages, at), next), next < blk1, lane, set[i]);
+                load_block<D, NG>(block_at(page_in(v, pages, at), real(next)), next < blk1, lane, set[i]);
                 ++at;
                 blk += KW;
             }
         }
 #pragma unroll
         for (int i = 0; i < PF - 1; ++i)
-            if (i < steps % PF) compute(set[i], blk + i * KW);
+            if (i < steps % PF) compute(set[i], real(blk + i * KW));
     }
 #pragma unroll
     for (int n = 0; n < NR; ++n) {             // the sum of a column over its lanes
@@ -552,14 +559,13 @@ __global__ __launch_bounds__(KW * 64, D == 256 && (GRP == 4 || NG <= 4) ? 2 : 1)
 // Returns how many, the first one in s0.
 __device__ __forceinline__ int splits_of(const AttnParams& p, const Sequence& s, int i, int h, int& s0)
 {
-    int lo, hi;
     const int r = i * p.gqa + h % p.gqa;
     const int rows = s.count * p.gqa;
     const int r0 = r / p.rows_per_wg * p.rows_per_wg;
     const int r1 = r0 + p.rows_per_wg <= rows ? r0 + p.rows_per_wg - 1 : rows - 1;
-    key_range(p.causal, p.window, s, r0 / p.gqa, r1 / p.gqa, lo, hi);
-    s0 = lo / p.chunk;
-    return hi > lo ? (hi + p.chunk - 1) / p.chunk - s0 : 0;
+    const Span span = span_of(p.causal, p.window, p.sinks, s, r0 / p.gqa, r1 / p.gqa);
+    s0 = span.lo / p.chunk;
+    return span.hi > span.lo ? (span.hi + p.chunk - 1) / p.chunk - s0 : 0;
 }
 
 constexpr int kJoinThreads = 256;
@@ -687,7 +693,8 @@ hipError_t launch_rows(const AttnParams& p, const Plan& c, hipStream_t s)
     // as many register sets as the registers hold without spilling
     constexpr bool big = D == 256 || (NR == 2 && F32) || (D == 128 && NG == 4 && (F32 || GRP == 1));
     constexpr int PF = KW == 8 ? 4 - 2 * (D == 128 && F32) : big ? 1 : D == 128 && (F32 || NR == 2) ? 2 : 3;
-    kv4_attention_kernel<D, NG, F32, GRP, NR, KW, PF><<<grid, dim3(KW * 64), 0, s>>>(p);
+    if (p.sinks >= 0 && p.window > 0) kv4_attention_kernel<D, NG, F32, GRP, NR, KW, PF, true><<<grid, dim3(KW * 64), 0, s>>>(p);
+    else kv4_attention_kernel<D, NG, F32, GRP, NR, KW, PF, false><<<grid, dim3(KW * 64), 0, s>>>(p);
     return hipGetLastError();
 }
 
@@ -782,6 +789,7 @@ hipError_t launch_kv4_attention(const AttentionArgs& a, hipStream_t stream, cons
     p.scale_log2 = a.scale * kLog2E;
     p.causal = a.causal;
     p.window = kv4::window_of(a.window, a.max_kv);
+    p.sinks = a.sinks < a.max_kv ? (int)a.sinks : (int)a.max_kv;
     p.max_q = (int)a.max_q;
     p.max_kv = (int)a.max_kv;
     p.gqa = a.v.q_heads / a.v.kv_heads;
@@ -789,8 +797,12 @@ hipError_t launch_kv4_attention(const AttentionArgs& a, hipStream_t stream, cons
     p.chunk = c.chunk;
     p.row_tiles = c.row_tiles;
     p.rows_per_wg = c.rows;
-    *variant = c.kind == 2 ? (c.splits > 1 ? "attention_kv4_prompt_split" : "attention_kv4_prompt")
-                           : (c.splits > 1 ? "attention_kv4_split" : "attention_kv4");
+    if (a.sinks < 0)
+        *variant = c.kind == 2 ? (c.splits > 1 ? "attention_kv4_prompt_split" : "attention_kv4_prompt")
+                               : (c.splits > 1 ? "attention_kv4_split" : "attention_kv4");
+    else
+        *variant = c.kind == 2 ? (c.splits > 1 ? "attention_kv4_sinks_prompt_split" : "attention_kv4_sinks_prompt")
+                               : (c.splits > 1 ? "attention_kv4_sinks_split" : "attention_kv4_sinks");
     const hipError_t e = c.kind == 2 ? kv4::launch_prompt(p, c, a.f16, stream) : kv4::launch_few_rows(p, c, a.f16, stream);
     if (e != hipSuccess || c.splits == 1) return e;
     return kv4::launch_join(p, a.f16, stream);

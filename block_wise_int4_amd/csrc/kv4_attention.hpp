@@ -32,6 +32,7 @@ struct AttnParams {
     float scale_log2;
     int causal;
     int window;                       // 0: none; else below max_kv
+    int sinks;                        // first keys that stay visible; -1: keys are counted from the first
     int max_q, max_kv;
     int gqa;                          // query heads per key head
     int splits, chunk;                // keys per split, a multiple of 32
@@ -121,12 +122,12 @@ template <int NJ> __device__ __forceinline__ float load_query(const float* q, h8
     return __builtin_bit_cast(float, (uint32_t)(127 + e) << 23);
 }
 
-// The pages of 64 blocks k0, k0 + step, ... , a lane each.  Entries past the
-// table or outside the cache are replaced, so a load ahead of the sequence's end
-// stays inside both.
-__device__ __forceinline__ int pages_from(const KvView& v, const int32_t* table, int k0, int step, int lane)
+// The pages of 64 blocks k0, k0 + step, ... , a lane each, in the count of the span.
+// Entries past the table or outside the cache are replaced, so a load ahead of the
+// sequence's end stays inside both.
+__device__ __forceinline__ int pages_from(const KvView& v, const Span& span, const int32_t* table, int k0, int step, int lane)
 {
-    int64_t at = (int64_t)(k0 + lane * step) >> (v.page_shift - 5);
+    int64_t at = (int64_t)span.at(k0 + lane * step) >> (v.page_shift - 5);
     at = at < v.table_stride ? at : v.table_stride - 1;
     return table[at];
 }

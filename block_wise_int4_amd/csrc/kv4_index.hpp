@@ -62,6 +62,41 @@ __host__ __device__ __forceinline__ void key_range(int causal, int window, const
     hi = hi < lo ? lo : hi;
 }
 
+// The keys that rows i0..i1 of a sequence can see, counted without the gap between the
+// first tokens that stay visible (`sinks`) and the window: block c of 32 keys in this count is
+// block at(c) of the sequence.  lo and hi are in the count's keys, end is the last row's end in the
+// sequence's.  Without sinks (negative: none, counted from the sequence's first key) at(c) is c.
+struct Span {
+    int lead, gap;                    // blocks before the gap, blocks left out
+    int lo, hi, end;
+    __host__ __device__ __forceinline__ int at(int c) const { return c + (c >= lead ? gap : 0); }
+};
+__host__ __device__ __forceinline__ Span span_of(int causal, int window, int sinks, const Sequence& s, int i0, int i1)
+{
+    Span r;
+    key_range(causal, window, s, i0, i1, r.lo, r.hi);
+    r.lead = r.gap = 0;
+    r.end = r.hi;
+    if (sinks < 0) return r;
+    const int first = r.lo >> 5, most = (int)(((uint32_t)sinks + 31) >> 5);
+    r.lead = most < first ? most : first;
+    if (r.hi <= r.lo) r.lead = first;          // no row sees a key
+    r.gap = first - r.lead;
+    r.lo = r.lead > 0 && r.hi > r.lo ? 0 : r.lo - 32 * r.gap;
+    r.hi -= 32 * r.gap;
+    return r;
+}
+
+// No row set of this many rows, of heads that share a key head by `gqa`, has keys past this many
+// in its count.
+__host__ __device__ __forceinline__ int64_t longest_span(int window, int sinks, int64_t max_kv, int64_t rows, int gqa)
+{
+    if (sinks < 0 || window == 0) return max_kv;
+    const int64_t tokens = (rows + gqa - 2) / gqa + 1;
+    const int64_t most = ((int64_t)sinks + 31) / 32 * 32 + 31 + window + tokens - 1;
+    return most < max_kv ? most : max_kv;
+}
+
 // A round of a wave's search among `batch` ends of sequences: lane i looks at
 // the end of sequence at(i) - 1 if the range holds it, and keep() takes the number of lanes
 // whose end is not past the token.  Unsigned: 64 steps may pass 2^31.

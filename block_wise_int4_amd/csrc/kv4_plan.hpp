@@ -2,6 +2,7 @@
 // function of the call's shapes alone.
 #pragma once
 
+#include "kv4_index.hpp"
 #include "mnb_kv4.hpp"
 
 namespace mnb {
@@ -24,6 +25,11 @@ inline Plan plan_of(const AttentionArgs& a)
     Plan c = {};
     const int64_t rows = a.max_q * (a.v.q_heads / a.v.kv_heads);
     const bool wide = a.v.head_dim == 256;
+    const int gqa = a.v.q_heads / a.v.kv_heads, window = window_of(a.window, a.max_kv);
+    int64_t span;                              // keys of a row set in the kernels' count
+    auto longest = [&](int64_t set) {
+        return longest_span(window, (int)(a.sinks < a.max_kv ? a.sinks : a.max_kv), a.max_kv, set < rows ? set : rows, gqa);
+    };
     // keys worth a split, in steps of grain; workgroups that fill the chip
     int64_t least = 256, grain = 256, want;
     if (rows <= (wide || a.v.groups > 2 ? 16 : 32)) {   // two column tiles where the registers hold them
@@ -34,9 +40,10 @@ inline Plan plan_of(const AttentionArgs& a)
         // head_dim 64; 42.7 and 42.9 at head_dim 128 with groups of 128, which memory bounds
         c.group = rows <= 4 ? 4 : rows <= 8 ? 2 : rows <= 16 ? 1 : 0;
         c.rows = c.group ? 16 / c.group : 32;
+        span = longest(c.rows);
         // up to 1024 keys one workgroup of 8 waves does without the join (1000 keys: 10.1 us
         // against 11.4, 64 sequences of them 20.4 against 23.4; 2000 keys: 14.0 against 10.7)
-        c.kind = !wide && a.v.groups <= 2 && c.group && a.max_kv <= 1024 ? 0 : 1;
+        c.kind = !wide && a.v.groups <= 2 && c.group && span <= 1024 ? 0 : 1;
         // one sequence: its pieces are alike, and two workgroups a CU in one round
         // are best (131072 keys: 34 us with 512, 44 with 2048); several of unknown
         // lengths: more and shorter pieces even them out (32 sequences of up to 8192 keys:
@@ -50,6 +57,7 @@ inline Plan plan_of(const AttentionArgs& a)
         const int64_t wgs = (rows + 255) / 256 * a.v.kv_heads * a.v.batch;
         c.tiles = wide || a.v.groups > 2 || wgs < 256 ? 1 : 2;
         c.rows = kPromptWaves * 16 * c.tiles;
+        span = longest(c.rows);
         // one workgroup a CU, so splits that make a second round gain nothing (800 new
         // tokens of 8000 keys, 200 workgroups: 196 us whole, 271 in two)
         want = 256;
@@ -60,13 +68,13 @@ inline Plan plan_of(const AttentionArgs& a)
     }
     c.row_tiles = (int)((rows + c.rows - 1) / c.rows);
     const int64_t units = (int64_t)c.row_tiles * a.v.kv_heads * a.v.batch;
-    const int64_t most = (a.max_kv + least - 1) / least;
+    const int64_t most = (span + least - 1) / least;
     int64_t splits = c.kind == 0 ? 1 : c.kind == 1 ? (want + units - 1) / units : want / units;
     splits = splits > most ? most : splits;
     splits = splits > kMaxSplits ? kMaxSplits : splits < 1 ? 1 : splits;
-    c.chunk = (int)(((a.max_kv + splits - 1) / splits + grain - 1) / grain * grain);
+    c.chunk = (int)(((span + splits - 1) / splits + grain - 1) / grain * grain);
     if (c.chunk < grain) c.chunk = (int)grain;
-    c.splits = (int)((a.max_kv + c.chunk - 1) / c.chunk);
+    c.splits = (int)((span + c.chunk - 1) / c.chunk);
     if (c.splits < 1) c.splits = 1;
     return c;
 }

@@ -31,7 +31,9 @@ namespace kv4 {
 
 namespace {
 
-template <int D, int NG, bool F32, int NR, int RW>
+// GAP: the call with first tokens that stay visible.  The call without keeps its own instances: with the
+// gap's scalars in them they spilled three times as many (250 us for the long case, 214 without).
+template <int D, int NG, bool F32, int NR, int RW, bool GAP>
 __global__ __launch_bounds__(RW * 64, 2) void kv4_prompt_kernel(AttnParams p)
 {
     typedef typename std::conditional<F32, float, _Float16>::type T;
@@ -66,19 +68,24 @@ __global__ __launch_bounds__(RW * 64, 2) void kv4_prompt_kernel(AttnParams p)
     const int row0 = tile * kRows;
     if (row0 >= rows) return;                          // the whole workgroup
     const int last_row = row0 + kRows <= rows ? row0 + kRows - 1 : rows - 1;
-    int lo, hi;
-    key_range(p.causal, p.window, s, row0 / p.gqa, last_row / p.gqa, lo, hi);
+    const Span span = span_of(p.causal, p.window, GAP ? p.sinks : -1, s, row0 / p.gqa, last_row / p.gqa);
     const int c0 = split * p.chunk, c1 = c0 + p.chunk;
-    const int from = lo > c0 ? lo : c0, to = hi < c1 ? hi : c1;
-    const bool any = from < to;
+    const int from = span.lo > c0 ? span.lo : c0, till = span.hi < c1 ? span.hi : c1;
+    const bool any = from < till;
     if (p.splits > 1 && !any) return;                  // the join reads only splits with keys
-    const int blk0 = from >> 5, blk1 = any ? (to + 31) >> 5 : blk0;
+    const int blk0 = from >> 5, blk1 = any ? (till + 31) >> 5 : blk0;
+    auto real = [&](int blk) { return GAP ? span.at(blk) : blk; };   // a block of the count in the sequence
+    int to = till;                                     // the split's end among the sequence's keys
+    if constexpr (GAP) {
+        const int last = 32 * real(blk1 - 1) + 32;  // blk1 is not used where it is 0
+        to = span.end < last ? span.end : last;
+    }
     const int stages = (blk1 - blk0 + SB - 1) / SB;
 
     const int nblk = 1 << (v.page_shift - 5);
     const int64_t block_bytes = kv_block_bytes(D, NG);
     const int32_t* table = v.table + (int64_t)b * v.table_stride;
-    int pages = pages_from(v, table, blk0, 1, lane);   // of blocks page0 ..
+    int pages = pages_from(v, span, table, blk0, 1, lane);   // of blocks page0 ..
     int page0 = blk0;
 
     // the rows of this wave
@@ -164,7 +171,7 @@ __global__ __launch_bounds__(RW * 64, 2) void kv4_prompt_kernel(AttnParams p)
             const bool there = blk < blk1;
             int at = blk - page0;
             at = at < 0 ? 0 : at > 63 ? 63 : at;
-            unsigned char* base = v.cache + (((int64_t)page_in(v, pages, at) * v.kv_heads + h) * nblk + (blk & (nblk - 1))) * block_bytes;
+            unsigned char* base = v.cache + (((int64_t)page_in(v, pages, at) * v.kv_heads + h) * nblk + (real(blk) & (nblk - 1))) * block_bytes;
             rs[it] = __builtin_amdgcn_make_buffer_rsrc(base, 0, there ? 32 * D + 256 * NG : 0, 0x00020000);
             code[it] = __builtin_amdgcn_raw_buffer_load_b128(rs[it], lane * 16, (is_v ? 16 * D : 0) + qi * 1024, 0);
             if constexpr (!LATE) words_of(it, is_v, qi);
@@ -257,7 +264,7 @@ __global__ __launch_bounds__(RW * 64, 2) void kv4_prompt_kernel(AttnParams p)
         }
     };
 
-    // KB blocks from b0 of a stage; the first is block blk of the sequence.
+    // KB blocks from b0 of a stage; the first is block blk of the count.
     constexpr int KB = SB < 2 || NG >= 4 || (F32 && NG > 1) ? 1 : 2;   // two where the registers hold them (249 us with one, 233 with two)
     auto compute = [&](int buf, int b0, int blk) {
         // ---- logits less M, 32 KB keys by 16 NR rows ----
@@ -295,17 +302,23 @@ __global__ __launch_bounds__(RW * 64, 2) void kv4_prompt_kernel(AttnParams p)
             }
         }
         // ---- masks: a hidden key's logit is -infinity ----
-        const bool edge = (blk + KB) * 32 > whole || blk * 32 < open;
+        const int first = real(blk) * 32, second = real(blk + KB - 1) * 32;   // their keys
+        const bool edge = second + 32 > whole || first < open;
         uint32_t seen[NR];                     // bit 4 t + i: the row sees the key
         if (edge) {
 #pragma unroll
             for (int n = 0; n < NR; ++n) {
                 const int below = p.causal && p.window > 0 ? pos[n] - p.window : -1;
+                // keys from the first tokens' end to the window are hidden too
+                const uint32_t hidden = below >= p.sinks ? below - p.sinks + 1 : 0;
+                const int most = pos[n] < to ? pos[n] : to - 1;
                 seen[n] = 0;
 #pragma unroll
                 for (int k = 0; k < 8 * KB; ++k) {
-                    const int key = blk * 32 + (k >> 2) * 16 + 4 * quarter + (k & 3);
-                    const bool ok = key <= pos[n] && key > below && key < to;
+                    const int at = (k < 8 ? first : second) + 4 * quarter, off = (k >> 2 & 1) * 16 + (k & 3);
+                    const int key = at + off;
+                    const bool ok = GAP ? off <= most - at && (uint32_t)(at - p.sinks) + off >= hidden
+                                        : key <= pos[n] && key > below && key < to;
                     seen[n] |= ok ? 1u << k : 0u;
                     y[n][k] = ok ? y[n][k] : -__builtin_inff();
                 }
@@ -414,7 +427,7 @@ __global__ __launch_bounds__(RW * 64, 2) void kv4_prompt_kernel(AttnParams p)
         // pages of the blocks to request: refilled before they leave the register
         if (blk0 + (st + 1) * SB > page0 + 64) {
             page0 = blk0 + st * SB;
-            pages = pages_from(v, table, page0, 1, lane);
+            pages = pages_from(v, span, table, page0, 1, lane);
         }
         request(st);
     };
@@ -440,7 +453,7 @@ __global__ __launch_bounds__(RW * 64, 2) void kv4_prompt_kernel(AttnParams p)
             for (int b0 = 0; b0 < SB; b0 += KB) {
                 const int blk = blk0 + st * SB + b0;
                 // blocks past the end hold zeros and are masked
-                if (busy && blk < blk1 && blk * 32 < none) compute(buf, b0, blk);
+                if (busy && blk < blk1 && real(blk) * 32 < none) compute(buf, b0, blk);
             }
             if (!first_half && more) unpack((st + EP) & (NB - 1));
             if (!first_half && further) ask(st + EP + 1);
@@ -472,22 +485,24 @@ __global__ __launch_bounds__(RW * 64, 2) void kv4_prompt_kernel(AttnParams p)
     }
 }
 
-template <int D, int NG, bool F32> hipError_t launch_tiles(const AttnParams& p, const Plan& c, hipStream_t s)
+template <int D, int NG, bool F32, bool GAP> hipError_t launch_tiles(const AttnParams& p, const Plan& c, hipStream_t s)
 {
     const dim3 grid((unsigned)(p.v.kv_heads * c.splits * c.row_tiles), (unsigned)p.v.batch);
     if constexpr (D < 256 && NG <= 2) {
         if (c.tiles == 2) {
-            kv4_prompt_kernel<D, NG, F32, 2, kPromptWaves><<<grid, dim3(kPromptWaves * 64), 0, s>>>(p);
+            kv4_prompt_kernel<D, NG, F32, 2, kPromptWaves, GAP><<<grid, dim3(kPromptWaves * 64), 0, s>>>(p);
             return hipGetLastError();
         }
     }
-    kv4_prompt_kernel<D, NG, F32, 1, kPromptWaves><<<grid, dim3(kPromptWaves * 64), 0, s>>>(p);
+    kv4_prompt_kernel<D, NG, F32, 1, kPromptWaves, GAP><<<grid, dim3(kPromptWaves * 64), 0, s>>>(p);
     return hipGetLastError();
 }
 
 template <int D, int NG> hipError_t launch_type(const AttnParams& p, const Plan& c, int f16, hipStream_t s)
 {
-    return f16 ? launch_tiles<D, NG, false>(p, c, s) : launch_tiles<D, NG, true>(p, c, s);
+    if (p.sinks >= 0 && p.window > 0)
+        return f16 ? launch_tiles<D, NG, false, true>(p, c, s) : launch_tiles<D, NG, true, true>(p, c, s);
+    return f16 ? launch_tiles<D, NG, false, false>(p, c, s) : launch_tiles<D, NG, true, false>(p, c, s);
 }
 
 }  // namespace

@@ -144,6 +144,52 @@ mnb::AttentionArgs plan_args(const mnb_kv4_desc* c, int64_t batch, int64_t token
     return a;
 }
 
+mnb_status check_sinks(int64_t window, int64_t sinks)
+{
+    if (window < 0) return fail(MNB_ERR_INVALID_ARGUMENT, "window must be >= 0 (got %lld)", (long long)window);
+    if (sinks < 0) return fail(MNB_ERR_INVALID_ARGUMENT, "sinks must be >= 0 (got %lld)", (long long)sinks);
+    return MNB_OK;
+}
+
+// sinks: -1 for the call without.
+mnb_status attention(const mnb_kv4_desc* c, const void* cache, const int32_t* block_table, int64_t table_stride,
+                     const int32_t* kv_len, const int32_t* q_start, int64_t batch, int64_t tokens, int64_t max_q,
+                     int64_t max_kv, int32_t dtype, const void* q, int64_t q_stride, float scale, int32_t causal,
+                     int64_t window, int64_t sinks, void* out, float* lse, void* workspace, size_t workspace_bytes,
+                     void* stream)
+{
+    if (!std::isfinite(scale * mnb::kLog2E))
+        return fail(MNB_ERR_INVALID_ARGUMENT, "scale must be finite, and times log2(e) too");
+    MNB_TRY(check_stride(q_stride, (int64_t)c->q_heads * c->head_dim, tokens, "q_stride"));
+    if (tokens == 0 || batch == 0 || max_q == 0) return ok("noop");
+    MNB_TRY(check_sequences(block_table, table_stride, kv_len, q_start, batch, tokens));
+    const uintptr_t elem = dtype == MNB_F16 ? 2 : 4;
+    MNB_TRY(check_ptr(q, elem, "q"));
+    MNB_TRY(check_ptr(out, elem, "out"));
+    if (lse) MNB_TRY(check_ptr(lse, 4, "lse"));
+    MNB_TRY(check_ptr(cache, 256, "cache"));
+    mnb::AttentionArgs a = plan_args(c, batch, tokens, max_q, max_kv);
+    a.window = window;
+    a.sinks = sinks;
+    const size_t need = mnb::kv4_attention_workspace(a);
+    if (workspace_bytes < need)
+        return fail(MNB_ERR_INVALID_ARGUMENT, "workspace too small: %zu bytes given, %zu needed", workspace_bytes, need);
+    if (need > 0) MNB_TRY(check_ptr(workspace, 256, "workspace"));
+    MNB_TRY(check_device());
+    a.v = view_of(c, cache, block_table, table_stride, kv_len, q_start, batch, tokens);
+    a.q = q;
+    a.q_stride = q_stride;
+    a.out = out;
+    a.lse = lse;
+    a.scale = scale;
+    a.causal = causal;
+    a.workspace = workspace;
+    a.f16 = dtype == MNB_F16;
+    const char* variant = "";
+    const hipError_t e = mnb::launch_kv4_attention(a, static_cast<hipStream_t>(stream), &variant);
+    return launched(e, variant);
+}
+
 }  // namespace
 
 extern "C" {
@@ -304,35 +350,34 @@ mnb_status mnb_attention_kv4(const mnb_kv4_desc* c, const void* cache, const int
     if (causal != 0 && causal != 1) return fail(MNB_ERR_INVALID_ARGUMENT, "causal must be 0 or 1 (got %d)", causal);
     if (window < 0) return fail(MNB_ERR_INVALID_ARGUMENT, "window must be >= 0 (got %lld)", (long long)window);
     if (window > 0 && !causal) return fail(MNB_ERR_INVALID_ARGUMENT, "a window needs causal = 1");
-    if (!std::isfinite(scale * mnb::kLog2E))
-        return fail(MNB_ERR_INVALID_ARGUMENT, "scale must be finite, and times log2(e) too");
-    MNB_TRY(check_stride(q_stride, (int64_t)c->q_heads * c->head_dim, tokens, "q_stride"));
-    if (tokens == 0 || batch == 0 || max_q == 0) return ok("noop");
-    MNB_TRY(check_sequences(block_table, table_stride, kv_len, q_start, batch, tokens));
-    const uintptr_t elem = dtype == MNB_F16 ? 2 : 4;
-    MNB_TRY(check_ptr(q, elem, "q"));
-    MNB_TRY(check_ptr(out, elem, "out"));
-    if (lse) MNB_TRY(check_ptr(lse, 4, "lse"));
-    MNB_TRY(check_ptr(cache, 256, "cache"));
+    return attention(c, cache, block_table, table_stride, kv_len, q_start, batch, tokens, max_q, max_kv, dtype, q,
+                     q_stride, scale, causal, window, -1, out, lse, workspace, workspace_bytes, stream);
+}
+
+size_t mnb_attention_kv4_sinks_workspace_bytes(const mnb_kv4_desc* c, int64_t batch, int64_t tokens, int64_t max_q,
+                                               int64_t max_kv, int64_t window, int64_t sinks)
+{
+    if (check_bounds(c, batch, tokens, max_q, max_kv) != MNB_OK) return 0;
+    if (check_sinks(window, sinks) != MNB_OK) return 0;
+    ok(nullptr);
+    if (batch == 0 || tokens == 0 || max_q == 0) return 0;
     mnb::AttentionArgs a = plan_args(c, batch, tokens, max_q, max_kv);
-    const size_t need = mnb::kv4_attention_workspace(a);
-    if (workspace_bytes < need)
-        return fail(MNB_ERR_INVALID_ARGUMENT, "workspace too small: %zu bytes given, %zu needed", workspace_bytes, need);
-    if (need > 0) MNB_TRY(check_ptr(workspace, 256, "workspace"));
-    MNB_TRY(check_device());
-    a.v = view_of(c, cache, block_table, table_stride, kv_len, q_start, batch, tokens);
-    a.q = q;
-    a.q_stride = q_stride;
-    a.out = out;
-    a.lse = lse;
-    a.scale = scale;
-    a.causal = causal;
     a.window = window;
-    a.workspace = workspace;
-    a.f16 = dtype == MNB_F16;
-    const char* variant = "";
-    const hipError_t e = mnb::launch_kv4_attention(a, static_cast<hipStream_t>(stream), &variant);
-    return launched(e, variant);
+    a.sinks = sinks;
+    return mnb::kv4_attention_workspace(a);
+}
+
+mnb_status mnb_attention_kv4_sinks(const mnb_kv4_desc* c, const void* cache, const int32_t* block_table,
+                                   int64_t table_stride, const int32_t* kv_len, const int32_t* q_start, int64_t batch,
+                                   int64_t tokens, int64_t max_q, int64_t max_kv, int32_t dtype, const void* q,
+                                   int64_t q_stride, float scale, int64_t window, int64_t sinks, void* out, float* lse,
+                                   void* workspace, size_t workspace_bytes, void* stream)
+{
+    MNB_TRY(check_bounds(c, batch, tokens, max_q, max_kv));
+    MNB_TRY(check_dtype(dtype));
+    MNB_TRY(check_sinks(window, sinks));
+    return attention(c, cache, block_table, table_stride, kv_len, q_start, batch, tokens, max_q, max_kv, dtype, q,
+                     q_stride, scale, 1, window, sinks, out, lse, workspace, workspace_bytes, stream);
 }
 
 }  // extern "C"

@@ -82,6 +82,7 @@ struct AttentionArgs {
     float scale;
     int causal;
     int64_t window;           // 0: none
+    int64_t sinks = -1;       // first keys that stay visible; -1: none, splits cut from the whole length
     int64_t max_q, max_kv;
     void* workspace;
     int f16;

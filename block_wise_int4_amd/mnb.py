@@ -45,7 +45,7 @@ EXPORTS = ("mnb_repacked_bytes", "mnb_repacked_layout", "mnb_repack", "mnb_gemv"
            "mnb_gemm_act_order", "mnb_gemm_group_indices", "mnb_gemm_accuracy4_workspace_bytes", "mnb_gemm_accuracy4",
            "mnb_gemm_accuracy4_noalloc", "mnb_gemm_accuracy4_codes", "mnb_rms_norm",
            "mnb_kv4_cache_bytes", "mnb_kv4_append", "mnb_kv4_read", "mnb_attention_kv4_workspace_bytes",
-           "mnb_attention_kv4",
+           "mnb_attention_kv4", "mnb_attention_kv4_sinks_workspace_bytes", "mnb_attention_kv4_sinks",
            "mnb_unpack_debug", "mnb_debug_prefill_rows", "mnb_status_string", "mnb_last_error", "mnb_last_variant")
 
 
@@ -127,6 +127,9 @@ def _load():
         "mnb_attention_kv4_workspace_bytes": (sz, [KV, i64, i64, i64, i64]),
         "mnb_attention_kv4": (ctypes.c_int, [KV, P, P, i64, P, P, i64, i64, i64, i64, i32, P, i64, f32, i32, i64, P,
                                              P, P, sz, P]),
+        "mnb_attention_kv4_sinks_workspace_bytes": (sz, [KV, i64, i64, i64, i64, i64, i64]),
+        "mnb_attention_kv4_sinks": (ctypes.c_int, [KV, P, P, i64, P, P, i64, i64, i64, i64, i32, P, i64, f32, i64, i64,
+                                                   P, P, P, sz, P]),
         "mnb_unpack_debug": (ctypes.c_int, [D, P, P, P, P]),
         "mnb_debug_prefill_rows": (ctypes.c_int32, [ctypes.c_int32]),
         "mnb_status_string": (ctypes.c_char_p, [ctypes.c_int]),
@@ -467,11 +470,8 @@ def mnb_attention_kv4_workspace_bytes(c: mnb_kv4_desc, batch: int, tokens: int, 
     return int(lib.mnb_attention_kv4_workspace_bytes(ctypes.byref(c), batch, tokens, max_q, max_kv))
 
 
-def mnb_attention_kv4(c: mnb_kv4_desc, cache, q, block_table, kv_len, q_start, max_q: int, max_kv: int, out,
-                      scale: float, causal: bool = True, window: int = 0, lse=None, workspace: Ptr = None,
-                      workspace_bytes: Optional[int] = None, stream=None) -> None:
-    """q [tokens, q_heads, head_dim] (tokens may be strided), out the same, lse fp32 [tokens, q_heads]."""
-    d, cp, tp, ts, lp, sp, batch = _sequences(c, cache, block_table, kv_len, q_start)
+def _attention_rows(c, q, out, lse, workspace, workspace_bytes):
+    """Address and stride of q and the workspace's size, after a look at the row arrays of an attention."""
     dtype, n, H, D = q.dtype, q.shape[0], c.q_heads, c.head_dim
     shape = (n, H, D)
     if q.shape != shape or out.dtype is not dtype or out.shape != shape:
@@ -481,10 +481,36 @@ def mnb_attention_kv4(c: mnb_kv4_desc, cache, q, block_table, kv_len, q_start, m
     if workspace_bytes is None:
         workspace_bytes = 0 if workspace is None or type(workspace) is int else \
             workspace.numel() * workspace.element_size()
-    qp, qs = _rows3(q, H, D, "q")
-    st = lib.mnb_attention_kv4(d, cp, tp, ts, lp, sp, batch, n, max_q, max_kv, _dtype_code(q), qp, qs, scale,
+    return (*_rows3(q, H, D, "q"), workspace_bytes)
+
+
+def mnb_attention_kv4(c: mnb_kv4_desc, cache, q, block_table, kv_len, q_start, max_q: int, max_kv: int, out,
+                      scale: float, causal: bool = True, window: int = 0, lse=None, workspace: Ptr = None,
+                      workspace_bytes: Optional[int] = None, stream=None) -> None:
+    """q [tokens, q_heads, head_dim] (tokens may be strided), out the same, lse fp32 [tokens, q_heads]."""
+    d, cp, tp, ts, lp, sp, batch = _sequences(c, cache, block_table, kv_len, q_start)
+    qp, qs, workspace_bytes = _attention_rows(c, q, out, lse, workspace, workspace_bytes)
+    st = lib.mnb_attention_kv4(d, cp, tp, ts, lp, sp, batch, q.shape[0], max_q, max_kv, _dtype_code(q), qp, qs, scale,
                                1 if causal else 0, window, _addr(out, "out"), _addr(lse, "lse"),
                                _addr(workspace, "workspace"), workspace_bytes, _stream(stream))
+    if st:
+        _check(st)
+
+
+def mnb_attention_kv4_sinks_workspace_bytes(c: mnb_kv4_desc, batch: int, tokens: int, max_q: int, max_kv: int,
+                                            window: int, sinks: int) -> int:
+    return int(lib.mnb_attention_kv4_sinks_workspace_bytes(ctypes.byref(c), batch, tokens, max_q, max_kv, window, sinks))
+
+
+def mnb_attention_kv4_sinks(c: mnb_kv4_desc, cache, q, block_table, kv_len, q_start, max_q: int, max_kv: int, out,
+                            scale: float, window: int, sinks: int, lse=None, workspace: Ptr = None,
+                            workspace_bytes: Optional[int] = None, stream=None) -> None:
+    """As mnb_attention_kv4, causal, through a window beside which the first `sinks` tokens stay visible."""
+    d, cp, tp, ts, lp, sp, batch = _sequences(c, cache, block_table, kv_len, q_start)
+    qp, qs, workspace_bytes = _attention_rows(c, q, out, lse, workspace, workspace_bytes)
+    st = lib.mnb_attention_kv4_sinks(d, cp, tp, ts, lp, sp, batch, q.shape[0], max_q, max_kv, _dtype_code(q), qp, qs,
+                                     scale, window, sinks, _addr(out, "out"), _addr(lse, "lse"),
+                                     _addr(workspace, "workspace"), workspace_bytes, _stream(stream))
     if st:
         _check(st)
 

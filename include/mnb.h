@@ -499,6 +499,22 @@ mnb_status mnb_attention_kv4(const mnb_kv4_desc* c, const void* cache, const int
                              int64_t q_stride, float scale, int32_t causal, int64_t window, void* out, float* lse,
                              void* workspace, size_t workspace_bytes, void* stream);
 
+/* The causal attention through a sliding window with a few first tokens that stay
+ * visible: a row at position i sees the keys j <= i with j > i - window or j <
+ * sinks (window 0: every j <= i).  All else as mnb_attention_kv4 with causal = 1;
+ * sinks 0 is its window.  The work is cut from the keys that are seen, whatever the
+ * length, so this call also serves a window over a long cache.  Pages whose tokens
+ * no row sees are not needed: their table entries may hold anything (-1, or a
+ * page given to another sequence).  The workspace depends on window and sinks;
+ * window >= 0, sinks >= 0. */
+size_t mnb_attention_kv4_sinks_workspace_bytes(const mnb_kv4_desc* c, int64_t batch, int64_t tokens, int64_t max_q,
+                                               int64_t max_kv, int64_t window, int64_t sinks);
+mnb_status mnb_attention_kv4_sinks(const mnb_kv4_desc* c, const void* cache, const int32_t* block_table,
+                                   int64_t table_stride, const int32_t* kv_len, const int32_t* q_start, int64_t batch,
+                                   int64_t tokens, int64_t max_q, int64_t max_kv, int32_t dtype, const void* q,
+                                   int64_t q_stride, float scale, int64_t window, int64_t sinks, void* out, float* lse,
+                                   void* workspace, size_t workspace_bytes, void* stream);
+
 /* Test-only: decode a repacked buffer with the production unpack code.
  * codes: device u8 [N,K] (the stored nibbles); w_f32: device f32 [N,K], the
  * dequantized weights (code - zp) * scale rounded once to fp32.  Either

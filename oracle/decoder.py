@@ -191,8 +191,9 @@ def attention_row(q, K, V, seen, scale):
         return p @ V[seen], m + np.log(total), p @ np.abs(V[seen]), reach
 
 
-def attention(geo, cache, table, kv_len, q_start, q, scale, causal=True, window=0, max_kv=None):
-    """out [T, H, D], lse [T, H], absolute bounds sum p|V| [T, H, D] and logit reach [T, H]."""
+def attention(geo, cache, table, kv_len, q_start, q, scale, causal=True, window=0, max_kv=None, sinks=0):
+    """out [T, H, D], lse [T, H], absolute bounds sum p|V| [T, H, D] and logit reach [T, H]; with a window the keys
+    below `sinks` stay visible."""
     T, H, D = q.shape
     out, lse = np.zeros((T, H, D)), np.full((T, H), -np.inf)
     size, reach = np.zeros((T, H, D)), np.zeros((T, H))
@@ -209,7 +210,7 @@ def attention(geo, cache, table, kv_len, q_start, q, scale, causal=True, window=
                 if causal:
                     seen = j <= p
                     if window > 0:
-                        seen &= j > p - window
+                        seen &= (j > p - window) | (j < sinks)
                 for g in range(h * per, (h + 1) * per):
                     out[t, g], lse[t, g], size[t, g], reach[t, g] = attention_row(
                         q[t, g].astype(np.float64), K, V, seen, scale)
