@@ -17,7 +17,8 @@ LIB = os.path.join(LIB_DIR, "libmnb.so")
 
 SOURCES = ["mnb_api.cpp", "repack.hip", "act_order.hip", "gemv.hip", "gemm_small.hip", "gemm_mfma.hip",
            "noalloc.hip", "f32_split.hip", "gidx.hip",
-           "acc4.hip", "rms_norm.hip", "kv4_append.hip", "kv4_attention.hip", "kv4_prompt.hip", "mnb_decoder_api.cpp"]
+           "acc4.hip", "rms_norm.hip", "kv4_append.hip", "kv4_attention.hip", "kv4_prompt.hip", "mnb_decoder_api.cpp",
+           "adapters.hip", "verify.hip", "mnb_requests_api.cpp"]
 
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
 ARCH = "gfx950"

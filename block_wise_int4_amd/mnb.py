@@ -46,6 +46,7 @@ EXPORTS = ("mnb_repacked_bytes", "mnb_repacked_layout", "mnb_repack", "mnb_gemv"
            "mnb_gemm_accuracy4_noalloc", "mnb_gemm_accuracy4_codes", "mnb_rms_norm",
            "mnb_kv4_cache_bytes", "mnb_kv4_append", "mnb_kv4_read", "mnb_attention_kv4_workspace_bytes",
            "mnb_attention_kv4", "mnb_attention_kv4_sinks_workspace_bytes", "mnb_attention_kv4_sinks",
+           "mnb_adapters_workspace_bytes", "mnb_adapters_add", "mnb_verify_workspace_bytes", "mnb_verify_drafts",
            "mnb_unpack_debug", "mnb_debug_prefill_rows", "mnb_status_string", "mnb_last_error", "mnb_last_variant")
 
 
@@ -65,6 +66,11 @@ class mnb_kv4_desc(ctypes.Structure):
     _fields_ = [("q_heads", ctypes.c_int32), ("kv_heads", ctypes.c_int32), ("head_dim", ctypes.c_int32),
                 ("group_size", ctypes.c_int32), ("page_size", ctypes.c_int32), ("reserved", ctypes.c_int32),
                 ("num_pages", ctypes.c_int64)]
+
+
+class mnb_adapter_desc(ctypes.Structure):
+    _fields_ = [("n", ctypes.c_int64), ("k", ctypes.c_int64), ("rank", ctypes.c_int32), ("count", ctypes.c_int32),
+                ("dtype", ctypes.c_int32), ("reserved", ctypes.c_int32)]
 
 
 class mnb_layout(ctypes.Structure):
@@ -99,6 +105,7 @@ def _load():
     P = ctypes.c_void_p
     D = ctypes.POINTER(mnb_weight_desc)
     KV = ctypes.POINTER(mnb_kv4_desc)
+    AD = ctypes.POINTER(mnb_adapter_desc)
     i32, i64, sz, f32 = ctypes.c_int32, ctypes.c_int64, ctypes.c_size_t, ctypes.c_float
     sig = {
         "mnb_repacked_bytes": (sz, [D]),
@@ -130,6 +137,10 @@ def _load():
         "mnb_attention_kv4_sinks_workspace_bytes": (sz, [KV, i64, i64, i64, i64, i64, i64]),
         "mnb_attention_kv4_sinks": (ctypes.c_int, [KV, P, P, i64, P, P, i64, i64, i64, i64, i32, P, i64, f32, i64, i64,
                                                    P, P, P, sz, P]),
+        "mnb_adapters_workspace_bytes": (sz, [AD, i64]),
+        "mnb_adapters_add": (ctypes.c_int, [AD, P, P, P, P, P, i64, P, i64, P, i64, P, i64, P, sz, P]),
+        "mnb_verify_workspace_bytes": (sz, [i64, i64]),
+        "mnb_verify_drafts": (ctypes.c_int, [P, i64, P, i64, P, P, i64, i64, i64, i32, P, P, P, P, P, sz, P]),
         "mnb_unpack_debug": (ctypes.c_int, [D, P, P, P, P]),
         "mnb_debug_prefill_rows": (ctypes.c_int32, [ctypes.c_int32]),
         "mnb_status_string": (ctypes.c_char_p, [ctypes.c_int]),
@@ -511,6 +522,88 @@ def mnb_attention_kv4_sinks(c: mnb_kv4_desc, cache, q, block_table, kv_len, q_st
     st = lib.mnb_attention_kv4_sinks(d, cp, tp, ts, lp, sp, batch, q.shape[0], max_q, max_kv, _dtype_code(q), qp, qs,
                                      scale, window, sinks, _addr(out, "out"), _addr(lse, "lse"),
                                      _addr(workspace, "workspace"), workspace_bytes, _stream(stream))
+    if st:
+        _check(st)
+
+
+# ---- many requests at once --------------------------------------------------
+
+def adapter_desc(n: int, k: int, rank: int, count: int, dtype) -> mnb_adapter_desc:
+    """dtype: torch.float16 or torch.float32, or its code."""
+    code = dtype if type(dtype) is int else MNB_F16 if dtype is torch.float16 else MNB_F32 if dtype is torch.float32 else -1
+    return mnb_adapter_desc(n, k, rank, count, code, 0)
+
+
+def mnb_adapters_workspace_bytes(d: mnb_adapter_desc, m: int) -> int:
+    return int(lib.mnb_adapters_workspace_bytes(ctypes.byref(d), m))
+
+
+def _size_of(workspace, workspace_bytes):
+    if workspace_bytes is None:
+        return 0 if workspace is None or type(workspace) is int else workspace.numel() * workspace.element_size()
+    return workspace_bytes
+
+
+def mnb_adapters_add(d: mnb_adapter_desc, a, b, scales, adapter, x, y, base=None, ranks=None, workspace: Ptr = None,
+                     workspace_bytes: Optional[int] = None, stream=None) -> None:
+    """a [count, rank, k], b [count, n, rank]; scales fp32 and ranks int32 [count] may be None; adapter int32 [m]; x [m, k],
+    base and y [m, n], rows may be strided; y may be base."""
+    shape, dtype = x.shape, x.dtype
+    m = shape[0]
+    n, k, r, count = d.n, d.k, d.rank, d.count
+    out = (m, n)
+    if shape != (m, k) or y.dtype is not dtype or y.shape != out or a.dtype is not dtype or b.dtype is not dtype or \
+            a.shape != (count, r, k) or b.shape != (count, n, r) or adapter.dtype is not torch.int32 or adapter.shape != (m,):
+        _refuse(((x, "x", dtype, (m, k)), (y, "y", dtype, out), (a, "a", dtype, (count, r, k)),
+                 (b, "b", dtype, (count, n, r)), (adapter, "adapter", torch.int32, (m,))))
+    if d.dtype != _dtype_code(x):
+        raise ValueError("x: the descriptor's dtype expected, got %s" % dtype)
+    if scales is not None and (scales.dtype is not torch.float32 or scales.shape != (count,)):
+        _refuse(((scales, "scales", torch.float32, (count,)),))
+    if ranks is not None and (ranks.dtype is not torch.int32 or ranks.shape != (count,)):
+        _refuse(((ranks, "ranks", torch.int32, (count,)),))
+    bp, bs = None, 0
+    if base is not None:
+        if base.dtype is not dtype or base.shape != out:
+            _refuse(((base, "base", dtype, out),))
+        bp, bs = _rows2(base, "base")
+    xp, xs = _rows2(x, "x")
+    yp, ys = _rows2(y, "y")
+    st = lib.mnb_adapters_add(d, _addr(a, "a"), _addr(b, "b"), _addr(scales, "scales"), _addr(ranks, "ranks"),
+                              _addr(adapter, "adapter"), m, xp, xs, bp, bs, yp, ys, _addr(workspace, "workspace"),
+                              _size_of(workspace, workspace_bytes), _stream(stream))
+    if st:
+        _check(st)
+
+
+def mnb_verify_workspace_bytes(batch: int, vocab: int) -> int:
+    return int(lib.mnb_verify_workspace_bytes(batch, vocab))
+
+
+def mnb_verify_drafts(target, ids, accept, pick, out, accepted, q_start=None, draft=None, workspace: Ptr = None,
+                      workspace_bytes: Optional[int] = None, stream=None) -> None:
+    """target and draft [tokens, vocab] (rows may be strided; draft None: certain drafts), ids and out int32 and accept fp32
+    [tokens], pick fp32 and accepted int32 [batch], q_start int32 [batch + 1] or None."""
+    i32, f32, dtype = torch.int32, torch.float32, target.dtype
+    tokens, vocab = target.shape
+    batch, rows = pick.shape[0], (tokens,)
+    if ids.dtype is not i32 or ids.shape != rows or out.dtype is not i32 or out.shape != rows or accept.dtype is not f32 or \
+            accept.shape != rows or pick.dtype is not f32 or accepted.dtype is not i32 or accepted.shape != (batch,) or \
+            pick.dim() != 1:
+        _refuse(((ids, "ids", i32, rows), (accept, "accept", f32, rows), (out, "out", i32, rows),
+                 (pick, "pick", f32, (batch,)), (accepted, "accepted", i32, (batch,))))
+    if q_start is not None and (q_start.dtype is not i32 or q_start.shape != (batch + 1,)):
+        _refuse(((q_start, "q_start", i32, (batch + 1,)),))
+    tp, ts = _rows2(target, "target")
+    dp, ds = None, 0
+    if draft is not None:
+        if draft.dtype is not dtype or draft.shape != target.shape:
+            _refuse(((draft, "draft", dtype, target.shape),))
+        dp, ds = _rows2(draft, "draft")
+    st = lib.mnb_verify_drafts(tp, ts, dp, ds, _addr(ids, "ids"), _addr(q_start, "q_start"), batch, tokens, vocab,
+                               _dtype_code(target), _addr(accept, "accept"), _addr(pick, "pick"), _addr(out, "out"),
+                               _addr(accepted, "accepted"), _addr(workspace, "workspace"),
+                               _size_of(workspace, workspace_bytes), _stream(stream))
     if st:
         _check(st)
 

@@ -515,6 +515,70 @@ mnb_status mnb_attention_kv4_sinks(const mnb_kv4_desc* c, const void* cache, con
                                    int64_t q_stride, float scale, int64_t window, int64_t sinks, void* out, float* lse,
                                    void* workspace, size_t workspace_bytes, void* stream);
 
+/* ---------------------------------------------------------------------------
+ * Many requests at once: each request's own low-rank adapter beside a projection
+ * that all share, and the verification of drafted tokens.  Conventions as above.
+ */
+
+/* Low-rank adapters of many requests:
+ *   y[t] = base[t] + scales[a] * B_a (A_a x[t]),   a = adapter[t],
+ * beside a projection's output base (of mnb_gemm, say; NULL: zeros).  A row whose
+ * adapter is negative or >= count gets base[t].  The descriptor is of the whole set:
+ * a [count, rank, k] and b [count, n, rank] of dtype, 16-byte aligned, hold an adapter in
+ * each slot; ranks (NULL: all of rank) its rank r, the first r rows of a and
+ * columns of b: the others are not read, r <= 0 is no adapter, r > rank is rank.
+ * scales NULL: 1.  adapter int32 [m]: rows of one adapter need not be neighbours,
+ * but a call whose rows are grouped reads less.
+ * x [m, k], base and y [m, n] of dtype, rows *_stride elements apart (a projection's
+ * slice of a fused one, say).  y may be base itself, with the same stride; it
+ * must not overlap x, or base in another way.  h = A x and the sums are kept in fp32;
+ * in fp16 calls h enters the second product as two fp16 parts, 22 bits (to 2^-39 of its
+ * row's largest where that is more), and y is rounded once.
+ * workspace (256-byte aligned): mnb_adapters_workspace_bytes of the same m; contents
+ * need no initialisation.  rank at most 128, n and k at most 2^24, m < 2^24, m * n <
+ * 2^38, else MNB_ERR_UNSUPPORTED.  m == 0 is a no-op.  Deterministic. */
+typedef struct {
+    int64_t n, k;
+    int32_t rank, count;
+    int32_t dtype;    /* MNB_F16 or MNB_F32, of x, a, b, base and y */
+    int32_t reserved; /* must be 0 */
+} mnb_adapter_desc;
+size_t mnb_adapters_workspace_bytes(const mnb_adapter_desc* d, int64_t m);
+mnb_status mnb_adapters_add(const mnb_adapter_desc* d, const void* a, const void* b, const float* scales,
+                            const int32_t* ranks, const int32_t* adapter, int64_t m, const void* x, int64_t x_stride,
+                            const void* base, int64_t base_stride, void* y, int64_t y_stride, void* workspace,
+                            size_t workspace_bytes, void* stream);
+
+/* Verification of drafted tokens against the target's probabilities, from given
+ * random numbers.  A sequence's rows q_start[b] .. q_start[b+1]-1 (NULL: one each)
+ * are those of its step: ids of its first row is the last sure token, ids of row i its
+ * i-th draft, and target [tokens, vocab] (of dtype) row i - 1 is the distribution p
+ * that judges draft i; so a sequence of c rows has c - 1 drafts.  draft (the same
+ * layout; NULL: the drafts are certain) row i - 1 is the distribution q that draft i
+ * was drawn from; a sequence's last row of it is not read.
+ *   Draft i, of token d, is accepted if accept[row i - 1] * q(d) < p(d) (q(d) = 1 where
+ *   certain) and all before it were; a d outside 0..vocab-1 is refused.
+ *   After n accepted drafts one token is drawn from the weights
+ *     w = max(p - q, 0) of the row that judged the refused draft (p without the refused
+ *         token where the drafts are certain), p itself if all of these are 0,
+ *     w = p of the last row if all drafts were accepted:
+ *   the lowest i with w[0] + .. + w[i] > pick[b] * (w[0] + .. + w[vocab-1]).
+ * out [tokens]: in the sequence's rows its accepted drafts, the drawn token, then -1;
+ * accepted [batch]: n (0 for a sequence without rows).  Rows of no sequence are left.
+ * A probability that is NaN, infinite or negative counts as 0; a row with no positive
+ * one draws -1.  accept [tokens] and pick [batch] are fp32 in [0, 1); a pick that is NaN or
+ * below 0 is 0, one of 1 or more draws the last token with a weight.  Rows need not be
+ * normalised.  Products and sums are kept in 64 bits.
+ * target_stride, draft_stride >= vocab.  out must not overlap ids.  workspace (256-byte
+ * aligned): mnb_verify_workspace_bytes; contents need no initialisation.  vocab at most
+ * 2^30, batch * ceil(vocab / 4096) < 2^24, else MNB_ERR_UNSUPPORTED.  batch == 0 is a
+ * no-op.  Deterministic. */
+size_t mnb_verify_workspace_bytes(int64_t batch, int64_t vocab);
+mnb_status mnb_verify_drafts(const void* target, int64_t target_stride, const void* draft, int64_t draft_stride,
+                             const int32_t* ids, const int32_t* q_start, int64_t batch, int64_t tokens, int64_t vocab,
+                             int32_t dtype, const float* accept, const float* pick, int32_t* out, int32_t* accepted,
+                             void* workspace, size_t workspace_bytes, void* stream);
+
 /* Test-only: decode a repacked buffer with the production unpack code.
  * codes: device u8 [N,K] (the stored nibbles); w_f32: device f32 [N,K], the
  * dequantized weights (code - zp) * scale rounded once to fp32.  Either
