@@ -89,34 +89,42 @@ template <typename F> __device__ __forceinline__ void for_adapters(const Rows& r
     }
 }
 
+// A step's 128 bytes of a row, in the wave's LDS: piece i of row r lies at i ^ (r % 8), so that
+// neither the rows' pieces, as they arrive, nor the operands' columns meet in a bank.
+__device__ __forceinline__ int in_row(int row, int piece) { return row * 8 + (piece ^ (row & 7)); }
+
 // Ranks rank0 .. of h = A x for up to 16 CU rows of one adapter, the waves sharing k.
-template <typename T, int CU, int RT>
+// Eight neighbouring lanes take 128 neighbouring bytes of a row, and the operands form in LDS: loaded
+// as operands, each of a load's lanes would go to another row, and the cache looks up four times
+// as often.  sink(n, r, sum) takes element r of the n-th row.
+template <typename T, int CU, int RT, int KW, typename F>
 __device__ __forceinline__ void down_rows(const Params& p, int ad, int rank0, int rank, int order, int rows, int64_t row0,
-                                          int split, float (*red)[64][20])
+                                          int split, u4_t* lds, F sink)
 {
-    constexpr int E = Vec<T>::E, STEP = 8 * E, KW = kDownWaves;
-    constexpr int U = RT + CU <= 2 ? 4 : RT + CU <= 5 ? 2 : 1;   // steps requested at once
-    constexpr int S = 4 < CU * RT ? 4 : CU * RT;        // 16 x 16 tiles that meet in LDS at once
+    constexpr int E = Vec<T>::E, STEP = 8 * E;
+    constexpr int R = 16 * (CU + RT), IT = R / 8;       // rows of x, then of A; loads of a step
+    constexpr int S = 4 < CU * RT ? 4 : CU * RT;        // 16 x 16 tiles that meet at once
     typedef typename Vec<T>::type V;
     const int lane = threadIdx.x & 63, wave = uniform(threadIdx.x >> 6);
     const int col = lane & 15, quarter = lane >> 4;
     const int64_t k0 = split * p.k_per, k1 = k0 + p.k_per < p.k ? k0 + p.k_per : p.k;
     const int full = (int)((k1 - k0) / STEP);
     const int left = (int)((k1 - k0) % STEP);
+    u4_t* mine = lds + wave * (R * 8);
 
-    const T* xp[CU];
+    const T* from[IT];
 #pragma unroll
-    for (int u = 0; u < CU; ++u) {
-        int n = 16 * u + col;
-        n = n < rows ? n : rows - 1;                    // not written
-        xp[u] = static_cast<const T*>(p.x) + (row0 + __shfl(order, n)) * p.x_stride + k0 + quarter * 2 * E;
-    }
-    const T* ap[RT];
-#pragma unroll
-    for (int t = 0; t < RT; ++t) {
-        int r = 16 * t + col;
-        r = r < rank ? r : rank - 1;                    // not written
-        ap[t] = static_cast<const T*>(p.a) + ((int64_t)ad * p.rank + rank0 + r) * p.k + k0 + quarter * 2 * E;
+    for (int i = 0; i < IT; ++i) {
+        int r = 8 * i + (lane >> 3);
+        if (i < 2 * CU) {
+            r = r < rows ? r : rows - 1;                // not written
+            from[i] = static_cast<const T*>(p.x) + (row0 + __shfl(order, r)) * p.x_stride;
+        } else {
+            r -= 16 * CU;
+            r = r < rank ? r : rank - 1;                // not written
+            from[i] = static_cast<const T*>(p.a) + ((int64_t)ad * p.rank + rank0 + r) * p.k;
+        }
+        from[i] += k0 + (lane & 7) * E;
     }
     f4_t acc[CU][RT];
 #pragma unroll
@@ -124,74 +132,73 @@ __device__ __forceinline__ void down_rows(const Params& p, int ad, int rank0, in
 #pragma unroll
         for (int t = 0; t < RT; ++t) acc[u][t] = f4_t{0.0f, 0.0f, 0.0f, 0.0f};
 
-    int s = wave;
-    for (; s + (U - 1) * KW < full; s += U * KW) {
-        V xv[U][CU][2], av[U][RT][2];
+    V next[IT];
+    auto request = [&](int s) {
+        if (s < full) {
 #pragma unroll
-        for (int i = 0; i < U; ++i)
-#pragma unroll
-            for (int e = 0; e < 2; ++e) {
-                const int64_t at = (int64_t)(s + i * KW) * STEP + e * E;
-#pragma unroll
-                for (int u = 0; u < CU; ++u) xv[i][u][e] = load(xp[u] + at);
-#pragma unroll
-                for (int t = 0; t < RT; ++t) av[i][t][e] = load(ap[t] + at);
+            for (int i = 0; i < IT; ++i) {
+                // one 16-row tile may hold few rows: the others' loads would cost as much
+                if (CU > 1 || i >= 2 || 8 * i + (lane >> 3) < rows) next[i] = load(from[i] + (int64_t)s * STEP);
+                else next[i] = V{};
             }
+        } else {
 #pragma unroll
-        for (int i = 0; i < U; ++i)
+            for (int i = 0; i < IT; ++i) next[i] = load_some(from[i] + (int64_t)s * STEP, left - (lane & 7) * E);
+        }
+    };
+    const int steps = full + (left > 0 ? 1 : 0);
+    if (wave < steps) request(wave);
+    __syncthreads();                                    // LDS held the last adapter's sums
+    for (int s = wave; s < steps; s += KW) {
 #pragma unroll
-            for (int e = 0; e < 2; ++e)
-#pragma unroll
-                for (int t = 0; t < RT; ++t)
-#pragma unroll
-                    for (int u = 0; u < CU; ++u) acc[u][t] = product(av[i][t][e], xv[i][u][e], acc[u][t]);
-    }
-    for (; s <= full; s += KW) {
-        const int64_t at = (int64_t)s * STEP;
-        const int valid = s < full ? STEP : left;
-        if (valid == 0) break;
+        for (int i = 0; i < IT; ++i)
+            mine[in_row(8 * i + (lane >> 3), lane & 7)] = __builtin_bit_cast(u4_t, next[i]);
+        __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");   // a wave's LDS operations complete in order
+        if (s + KW < steps) request(s + KW);
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
-            const int here = valid - quarter * 2 * E - e * E;
             V xv[CU], av[RT];
 #pragma unroll
-            for (int u = 0; u < CU; ++u) xv[u] = load_some(xp[u] + at + e * E, here);
+            for (int u = 0; u < CU; ++u) xv[u] = __builtin_bit_cast(V, mine[in_row(16 * u + col, 2 * quarter + e)]);
 #pragma unroll
-            for (int t = 0; t < RT; ++t) av[t] = load_some(ap[t] + at + e * E, here);
+            for (int t = 0; t < RT; ++t) av[t] = __builtin_bit_cast(V, mine[in_row(16 * (CU + t) + col, 2 * quarter + e)]);
 #pragma unroll
             for (int t = 0; t < RT; ++t)
 #pragma unroll
                 for (int u = 0; u < CU; ++u) acc[u][t] = product(av[t], xv[u], acc[u][t]);
         }
+        __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");   // before the next step's
     }
     // the waves' sums meet in LDS
+    float(*red)[64][20] = reinterpret_cast<float(*)[64][20]>(lds);
 #pragma unroll
     for (int i0 = 0; i0 < CU * RT; i0 += S) {
         if (i0 / CU * 16 >= rank) break;
-        __syncthreads();                                // the last ones have been read
+        __syncthreads();                                // the operands, or the last sums, have been read
 #pragma unroll
         for (int i = 0; i < S; ++i)
             *reinterpret_cast<f4_t*>(&red[wave][16 * i + col][4 * quarter]) = acc[(i0 + i) % CU][(i0 + i) / CU];
         __syncthreads();
 #pragma unroll
-        for (int part = 0; part < (16 * S + 31) / 32; ++part) {
-            const int at = (threadIdx.x >> 4) + 32 * part, r0 = threadIdx.x & 15;
+        for (int part = 0; part < (4 * S + KW - 1) / KW; ++part) {
+            const int at = (threadIdx.x >> 4) + 4 * KW * part, r0 = threadIdx.x & 15;
             const int i = i0 + at / 16, n = 16 * (i % CU) + at % 16, r = 16 * (i / CU) + r0;
-            const int row = __shfl(order, n & 63);
-            if (at < 16 * S && n < rows && r < rank) {
-                float sum = 0.0f;
+            float sum = 0.0f;
+            if (at < 16 * S) {
 #pragma unroll
                 for (int w = 0; w < KW; ++w) sum += red[w][at][r0];
-                p.h[((int64_t)split * p.m + row0 + row) * p.pitch + rank0 + r] = sum;
             }
+            sink(n, r, sum, at < 16 * S && n < rows && r < rank);
         }
     }
 }
 
 // h = A x for a tile of 64 rows, 16 RT ranks and the adapters of one slot.
-template <typename T, int RT> __global__ __launch_bounds__(kDownWaves * 64, RT <= 2 ? 4 : 2) void adapters_down_kernel(Params p)
+template <typename T, int RT> __global__ __launch_bounds__(kDownWaves * 64, RT <= 2 ? 3 : 2) void adapters_down_kernel(Params p)
 {
-    __shared__ __align__(16) float red[kDownWaves][64][20];
+    constexpr int KW = kDownWaves;
+    __shared__ __align__(16) u4_t lds[KW * 16 * (4 + RT) * 8];
+    static_assert(sizeof(lds) >= sizeof(float) * KW * 64 * 20, "the sums fit");
     const int lane = threadIdx.x & 63;
     const int slot = blockIdx.x % p.slots, split = blockIdx.x / p.slots % p.splits;
     const int rank0 = blockIdx.x / p.slots / p.splits % p.rblocks * (16 * RT);
@@ -201,237 +208,298 @@ template <typename T, int RT> __global__ __launch_bounds__(kDownWaves * 64, RT <
         const int order = gathered(same, lane), rows = __builtin_popcountll(same);
         const int here = rank - rank0 < 16 * RT ? rank - rank0 : 16 * RT;
         if (here <= 0) return;
-        if (rows > 32) down_rows<T, 4, RT>(p, ad, rank0, here, order, rows, row0, split, red);
-        else if (rows > 16) down_rows<T, 2, RT>(p, ad, rank0, here, order, rows, row0, split, red);
-        else down_rows<T, 1, RT>(p, ad, rank0, here, order, rows, row0, split, red);
+        float* h = p.h + ((int64_t)split * p.m + row0) * p.pitch + rank0;
+        auto sink = [&](int n, int r, float sum, bool there) {
+            const int row = __shfl(order, n & 63);
+            if (there) h[row * p.pitch + r] = sum;
+        };
+        if (rows > 32) down_rows<T, 4, RT, KW>(p, ad, rank0, here, order, rows, row0, split, lds, sink);
+        else if (rows > 16) down_rows<T, 2, RT, KW>(p, ad, rank0, here, order, rows, row0, split, lds, sink);
+        else down_rows<T, 1, RT, KW>(p, ad, rank0, here, order, rows, row0, split, lds, sink);
     });
 }
 
-// N ranks of h from rank r of a row on, the splits' sums added.
-template <int N>
-__device__ __forceinline__ void add_parts(const Params& p, int64_t row, int r, int rank, bool there, float* v)
-{
-#pragma unroll
-    for (int i = 0; i < N; ++i) v[i] = 0.0f;
-    if (!there || r >= rank) return;
-    const float* h = p.h + row * p.pitch + r;
-    const int64_t step = p.m * p.pitch;
-    int s = 0;
-    for (; s + 4 <= p.splits; s += 4, h += 4 * step) {
-        f4_t q[4][N / 4];
-#pragma unroll
-        for (int k = 0; k < 4; ++k)
-#pragma unroll
-            for (int i = 0; i < N / 4; ++i) q[k][i] = *reinterpret_cast<const f4_t*>(h + k * step + 4 * i);
-#pragma unroll
-        for (int k = 0; k < 4; ++k)
-#pragma unroll
-            for (int i = 0; i < N; ++i) v[i] += q[k][i / 4][i % 4];
-    }
-    for (; s < p.splits; ++s, h += step)
-#pragma unroll
-        for (int i = 0; i < N / 4; ++i) {
-            const f4_t q = *reinterpret_cast<const f4_t*>(h + 4 * i);
-#pragma unroll
-            for (int e = 0; e < 4; ++e) v[4 * i + e] += q[e];
-        }
-#pragma unroll
-    for (int i = 0; i < N; ++i) v[i] = r + i < rank ? v[i] : 0.0f;
-}
-
 // The second product's operands.  RC: 32-rank chunks; 0: up to 16 ranks, both fp16 parts
-// of h in one product.
+// of h in one product.  Four ranks r0 .. of a row of h, summed over the splits, go into LDS
+// as operands; PITCH / 4 neighbouring lanes hold a row.
 template <typename T, int RC> struct Up;
 
 template <int RC> struct Up<_Float16, RC> {
-    static constexpr int NC = RC == 0 ? 1 : RC, PARTS = RC == 0 ? 1 : 2;
+    static constexpr int PITCH = RC == 0 ? 16 : 32 * RC, NC = RC == 0 ? 1 : RC, PARTS = RC == 0 ? 1 : 2, NH = NC * PARTS;
     typedef h8_t piece;
-    // column of row i of tile j: a lane's results are 8 neighbours of the first 32
-    // columns and 8 of the second
-    static __device__ __forceinline__ int column(int j, int i) { return 32 * (j >> 1) + 8 * (i >> 2) + 4 * (j & 1) + (i & 3); }
+    typedef _Float16 h4 __attribute__((ext_vector_type(4)));
     static __device__ __forceinline__ int rank0(int c, int quarter) { return RC == 0 ? 8 * (quarter & 1) : 32 * c + 8 * quarter; }
     // h as two fp16 parts, 22 bits, of the row scaled to below 2^15; the power of two taken out
-    static __device__ __forceinline__ float load_h(const Params& p, int64_t row, int rank, bool there, int quarter, piece* out)
+    static __device__ __forceinline__ float put(const f4_t& v, int row, int r0, piece (*hf)[NH][64])
     {
-        float v[NC][8], mx = 0.0f;
+        float mx = 0.0f;
 #pragma unroll
-        for (int c = 0; c < NC; ++c) {
-            add_parts<8>(p, row, rank0(c, quarter), rank, there, v[c]);
+        for (int i = 0; i < 4; ++i) mx = fmaxf(mx, fabsf(v[i]) < __builtin_inff() ? fabsf(v[i]) : 0.0f);
 #pragma unroll
-            for (int i = 0; i < 8; ++i) mx = fmaxf(mx, fabsf(v[c][i]) < __builtin_inff() ? fabsf(v[c][i]) : 0.0f);
-        }
-        mx = fmaxf(mx, __shfl_xor(mx, 16));
-        mx = fmaxf(mx, __shfl_xor(mx, 32));
+        for (int off = 1; off < PITCH / 4; off <<= 1) mx = fmaxf(mx, __shfl_xor(mx, off));
         int e = mx > 0.0f ? (int)(__builtin_bit_cast(uint32_t, mx) >> 23) - 127 - 14 : 0;
         e = e < -126 ? -126 : e;
         const float down = __builtin_bit_cast(float, (uint32_t)(127 - e) << 23);
+        h4 hi, lo;
 #pragma unroll
-        for (int c = 0; c < NC; ++c) {
-            h8_t hi, lo;
-#pragma unroll
-            for (int i = 0; i < 8; ++i) {
-                const float s = v[c][i] * down;
-                hi[i] = (_Float16)s;
-                lo[i] = fabsf(s) < __builtin_inff() ? (_Float16)(s - (float)hi[i]) : (_Float16)0.0f;
-            }
-            if constexpr (RC == 0) out[0] = quarter < 2 ? hi : lo;
-            else {
-                out[2 * c] = hi;
-                out[2 * c + 1] = lo;
-            }
+        for (int i = 0; i < 4; ++i) {
+            const float s = v[i] * down;
+            hi[i] = (_Float16)s;
+            lo[i] = fabsf(s) < __builtin_inff() ? (_Float16)(s - (float)hi[i]) : (_Float16)0.0f;
+        }
+        const int u = row / 16, at = 16 * (r0 % 32 / 8) + row % 16, half = r0 / 4 & 1;
+        if constexpr (RC == 0) {
+            reinterpret_cast<h4*>(&hf[u][0][at])[half] = hi;
+            reinterpret_cast<h4*>(&hf[u][0][at + 32])[half] = lo;
+        } else {
+            reinterpret_cast<h4*>(&hf[u][r0 / 32 * 2][at])[half] = hi;
+            reinterpret_cast<h4*>(&hf[u][r0 / 32 * 2 + 1][at])[half] = lo;
         }
         return __builtin_bit_cast(float, (uint32_t)(127 + e) << 23);
     }
 };
 
 template <int RC> struct Up<float, RC> {
-    static constexpr int NC = RC == 0 ? 1 : 2 * RC, PARTS = 1;   // 16-rank chunks
+    static constexpr int PITCH = RC == 0 ? 16 : 32 * RC, NC = PITCH / 16, PARTS = 1, NH = NC;   // 16-rank chunks
     typedef f4_t piece;
-    static __device__ __forceinline__ int column(int j, int i) { return 16 * j + i; }
     static __device__ __forceinline__ int rank0(int c, int quarter) { return 16 * c + 4 * quarter; }
-    static __device__ __forceinline__ float load_h(const Params& p, int64_t row, int rank, bool there, int quarter, piece* out)
+    static __device__ __forceinline__ float put(const f4_t& v, int row, int r0, piece (*hf)[NH][64])
     {
-#pragma unroll
-        for (int c = 0; c < NC; ++c) {
-            float v[4];
-            add_parts<4>(p, row, rank0(c, quarter), rank, there, v);
-            out[c] = f4_t{v[0], v[1], v[2], v[3]};
-        }
+        hf[row / 16][r0 / 16][16 * (r0 % 16 / 4) + row % 16] = v;
         return 1.0f;
     }
 };
 
-// A lane's elements of base in N 16-row tiles.
+// A lane's pieces of base in N 16-row tiles.
 template <typename T, int NT> struct Base {
     static constexpr int N = NT;
     typename Vec<T>::type v[N][16 / Vec<T>::E];
-    int row[N];
+    int row[N][16 / Vec<T>::E];
 };
 
-// y = base + s B h for 64 rows and 64 columns a wave.
-template <typename T, int RC> __global__ __launch_bounds__(kUpWaves * 64, RC <= 1 ? 4 : 2) void adapters_up_kernel(Params p)
-{
+// A wave's 64 columns of y = base + s B h, for rows of a tile of 64.  The products leave a column
+// of 16 rows to a quarter of the wave; through LDS they come back as whole pieces of a row, and base
+// and y are read and written 128 (fp32: 256) neighbouring bytes at a time.
+template <typename T, int RC> struct Columns {
     typedef Up<T, RC> O;
     typedef typename Vec<T>::type V;
-    constexpr int E = Vec<T>::E, PIECES = 16 / E;       // 16-byte pieces of a lane's 16 columns
-    constexpr int NH = O::NC * O::PARTS;
-    constexpr int PRE = sizeof(T) == 4 ? (RC < 2 ? 2 : 1) : RC < 4 ? 4 : 2;   // 16-row tiles whose base is requested at once
-    __shared__ __align__(16) typename O::piece hf[4][NH][64];    // h of four 16-row tiles, as operands
-    __shared__ float back[4][16];
+    static constexpr int E = Vec<T>::E, LANES = 64 / E, STEP = 64 / LANES;   // lanes to a row's 64 columns, rows at a time
+    static constexpr int PIECES = 16 / STEP;            // of a lane in a 16-row tile
 
-    const int lane = threadIdx.x & 63, wave = uniform(threadIdx.x >> 6);
-    const int col = lane & 15, quarter = lane >> 4;
-    const int slot = blockIdx.x % p.slots;
-    const int64_t n0 = ((int64_t)(blockIdx.x / p.slots % p.nblocks) * kUpWaves + wave) * 64;
-    const int64_t row0 = (int64_t)(blockIdx.x / p.slots / p.nblocks) * 64;
-    const bool busy = n0 < p.n;                         // a wave past the columns only prepares h
-    const Rows mine = rows_of(p, row0 + lane);
-    auto at = [&](int i) { return O::column(i * E / 4, 4 * quarter); };   // column of piece i of the lane
-    auto put = [&](T* y, int i, const V& v) {
-        const int64_t left = p.n - n0 - at(i);
-        if (left >= E) store(y + at(i), v);
+    const Params& p;
+    int64_t n0, left;
+    int lane, c0, r0;                                   // column and row of the lane's first piece
+    bool busy;                                          // a wave past the columns only prepares h
+    const T* base;
+    T* y;
+    V b[O::NC][4];
+    float scale;
+
+    __device__ __forceinline__ Columns(const Params& q, int64_t row0, int64_t first) : p(q), n0(first)
+    {
+        lane = threadIdx.x & 63;
+        c0 = lane % LANES * E;
+        r0 = lane / LANES;
+        left = p.n - n0 - c0;
+        busy = n0 < p.n;
+        base = p.base ? static_cast<const T*>(p.base) + row0 * p.base_stride + n0 + c0 : nullptr;
+        y = static_cast<T*>(p.y) + row0 * p.y_stride + n0 + c0;
+    }
+    __device__ __forceinline__ void put(T* at, const V& v) const
+    {
+        if (left >= E) store(at, v);
         else
 #pragma unroll
             for (int e = 0; e < E; ++e)
-                if (e < left) y[at(i) + e] = v[e];
-    };
-    const T* base0 = p.base ? static_cast<const T*>(p.base) + row0 * p.base_stride + n0 : nullptr;
-    T* y0 = static_cast<T*>(p.y) + row0 * p.y_stride + n0;
-
+                if (e < left) at[e] = v[e];
+    }
     // rows without an adapter
-    const uint64_t none = __builtin_amdgcn_ballot_w64(mine.adapter < 0 && row0 + lane < p.m);
-    if (none && slot == 0 && busy && base0 != y0) {
+    __device__ __forceinline__ void copy(uint64_t none) const
+    {
+        if (!none || !busy || base == y) return;
         const int order = gathered(none, lane), rows = __builtin_popcountll(none);
-        for (int u = 0; 16 * u < rows; ++u) {
-            const int row = __shfl(order, 16 * u + col);
-            if (16 * u + col < rows) {
-#pragma unroll
-                for (int i = 0; i < PIECES; ++i) {
-                    V v = {};
-                    if (base0) v = load_some(base0 + row * p.base_stride + at(i), p.n - n0 - at(i));
-                    put(y0 + row * p.y_stride, i, v);
-                }
+        for (int n = r0; n < rows + r0; n += STEP) {
+            const int row = __shfl(order, n & 63);
+            if (n < rows) {
+                V v = {};
+                if (base) v = load_some(base + row * p.base_stride, left);
+                put(y + row * p.y_stride, v);
             }
         }
     }
-    for_adapters(mine, slot, p.slots, [&](int ad, int rank, uint64_t same) {
-        const int order = gathered(same, lane), rows = __builtin_popcountll(same);
-        // B, of this wave's columns
-        V b[O::NC][4];
+    __device__ __forceinline__ void load_b(int ad, int rank)
+    {
+        const int col = lane & 15, quarter = lane >> 4;
         const T* w = static_cast<const T*>(p.b) + (int64_t)ad * p.n * p.rank;
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
-            int64_t n = n0 + O::column(j, col);
+            int64_t n = n0 + 16 * j + col;
             n = n < p.n ? n : p.n - 1;                  // not written
 #pragma unroll
             for (int c = 0; c < O::NC; ++c)
                 b[c][j] = load_some(w + n * p.rank + O::rank0(c, quarter), rank - O::rank0(c, quarter));
         }
-        const float scale = p.scales ? p.scales[ad] : 1.0f;
-        // N 16-row tiles of base from tile g on
-        auto request = [&](auto in, int g) {
+        scale = p.scales ? p.scales[ad] : 1.0f;
+    }
+    // base of N 16-row tiles from tile g on
+    template <int N> __device__ __forceinline__ Base<T, N> request(int order, int rows, int g) const
+    {
+        Base<T, N> in;
 #pragma unroll
-            for (int u = 0; u < decltype(in)::N; ++u) {
-                in.row[u] = __shfl(order, 16 * (g + u) + col);
+        for (int u = 0; u < N; ++u)
 #pragma unroll
-                for (int i = 0; i < PIECES; ++i) {
-                    in.v[u][i] = V{};
-                    if (base0 && busy && 16 * (g + u) + col < rows)
-                        in.v[u][i] = load_some(base0 + in.row[u] * p.base_stride + at(i), p.n - n0 - at(i));
-                }
+            for (int i = 0; i < PIECES; ++i) {
+                const int n = 16 * (g + u) + i * STEP + r0;
+                in.row[u][i] = __shfl(order, n & 63);
+                in.v[u][i] = V{};
+                if (base && busy && n < rows) in.v[u][i] = load_some(base + in.row[u][i] * p.base_stride, left);
             }
-            return in;
-        };
-        auto finish = [&](const auto& in, int g) {
+        return in;
+    }
+    template <int N>
+    __device__ __forceinline__ void finish(const Base<T, N>& in, int rows, int g, const typename O::piece (*hf)[O::NH][64],
+                                           const float* back, float (*turn)[68]) const
+    {
+        const int col = lane & 15, quarter = lane >> 4;
 #pragma unroll
-            for (int u = 0; u < std::decay<decltype(in)>::type::N; ++u) {
-                if (16 * (g + u) >= rows) break;
-                f4_t acc[4];
+        for (int u = 0; u < N; ++u) {
+            if (16 * (g + u) >= rows) break;
+            f4_t acc[4];
 #pragma unroll
-                for (int j = 0; j < 4; ++j) acc[j] = f4_t{0.0f, 0.0f, 0.0f, 0.0f};
+            for (int j = 0; j < 4; ++j) acc[j] = f4_t{0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
-                for (int c = 0; c < NH; ++c) {
-                    const typename O::piece h = hf[g + u][c][lane];
+            for (int c = 0; c < O::NH; ++c) {
+                const typename O::piece h = hf[g + u][c][lane];
 #pragma unroll
-                    for (int j = 0; j < 4; ++j) acc[j] = product(b[c / O::PARTS][j], h, acc[j]);
-                }
-                const float factor = scale * back[g + u][col];
-                if (16 * (g + u) + col < rows) {
-#pragma unroll
-                    for (int i = 0; i < PIECES; ++i) {
-                        V v;
-#pragma unroll
-                        for (int e = 0; e < E; ++e)
-                            v[e] = (T)__builtin_fmaf(acc[(i * E + e) / 4][e & 3], factor, (float)in.v[u][i][e]);
-                        put(y0 + in.row[u] * p.y_stride, i, v);
-                    }
-                }
+                for (int j = 0; j < 4; ++j) acc[j] = product(b[c / O::PARTS][j], h, acc[j]);
             }
-        };
-        // h: a 16-row tile to a wave
+#pragma unroll
+            for (int j = 0; j < 4; ++j) *reinterpret_cast<f4_t*>(&turn[col][16 * j + 4 * quarter]) = acc[j];
+            __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+#pragma unroll
+            for (int i = 0; i < PIECES; ++i) {
+                const int at = i * STEP + r0, n = 16 * (g + u) + at;
+                const float factor = scale * back[n];
+                V v;
+#pragma unroll
+                for (int q = 0; q < E / 4; ++q) {
+                    const f4_t t = *reinterpret_cast<const f4_t*>(&turn[at][c0 + 4 * q]);
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) v[4 * q + e] = (T)__builtin_fmaf(t[e], factor, (float)in.v[u][i][4 * q + e]);
+                }
+                if (n < rows) put(y + in.row[u][i] * p.y_stride, v);
+            }
+            __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+        }
+    }
+};
+
+template <typename T, int RC> __global__ __launch_bounds__(kUpWaves * 64, RC <= 1 ? 4 : 2) void adapters_up_kernel(Params p)
+{
+    typedef Up<T, RC> O;
+    constexpr int TH = O::PITCH / 4;                    // lanes to a row of h
+    constexpr int PRE = sizeof(T) == 4 ? (RC < 2 ? 2 : 1) : RC < 4 ? 4 : 2;   // 16-row tiles whose base is requested at once
+    __shared__ __align__(16) typename O::piece hf[4][O::NH][64];    // h of four 16-row tiles, as operands
+    __shared__ float back[64];
+    __shared__ __align__(16) float turn[kUpWaves][16][68];
+
+    const int lane = threadIdx.x & 63, wave = uniform(threadIdx.x >> 6);
+    const int slot = blockIdx.x % p.slots;
+    const int64_t n0 = ((int64_t)(blockIdx.x / p.slots % p.nblocks) * kUpWaves + wave) * 64;
+    const int64_t row0 = (int64_t)(blockIdx.x / p.slots / p.nblocks) * 64;
+    const Rows mine = rows_of(p, row0 + lane);
+    Columns<T, RC> w(p, row0, n0);
+    const uint64_t none = __builtin_amdgcn_ballot_w64(mine.adapter < 0 && row0 + lane < p.m);
+    if (slot == 0) w.copy(none);
+    for_adapters(mine, slot, p.slots, [&](int ad, int rank, uint64_t same) {
+        const int order = gathered(same, lane), rows = __builtin_popcountll(same);
+        w.load_b(ad, rank);
+        // h: four ranks to a thread
         auto prepare = [&]() {
             __syncthreads();                            // the last adapter's has been read
-            for (int u = wave; 16 * u < rows; u += kUpWaves) {
-                typename O::piece h[NH];
-                const int64_t from = row0 + __shfl(order, 16 * u + col);
-                const float f = O::load_h(p, from, rank, 16 * u + col < rows, quarter, h);
+            for (int at = threadIdx.x; at < (rows + 15) / 16 * 16 * TH; at += kUpWaves * 64) {
+                const int n = at / TH, r = at % TH * 4;
+                const float* h = p.h + (row0 + __shfl(order, n & 63)) * p.pitch + r;
+                f4_t v = {0.0f, 0.0f, 0.0f, 0.0f};
+                if (n < rows && r < rank) {
+                    const int64_t step = p.m * p.pitch;
+                    int s = 0;
+                    for (; s + 4 <= p.splits; s += 4, h += 4 * step) {
+                        f4_t q[4];
 #pragma unroll
-                for (int c = 0; c < NH; ++c) hf[u][c][lane] = h[c];
-                if (quarter == 0) back[u][col] = f;
+                        for (int k = 0; k < 4; ++k) q[k] = *reinterpret_cast<const f4_t*>(h + k * step);
+#pragma unroll
+                        for (int k = 0; k < 4; ++k) v += q[k];
+                    }
+                    for (; s < p.splits; ++s, h += step) v += *reinterpret_cast<const f4_t*>(h);
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) v[i] = r + i < rank ? v[i] : 0.0f;
+                }
+                const float f = O::put(v, n, r, hf);
+                if (r == 0) back[n] = f;
             }
             __syncthreads();
         };
         if (rows <= 16) {
             // a few rows wait for their loads: base on its way beside h.  (More have no registers for it.)
-            const auto in = request(Base<T, 1>(), 0);
+            const auto in = w.template request<1>(order, rows, 0);
             prepare();
-            if (busy) finish(in, 0);
+            if (w.busy) w.finish(in, rows, 0, hf, back, turn[wave]);
         } else {
             prepare();
-            if (!busy) return;
+            if (!w.busy) return;
 #pragma unroll
             for (int g = 0; g < 4; g += PRE)
-                if (16 * g < rows) finish(request(Base<T, PRE>(), g), g);
+                if (16 * g < rows) w.finish(w.template request<PRE>(order, rows, g), rows, g, hf, back, turn[wave]);
+        }
+    });
+}
+
+// Both products in one launch, for few rows: every workgroup forms the h of its slot's
+// adapters, of a tile of 32 rows, by itself.
+template <typename T, int RC> __global__ __launch_bounds__(kOneWaves * 64, 2) void adapters_one_kernel(Params p)
+{
+    typedef Up<T, RC> O;
+    constexpr int RT = O::PITCH / 16, TH = O::PITCH / 4, KW = kOneWaves;
+    __shared__ __align__(16) u4_t lds[KW * 16 * (2 + RT) * 8];
+    static_assert(sizeof(lds) >= sizeof(float) * KW * 16 * 20 * (RT == 1 ? 2 : 4), "the sums fit");
+    __shared__ __align__(16) float hs[32][O::PITCH];
+    __shared__ __align__(16) typename O::piece hf[2][O::NH][64];
+    __shared__ float back[32];
+    float(*turn)[16][68] = reinterpret_cast<float(*)[16][68]>(lds);
+    static_assert(sizeof(lds) >= sizeof(float) * KW * 16 * 68, "a tile of every wave fits");
+
+    const int lane = threadIdx.x & 63, wave = uniform(threadIdx.x >> 6);
+    const int slot = blockIdx.x % p.slots;
+    const int64_t n0 = ((int64_t)(blockIdx.x / p.slots % p.nblocks) * KW + wave) * 64;
+    const int64_t row0 = (int64_t)(blockIdx.x / p.slots / p.nblocks) * 32;
+    const bool there = lane < 32 && row0 + lane < p.m;
+    const Rows mine = rows_of(p, there ? row0 + lane : p.m);
+    Columns<T, RC> w(p, row0, n0);
+    const uint64_t none = __builtin_amdgcn_ballot_w64(there && mine.adapter < 0);
+    if (slot == 0) w.copy(none);
+    for_adapters(mine, slot, p.slots, [&](int ad, int rank, uint64_t same) {
+        const int order = gathered(same, lane), rows = __builtin_popcountll(same);
+        w.load_b(ad, rank);
+        const auto in = w.template request<1>(order, rows, 0);
+        auto sink = [&](int n, int r, float sum, bool real) {
+            if (real) hs[n][r] = sum;
+        };
+        if (rows > 16) down_rows<T, 2, RT, KW>(p, ad, 0, rank, order, rows, row0, 0, lds, sink);
+        else down_rows<T, 1, RT, KW>(p, ad, 0, rank, order, rows, row0, 0, lds, sink);
+        __syncthreads();
+        for (int at = threadIdx.x; at < (rows + 15) / 16 * 16 * TH; at += KW * 64) {
+            const int n = at / TH, r = at % TH * 4;
+            f4_t v = *reinterpret_cast<const f4_t*>(&hs[n][r]);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) v[i] = n < rows && r + i < rank ? v[i] : 0.0f;
+            const float f = O::put(v, n, r, hf);
+            if (r == 0) back[n] = f;
+        }
+        __syncthreads();
+        if (w.busy) {
+            w.finish(in, rows, 0, hf, back, turn[wave]);
+            if (rows > 16) w.finish(w.template request<1>(order, rows, 1), rows, 1, hf, back, turn[wave]);
         }
     });
 }
@@ -459,8 +527,20 @@ template <typename T> hipError_t launch_up(Params p, const Plan& c, hipStream_t 
     return hipGetLastError();
 }
 
+template <typename T> hipError_t launch_one(Params p, const Plan& c, hipStream_t s)
+{
+    p.slots = c.one_slots;
+    p.k_per = p.k;
+    p.nblocks = (int)ceil_div(p.n, 64 * kOneWaves);
+    const dim3 grid((unsigned)(ceil_div(p.m, 32) * p.nblocks * p.slots)), block(kOneWaves * 64);
+    if (p.rank <= 16) adapters_one_kernel<T, 0><<<grid, block, 0, s>>>(p);
+    else adapters_one_kernel<T, 1><<<grid, block, 0, s>>>(p);
+    return hipGetLastError();
+}
+
 template <typename T> hipError_t launch_both(const Params& p, const Plan& c, hipStream_t s)
 {
+    if (c.one) return launch_one<T>(p, c, s);
     const hipError_t e = launch_down<T>(p, c, s);
     return e != hipSuccess ? e : launch_up<T>(p, c, s);
 }
@@ -472,7 +552,7 @@ template <typename T> hipError_t launch_both(const Params& p, const Plan& c, hip
 size_t adapters_workspace(int64_t m, int64_t n, int64_t k, int rank, int count, int f16)
 {
     const adapters::Plan c = adapters::plan_of(m, n, k, rank, count, f16);
-    return (size_t)c.splits * m * c.pitch * 4;
+    return c.one ? 0 : (size_t)c.splits * m * c.pitch * 4;
 }
 
 hipError_t launch_adapters(const AdapterArgs& a, hipStream_t stream, const char** variant)
@@ -499,7 +579,7 @@ hipError_t launch_adapters(const AdapterArgs& a, hipStream_t stream, const char*
     p.count = a.count;
     p.splits = c.splits;
     p.pitch = c.pitch;
-    *variant = "adapters";
+    *variant = c.one ? "adapters_one" : "adapters";
     return a.f16 ? adapters::launch_both<_Float16>(p, c, stream) : adapters::launch_both<float>(p, c, stream);
 }
 

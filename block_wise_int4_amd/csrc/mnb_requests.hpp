@@ -41,7 +41,7 @@ struct VerifyArgs {
     void* workspace;
     int f16;
 };
-constexpr int kVerifyChunk = 4096;   // tokens of a workgroup
+constexpr int kVerifyChunk = 1024;   // tokens of a wave
 inline int64_t verify_chunks(int64_t vocab) { return (vocab + kVerifyChunk - 1) / kVerifyChunk; }
 // Two sums in 64 bits per sequence and chunk.
 inline size_t verify_workspace(int64_t batch, int64_t vocab) { return (size_t)(batch * verify_chunks(vocab)) * 16; }

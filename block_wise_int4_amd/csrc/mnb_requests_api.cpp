@@ -59,7 +59,7 @@ mnb_status check_verify(int64_t batch, int64_t vocab)
         return fail(MNB_ERR_INVALID_ARGUMENT, "batch must be >= 0 and vocab >= 1 (got %lld, %lld)", (long long)batch,
                     (long long)vocab);
     if (vocab > (1 << 30)) return fail(MNB_ERR_UNSUPPORTED, "vocab %lld not supported (at most 2^30)", (long long)vocab);
-    // a workgroup of 256 threads a chunk, in a grid of less than 2^32 threads
+    // a wave a chunk and at most three idle ones a sequence, in a grid of less than 2^32 threads
     if (batch >= (1 << 24) || mnb::verify_chunks(vocab) * batch >= (1 << 24))
         return fail(MNB_ERR_UNSUPPORTED, "batch %lld with vocab %lld not supported", (long long)batch, (long long)vocab);
     return MNB_OK;

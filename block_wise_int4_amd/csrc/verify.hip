@@ -107,29 +107,44 @@ __device__ __forceinline__ double wave_sum(double x)
     return x;
 }
 
+// Sums of a wave's lanes before this one, and of all.
+__device__ __forceinline__ double before(double x, int lane, double& total)
+{
+    double upto = x;
+#pragma unroll
+    for (int off = 1; off < 64; off <<= 1) {
+        const double y = __shfl_up(upto, off);
+        if (lane >= off) upto += y;
+    }
+    total = __shfl(upto, 63);
+    const double own = __shfl_up(upto, 1);
+    return lane > 0 ? own : 0.0;
+}
+
 template <typename T> __global__ __launch_bounds__(kThreads) void verify_sums_kernel(Params p)
 {
-    constexpr int E = Vec<T>::E, PIECES = kChunk / kThreads / E;
-    __shared__ double red[kThreads / 64][2];
-    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-    const int b = blockIdx.x / p.chunks, chunk = blockIdx.x % p.chunks;
+    constexpr int E = Vec<T>::E, PIECES = kChunk / 64 / E;
+    const int lane = threadIdx.x & 63, wave = uniform(threadIdx.x >> 6);
+    const int groups = (p.chunks + kThreads / 64 - 1) / (kThreads / 64);
+    const int b = blockIdx.x / groups, chunk = blockIdx.x % groups * (kThreads / 64) + wave;
     const Rows r = rows_of(p, b);
     if (r.count == 0) return;
     const int n = uniform(accepted_of<T>(p, r, lane));
-    if (chunk == 0 && threadIdx.x == 0) p.accepted[b] = n;
+    if (chunk == 0 && lane == 0) p.accepted[b] = n;
+    if (chunk >= p.chunks) return;
     const Draw<T> d(p, r, n);
     double rest = 0.0, all = 0.0;
     typename Vec<T>::type tv[PIECES], qv[PIECES];
 #pragma unroll
     for (int i = 0; i < PIECES; ++i) {
-        const int at = chunk * kChunk + (i * kThreads + threadIdx.x) * E;
+        const int at = chunk * kChunk + (i * 64 + lane) * E;
         tv[i] = load_some(d.p + at, p.vocab - at);
         qv[i] = {};
         if (d.q) qv[i] = load_some(d.q + at, p.vocab - at);
     }
 #pragma unroll
     for (int i = 0; i < PIECES; ++i) {
-        const int at = chunk * kChunk + (i * kThreads + threadIdx.x) * E;
+        const int at = chunk * kChunk + (i * 64 + lane) * E;
 #pragma unroll
         for (int e = 0; e < E; ++e) {
             const double w = weight(tv[i][e]);
@@ -140,136 +155,87 @@ template <typename T> __global__ __launch_bounds__(kThreads) void verify_sums_ke
     all = wave_sum(all);
     rest = wave_sum(rest);
     if (lane == 0) {
-        red[wave][0] = rest;
-        red[wave][1] = all;
-    }
-    __syncthreads();
-    if (threadIdx.x < 2) {
-        double s = 0.0;
-#pragma unroll
-        for (int w = 0; w < kThreads / 64; ++w) s += red[w][threadIdx.x];
-        p.sums[((int64_t)b * p.chunks + chunk) * 2 + threadIdx.x] = s;
+        double* out = p.sums + ((int64_t)b * p.chunks + chunk) * 2;
+        out[0] = rest;
+        out[1] = all;
     }
 }
 
-// Sums of a workgroup's threads before this one, and of all.
-__device__ __forceinline__ double scan(double x, double* red, double& total)
+// One wave: the chunk whose sums pass the border, then the token in it.  A lane holds
+// neighbouring chunks, then neighbouring tokens.
+template <typename T> __global__ __launch_bounds__(64) void verify_draw_kernel(Params p)
 {
-    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-    double upto = x;
-#pragma unroll
-    for (int off = 1; off < 64; off <<= 1) {
-        const double y = __shfl_up(upto, off);
-        if (lane >= off) upto += y;
-    }
-    __syncthreads();
-    if (lane == 63) red[wave] = upto;
-    __syncthreads();
-    double before = 0.0;
-    total = 0.0;
-#pragma unroll
-    for (int w = 0; w < kThreads / 64; ++w) {
-        if (w < wave) before += red[w];
-        total += red[w];
-    }
-    const double own = __shfl_up(upto, 1);
-    return before + (lane > 0 ? own : 0.0);
-}
-
-template <typename T> __global__ __launch_bounds__(kThreads) void verify_draw_kernel(Params p)
-{
-    constexpr int E = Vec<T>::E, PER = kChunk / kThreads;
-    __shared__ double red[kThreads / 64];
-    __shared__ int found, last;
-    __shared__ double below;
-    const int b = blockIdx.x, tid = threadIdx.x;
+    constexpr int E = Vec<T>::E, PER = kChunk / 64;
+    typedef double d2_t __attribute__((ext_vector_type(2)));
+    const int b = blockIdx.x, lane = threadIdx.x;
     const Rows r = rows_of(p, b);
     if (r.count == 0) {
-        if (tid == 0) p.accepted[b] = 0;
+        if (lane == 0) p.accepted[b] = 0;
         return;
     }
     int n = p.accepted[b];
     n = n < 0 ? 0 : n >= r.count ? r.count - 1 : n;
-    const Draw<T> d(p, r, n);
-    const double* sums = p.sums + (int64_t)b * p.chunks * 2;
-    // a thread's chunks are neighbours
-    const int per = (p.chunks + kThreads - 1) / kThreads, c0 = tid * per, c1 = c0 + per < p.chunks ? c0 + per : p.chunks;
-    double mine[2] = {0.0, 0.0}, total[2], before[2];
-    for (int c = c0; c < c1; ++c) {
-        mine[0] += sums[2 * c];
-        mine[1] += sums[2 * c + 1];
-    }
-    before[0] = scan(mine[0], red, total[0]);
-    before[1] = scan(mine[1], red, total[1]);
+    n = uniform(n);
+    const d2_t* sums = reinterpret_cast<const d2_t*>(p.sums) + (int64_t)b * p.chunks;
+    const int per = (p.chunks + 63) / 64, c0 = lane * per, c1 = c0 + per < p.chunks ? c0 + per : p.chunks;
+    d2_t mine = {0.0, 0.0};
+#pragma unroll 4
+    for (int c = c0; c < c1; ++c) mine += sums[c];
+    double rest, all;
+    const double rest_before = before(mine[0], lane, rest), all_before = before(mine[1], lane, all);
     // nothing is left of p where q is no smaller anywhere: then p itself
-    const int which = n < r.count - 1 && total[0] > 0.0 ? 0 : 1;
+    const bool left = n < r.count - 1 && rest > 0.0;
     const float u = p.pick[b];
-    const double border = (u > 0.0f ? (double)u : 0.0) * total[which];
-    if (tid == 0) {
-        found = 0x7FFFFFFF;
-        last = -1;
-        below = 0.0;
-    }
-    __syncthreads();
-    double run = before[which];
-    int hit = 0x7FFFFFFF, end = -1;
-    double under = 0.0;
+    const double border = (u > 0.0f ? (double)u : 0.0) * (left ? rest : all);
+    // the first chunk that passes the border; pick of 1 or more passes all: the last with a weight
+    double run = left ? rest_before : all_before, under = 0.0;
+    int hit = -1, end = -1;
     for (int c = c0; c < c1; ++c) {
-        const double s = sums[2 * c + which];
-        if (hit == 0x7FFFFFFF && s > 0.0 && run + s > border) {
+        const double s = left ? sums[c][0] : sums[c][1];
+        if (hit < 0 && s > 0.0 && run + s > border) {
             hit = c;
             under = run;
         }
         if (s > 0.0) end = c;
         run += s;
     }
-    if (hit != 0x7FFFFFFF) atomicMin(&found, hit);
-    if (end >= 0) atomicMax(&last, end);
-    __syncthreads();
-    const bool past = found == 0x7FFFFFFF;              // pick of 1 or more: the last token
-    const int chunk = past ? last : found;
-    if (hit == chunk && !past) below = under;
-    __syncthreads();
-    const double from = below;
+    const uint64_t hits = __builtin_amdgcn_ballot_w64(hit >= 0), ends = __builtin_amdgcn_ballot_w64(end >= 0);
     int token = -1;
-    if (chunk >= 0) {
-        __syncthreads();
-        if (tid == 0) {
-            found = 0x7FFFFFFF;
-            last = -1;
-        }
+    if (ends) {
+        const int from = hits ? __builtin_ctzll(hits) : 63 - __builtin_clzll(ends);
+        const int chunk = __shfl(hits ? hit : end, from);
+        run = __shfl(under, from);
+        const Draw<T> d(p, r, n);
         double w[PER], own = 0.0;
-        const int at = chunk * kChunk + tid * PER;
+        const int at = chunk * kChunk + lane * PER;
+        typename Vec<T>::type tv[PER / E], qv[PER / E];
 #pragma unroll
         for (int i = 0; i < PER / E; ++i) {
-            const typename Vec<T>::type tv = load_some(d.p + at + i * E, p.vocab - at - i * E);
-            typename Vec<T>::type qv = {};
-            if (d.q && which == 0) qv = load_some(d.q + at + i * E, p.vocab - at - i * E);
-#pragma unroll
-            for (int e = 0; e < E; ++e) {
-                const double v = weight(tv[e]);
-                w[i * E + e] = which ? v : d.rest(v, weight(qv[e]), at + i * E + e);
-                own += w[i * E + e];
-            }
+            tv[i] = load_some(d.p + at + i * E, p.vocab - at - i * E);
+            qv[i] = {};
+            if (d.q && left) qv[i] = load_some(d.q + at + i * E, p.vocab - at - i * E);
         }
-        double all;
-        run = from + scan(own, red, all);
-        int first = 0x7FFFFFFF, most = -1;
+#pragma unroll
+        for (int i = 0; i < PER; ++i) {
+            const double v = weight(tv[i / E][i % E]);
+            w[i] = left ? d.rest(v, weight(qv[i / E][i % E]), at + i) : v;
+            own += w[i];
+        }
+        run += before(own, lane, all);
+        int first = -1, last = -1;
 #pragma unroll
         for (int i = 0; i < PER; ++i) {
             run += w[i];
             if (w[i] > 0.0) {
-                if (first == 0x7FFFFFFF && run > border) first = at + i;
-                most = at + i;
+                if (first < 0 && run > border) first = at + i;
+                last = at + i;
             }
         }
-        if (first != 0x7FFFFFFF && !past) atomicMin(&found, first);
-        if (most >= 0) atomicMax(&last, most);
-        __syncthreads();
         // sums of another order may end just below the border: then the chunk's last token
-        token = found == 0x7FFFFFFF ? last : found;
+        const uint64_t firsts = __builtin_amdgcn_ballot_w64(first >= 0), lasts = __builtin_amdgcn_ballot_w64(last >= 0);
+        token = hits && firsts ? __shfl(first, __builtin_ctzll(firsts)) : __shfl(last, 63 - __builtin_clzll(lasts));
     }
-    for (int i = tid; i < r.count; i += kThreads)
+    for (int i = lane; i < r.count; i += 64)
         p.out[r.first + i] = i < n ? p.ids[r.first + i + 1] : i == n ? token : -1;
 }
 
@@ -296,13 +262,14 @@ hipError_t launch_verify(const VerifyArgs& a, hipStream_t stream, const char** v
     p.vocab = (int)a.vocab;
     p.chunks = (int)verify_chunks(a.vocab);
     *variant = "verify_drafts";
-    const dim3 grid((unsigned)(a.batch * p.chunks)), block(verify::kThreads);
+    const int64_t groups = (p.chunks + verify::kThreads / 64 - 1) / (verify::kThreads / 64);
+    const dim3 grid((unsigned)(a.batch * groups)), block(verify::kThreads), one((unsigned)a.batch), wave(64);
     if (a.f16) verify::verify_sums_kernel<_Float16><<<grid, block, 0, stream>>>(p);
     else verify::verify_sums_kernel<float><<<grid, block, 0, stream>>>(p);
     const hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
-    if (a.f16) verify::verify_draw_kernel<_Float16><<<dim3((unsigned)a.batch), block, 0, stream>>>(p);
-    else verify::verify_draw_kernel<float><<<dim3((unsigned)a.batch), block, 0, stream>>>(p);
+    if (a.f16) verify::verify_draw_kernel<_Float16><<<one, wave, 0, stream>>>(p);
+    else verify::verify_draw_kernel<float><<<one, wave, 0, stream>>>(p);
     return hipGetLastError();
 }
 

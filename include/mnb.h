@@ -571,7 +571,7 @@ mnb_status mnb_adapters_add(const mnb_adapter_desc* d, const void* a, const void
  * normalised.  Products and sums are kept in 64 bits.
  * target_stride, draft_stride >= vocab.  out must not overlap ids.  workspace (256-byte
  * aligned): mnb_verify_workspace_bytes; contents need no initialisation.  vocab at most
- * 2^30, batch * ceil(vocab / 4096) < 2^24, else MNB_ERR_UNSUPPORTED.  batch == 0 is a
+ * 2^30, batch * ceil(vocab / 1024) < 2^24, else MNB_ERR_UNSUPPORTED.  batch == 0 is a
  * no-op.  Deterministic. */
 size_t mnb_verify_workspace_bytes(int64_t batch, int64_t vocab);
 mnb_status mnb_verify_drafts(const void* target, int64_t target_stride, const void* draft, int64_t draft_stride,

@@ -57,6 +57,9 @@ SIZES = [  # m, k, n, rank, count
     (15, 512, 128, 32, 4), (16, 521, 5, 33, 40), (17, 63, 257, 64, 2), (33, 1000, 130, 9, 33), (50, 257, 64, 100, 3),
     (100, 2050, 70, 12, 7), (64, 256, 40, 128, 5), (130, 96, 513, 4, 130), (300, 40, 90, 16, 300), (7, 7, 1000, 2, 5),
     (1030, 200, 321, 24, 6), (2049, 72, 50, 3, 3), (4100, 136, 77, 20, 5), (4113, 70, 66, 65, 2),
+    # two launches: many sets of rows and adapters, or ranks past 64
+    (800, 130, 70, 16, 200), (1030, 200, 321, 24, 40), (1000, 513, 65, 33, 64), (830, 2100, 40, 9, 64), (70, 300, 60, 100, 9),
+    (3, 5000, 200, 128, 3), (2100, 64, 300, 8, 5), (33, 600, 16400, 5, 33),
 ]
 
 
@@ -74,7 +77,7 @@ def test_against_the_oracle(mnb, size, order, dt):
 
 
 @pytest.mark.parametrize("dt", ["f16", "f32"])
-@pytest.mark.parametrize("m", [3, 1100])
+@pytest.mark.parametrize("m", [3, 1100, 9000])
 def test_without_base_scales_or_adapters(mnb, m, dt):
     rng = np.random.default_rng(971)
     a, b, x, base, _, _ = operands(rng, m, 100, 70, 10, 4, dt)
@@ -89,7 +92,7 @@ def test_without_base_scales_or_adapters(mnb, m, dt):
 
 
 @pytest.mark.parametrize("dt", ["f16", "f32"])
-@pytest.mark.parametrize("m", [5, 1040])
+@pytest.mark.parametrize("m", [5, 1040, 9001])
 def test_slices_of_wider_rows_and_in_place(mnb, m, dt):
     """x, base and y as columns of wider rows at an odd element; what is beside them stays; y may be base."""
     t = G.torch()
@@ -111,7 +114,7 @@ def test_slices_of_wider_rows_and_in_place(mnb, m, dt):
 
 
 @pytest.mark.parametrize("dt", ["f16", "f32"])
-@pytest.mark.parametrize("m", [20, 1050])
+@pytest.mark.parametrize("m", [20, 1050, 9010])
 def test_bad_values_stay_in_their_row(mnb, m, dt):
     """NaN and infinity in one row, and in an adapter's slot that no row has: the other rows' bits stay."""
     t = G.torch()
@@ -129,15 +132,15 @@ def test_bad_values_stay_in_their_row(mnb, m, dt):
         assert t.equal(got[keep], clean[keep]) and not t.isfinite(got[7]).any()
 
 
-@pytest.mark.parametrize("m", [1, 40])
-def test_large_and_small_products_between(mnb, m):
+@pytest.mark.parametrize("m,n", [(1, 64), (40, 64), (70, 30000)])
+def test_large_and_small_products_between(mnb, m, n):
     """h far past fp16's range, and far below it, while y is inside."""
     rng = np.random.default_rng(974)
     for size, back in ((60000.0, 2.0 ** -20), (2.0 ** -14, 2.0 ** 12)):
-        a, b, x, base, _, _ = operands(rng, m, 600, 64, 24, 2, "f16")
-        x = (x.astype(np.float64) * size / 4).astype(np.float16)
-        scales = np.full(2, back, np.float32)
-        check(mnb, a, b, scales, None, rng.integers(0, 2, m), x, base)
+        a, b, x, base, _, _ = operands(rng, m, 600, n, 24, 9, "f16")
+        x = (x.astype(np.float64) * size / 8).astype(np.float16)
+        scales = np.full(9, back, np.float32)
+        check(mnb, a, b, scales, None, rng.integers(0, 9, m), x, base)
 
 
 def test_repeated_calls_graphs_and_streams_give_the_same_bits(mnb):
@@ -145,7 +148,8 @@ def test_repeated_calls_graphs_and_streams_give_the_same_bits(mnb):
     t = G.torch()
     rng = np.random.default_rng(975)
     sets = []
-    for m, k, n, rank, dt in ((9, 512, 200, 16, "f16"), (1100, 200, 130, 40, "f16"), (30, 300, 100, 8, "f32")):
+    for m, k, n, rank, dt in ((9, 512, 200, 16, "f16"), (1100, 200, 130, 70, "f16"), (30, 300, 100, 8, "f32"),
+                              (9000, 100, 65, 20, "f32")):
         a, b, x, base, scales, _ = operands(rng, m, k, n, rank, 4, dt)
         dev = [G.to_dev(v) for v in (a, b, scales, rng.integers(-1, 4, m).astype(np.int32), x, base)]
         sets.append((mnb.adapter_desc(n, k, rank, 4, dev[4].dtype), dev, t.empty_like(dev[5])))
@@ -196,5 +200,16 @@ def test_binding_refuses_wrong_tensors(mnb):
                       ("adapter", good["adapter"][:2]), ("x", good["x"].cpu()), ("adapter", good["adapter"].cpu())):
         with pytest.raises(ValueError):
             mnb.mnb_adapters_add(d, **dict(good, **{name: bad}))
+    mnb.mnb_adapters_add(d, **dict(good, workspace=None))            # few rows need none
+    a, b = t.zeros(2, 40, 64, **f), t.zeros(2, 32, 40, **f)
     with pytest.raises(mnb.MnbError):
-        mnb.mnb_adapters_add(d, **dict(good, workspace=None))
+        mnb.mnb_adapters_add(mnb.adapter_desc(32, 64, 40, 2, t.float16), **dict(good, a=a, b=b, workspace=None))
+
+
+@pytest.mark.parametrize("m,rank,count,name", [(1, 16, 4, "adapters_one"), (60, 32, 30, "adapters_one"), (3, 33, 2, "adapters"),
+                                               (5000, 16, 9, "adapters")])
+def test_which_kernels_ran(mnb, m, rank, count, name):
+    rng = np.random.default_rng(976)
+    a, b, x, base, scales, _ = operands(rng, m, 80, 70, rank, count, "f16")
+    run(mnb, a, b, scales, None, rng.integers(0, count, m), x, base)
+    assert mnb.mnb_last_variant() == name

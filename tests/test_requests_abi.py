@@ -29,8 +29,8 @@ def verify(**kw):
     dict(dt=2), dict(dt=-1), dict(reserved=1), dict(n=-1), dict(k=0), dict(rank=0), dict(count=-1), dict(m=-1), dict(xs=127),
     dict(bs=95), dict(ys=95), dict(xs=1 << 62), dict(ys=1 << 62), dict(bs=1 << 62), dict(a=None), dict(b=None),
     dict(ad=None), dict(x=None), dict(y=None), dict(a=P + 8), dict(b=P + 8), dict(sc=P + 2), dict(ranks=P + 1),
-    dict(ad=P + 2), dict(x=P + 1), dict(base=P + 1), dict(y=P + 1), dict(dt=F32, x=P + 2), dict(ws=None), dict(ws=P + 16),
-    dict(wb=16)])
+    dict(ad=P + 2), dict(x=P + 1), dict(base=P + 1), dict(y=P + 1), dict(dt=F32, x=P + 2), dict(rank=65, ws=None),
+    dict(rank=65, ws=P + 16), dict(rank=65, wb=16)])
 def test_adapters_refuse(kw):
     _refused(INVALID, add, **kw)
 
@@ -43,15 +43,20 @@ def test_adapters_unsupported(kw):
 
 
 def test_adapters_workspace():
-    d = mnb.mnb_adapter_desc(96, 4096, 20, 3, F16, 0)
-    for m in (1, 5, 100, 5000):
+    # few rows need none; many, or a high rank, rows of h between two launches
+    few, many = mnb.mnb_adapter_desc(96, 2048, 20, 30, F16, 0), mnb.mnb_adapter_desc(96, 4096, 100, 30, F16, 0)
+    assert mnb.mnb_adapters_workspace_bytes(few, 5) == 0
+    if _no_device():
+        _refused(DEVICE, add, m=5, k=2048, xs=2048, rank=20, count=30, ws=None, wb=0)
+    for d, m, pitch in ((few, 5000, 32), (many, 1, 128), (many, 300, 128)):
         n = mnb.mnb_adapters_workspace_bytes(d, m)
-        assert m * 32 * 4 <= n <= m * 32 * 4 * 8
-        _refused(INVALID, add, m=m, k=4096, xs=4096, rank=20, wb=n - 1)
+        assert m * pitch * 4 <= n <= m * pitch * 4 * 8 and n % (m * pitch * 4) == 0
+        kw = dict(m=m, k=d.k, xs=d.k, rank=d.rank, count=30)
+        _refused(INVALID, add, wb=n - 1, **kw)
         if _no_device():
-            _refused(DEVICE, add, m=m, k=4096, xs=4096, rank=20, wb=n)
-    assert mnb.mnb_adapters_workspace_bytes(d, 0) == 0 and mnb.mnb_last_error() == ""
-    assert mnb.mnb_adapters_workspace_bytes(d, -1) == 0 and mnb.mnb_last_error() != ""
+            _refused(DEVICE, add, wb=n, **kw)
+    assert mnb.mnb_adapters_workspace_bytes(few, 0) == 0 and mnb.mnb_last_error() == ""
+    assert mnb.mnb_adapters_workspace_bytes(few, -1) == 0 and mnb.mnb_last_error() != ""
     assert mnb.mnb_adapters_workspace_bytes(mnb.mnb_adapter_desc(96, 4096, 200, 3, F16, 0), 5) == 0
 
 
@@ -77,7 +82,7 @@ def test_verify_unsupported():
 
 
 def test_verify_workspace():
-    for batch, vocab, chunks in ((1, 1, 1), (3, 4096, 1), (3, 4097, 2), (7, 128000, 32)):
+    for batch, vocab, chunks in ((1, 1, 1), (3, 1024, 1), (3, 1025, 2), (7, 128000, 125)):
         assert mnb.mnb_verify_workspace_bytes(batch, vocab) == 16 * batch * chunks
     assert mnb.mnb_verify_workspace_bytes(0, 5) == 0 and mnb.mnb_last_error() == ""
     assert mnb.mnb_verify_workspace_bytes(1, 0) == 0 and mnb.mnb_last_error() != ""
