@@ -27,6 +27,7 @@ inline Plan plan_of(const AttentionArgs& a)
     const bool wide = a.v.head_dim == 256;
     const int gqa = a.v.q_heads / a.v.kv_heads, window = window_of(a.window, a.max_kv);
     int64_t span;                              // keys of a row set in the kernels' count
+    const bool even = a.sinks >= 0 && window > 0;
     auto longest = [&](int64_t set) {
         return longest_span(window, (int)(a.sinks < a.max_kv ? a.sinks : a.max_kv), a.max_kv, set < rows ? set : rows, gqa);
     };
@@ -49,6 +50,15 @@ inline Plan plan_of(const AttentionArgs& a)
         // lengths: more and shorter pieces even them out (32 sequences of up to 8192 keys:
         // 45 us with 512, 41 with 3072)
         want = a.v.batch == 1 ? 512 : 3072;
+        if (even) {
+            // cut from the window, all pieces are alike: a workgroup a CU (window 4096, 8 key heads: 32
+            // sequences 29.8 us whole, 44.0 in nine; 8 sequences 15.5 in four, 18.1 in eleven; 4 of window
+            // 16384 21.7 in eight, 26.8 in sixteen), and halves only of longer spans than 2048 (16 sequences,
+            // window 1024: 11.1 whole, 12.0)
+            const int64_t units = ((rows + c.rows - 1) / c.rows) * a.v.kv_heads * a.v.batch;
+            want = units >= 128 && span <= 2048 ? 1 : units > 256 ? 1 : 256 / units * units;
+            grain = 128;
+        }
     } else {
         c.kind = 2;
         // two column tiles a wave where that leaves a workgroup for every CU (1000
