@@ -536,7 +536,7 @@ mnb_status mnb_attention_kv4_sinks(const mnb_kv4_desc* c, const void* cache, con
  * row's largest where that is more), and y is rounded once.
  * workspace (256-byte aligned): mnb_adapters_workspace_bytes of the same m; contents
  * need no initialisation.  rank at most 128, n and k at most 2^24, m < 2^24, m * n <
- * 2^38, else MNB_ERR_UNSUPPORTED.  m == 0 is a no-op.  Deterministic. */
+ * 2^37, else MNB_ERR_UNSUPPORTED.  m == 0 is a no-op.  Deterministic. */
 typedef struct {
     int64_t n, k;
     int32_t rank, count;
