@@ -27,7 +27,7 @@ struct Params {
     void* y;
     float* h;                         // [splits][m][pitch]
     int64_t m, n, k, x_stride, base_stride, y_stride, k_per;
-    int rank, count, splits, slots, pitch, rblocks, nblocks;
+    int rank, count, splits, slots, pitch, rblocks, nblocks, tile;
 };
 
 __device__ __forceinline__ f4_t mfma16(const h8_t& a, const h8_t& b, const f4_t& c)
@@ -45,14 +45,16 @@ __device__ __forceinline__ f4_t product(const f4_t& a, const f4_t& b, f4_t c)
     return c;
 }
 
-// The rows of a tile of 64, a lane each: adapter (-1: none, out of range or of rank 0) and its rank.
+// The rows of a tile of up to 64, a lane each: adapter (-1: none, out of range or of rank 0) and its rank.
 struct Rows {
     int adapter, rank;
+    bool there;
 };
-__device__ __forceinline__ Rows rows_of(const Params& p, int64_t row)
+__device__ __forceinline__ Rows rows_of(const Params& p, int64_t row0, int lane)
 {
-    Rows r = {-1, p.rank};
-    if (row < p.m) {
+    const int64_t row = row0 + lane;
+    Rows r = {-1, p.rank, lane < p.tile && row < p.m};
+    if (r.there) {
         const int a = p.adapter[row];
         if (a >= 0 && a < p.count) {
             if (p.ranks) r.rank = p.ranks[a] < p.rank ? p.ranks[a] : p.rank;
@@ -60,6 +62,27 @@ __device__ __forceinline__ Rows rows_of(const Params& p, int64_t row)
         }
     }
     return r;
+}
+
+// The slot of a workgroup, and which of the slot's it is.  Slots that may find no adapter come
+// last: the first ones' work spreads over all XCDs, whatever the number of slots is a multiple of.
+struct Place {
+    int slot;
+    uint32_t rest;
+};
+__device__ __forceinline__ Place place_of(const Params& p)
+{
+    const uint32_t per = gridDim.x / p.slots;
+    return Place{(int)(blockIdx.x / per), blockIdx.x % per};
+}
+
+// The same with all of a slot's workgroups on one XCD, since each reads all of the slot's A (32 rows of
+// 24 adapters: 8.0 us, 10.4 with them spread).  Fewer slots than XCDs are spread.
+__device__ __forceinline__ Place place_near(const Params& p)
+{
+    if (p.slots < 8) return place_of(p);
+    const uint32_t per = gridDim.x / ((p.slots + 7) / 8 * 8), on = blockIdx.x / 8;
+    return Place{(int)(on / per * 8 + blockIdx.x % 8), on % per};
 }
 
 // Lane n of the result holds the n-th row of a set of rows (the others behind them).
@@ -193,17 +216,17 @@ __device__ __forceinline__ void down_rows(const Params& p, int ad, int rank0, in
     }
 }
 
-// h = A x for a tile of 64 rows, 16 RT ranks and the adapters of one slot.
+// h = A x for a tile of rows, 16 RT ranks and the adapters of one slot.
 template <typename T, int RT> __global__ __launch_bounds__(kDownWaves * 64, RT <= 2 ? 3 : 2) void adapters_down_kernel(Params p)
 {
     constexpr int KW = kDownWaves;
     __shared__ __align__(16) u4_t lds[KW * 16 * (4 + RT) * 8];
     static_assert(sizeof(lds) >= sizeof(float) * KW * 64 * 20, "the sums fit");
     const int lane = threadIdx.x & 63;
-    const int slot = blockIdx.x % p.slots, split = blockIdx.x / p.slots % p.splits;
-    const int rank0 = blockIdx.x / p.slots / p.splits % p.rblocks * (16 * RT);
-    const int64_t row0 = (int64_t)(blockIdx.x / p.slots / p.splits / p.rblocks) * 64;
-    const Rows mine = rows_of(p, row0 + lane);
+    const Place at = place_of(p);
+    const int slot = at.slot, split = at.rest % p.splits, rank0 = at.rest / p.splits % p.rblocks * (16 * RT);
+    const int64_t row0 = (int64_t)(at.rest / p.splits / p.rblocks) * p.tile;
+    const Rows mine = rows_of(p, row0, lane);
     for_adapters(mine, slot, p.slots, [&](int ad, int rank, uint64_t same) {
         const int order = gathered(same, lane), rows = __builtin_popcountll(same);
         const int here = rank - rank0 < 16 * RT ? rank - rank0 : 16 * RT;
@@ -404,38 +427,57 @@ template <typename T, int RC> __global__ __launch_bounds__(kUpWaves * 64, RC <= 
     __shared__ __align__(16) float turn[kUpWaves][16][68];
 
     const int lane = threadIdx.x & 63, wave = uniform(threadIdx.x >> 6);
-    const int slot = blockIdx.x % p.slots;
-    const int64_t n0 = ((int64_t)(blockIdx.x / p.slots % p.nblocks) * kUpWaves + wave) * 64;
-    const int64_t row0 = (int64_t)(blockIdx.x / p.slots / p.nblocks) * 64;
-    const Rows mine = rows_of(p, row0 + lane);
+    const Place at = place_of(p);
+    const int slot = at.slot;
+    const int64_t n0 = ((int64_t)(at.rest % p.nblocks) * kUpWaves + wave) * 64;
+    const int64_t row0 = (int64_t)(at.rest / p.nblocks) * p.tile;
+    const Rows mine = rows_of(p, row0, lane);
     Columns<T, RC> w(p, row0, n0);
-    const uint64_t none = __builtin_amdgcn_ballot_w64(mine.adapter < 0 && row0 + lane < p.m);
+    const uint64_t none = __builtin_amdgcn_ballot_w64(mine.adapter < 0 && mine.there);
     if (slot == 0) w.copy(none);
     for_adapters(mine, slot, p.slots, [&](int ad, int rank, uint64_t same) {
         const int order = gathered(same, lane), rows = __builtin_popcountll(same);
         w.load_b(ad, rank);
-        // h: four ranks to a thread
-        auto prepare = [&]() {
+        // h: N times four ranks to a thread, some splits of each at once.  Where there is nothing to read the
+        // first of h stands in, so that no load waits for a branch
+        auto prepare = [&](auto count) {
+            constexpr int N = decltype(count)::value, AT_ONCE = N >= 8 ? (sizeof(T) == 4 ? 1 : 2) : N >= 2 ? 4 : 8;
+            const f4_t zero = {0.0f, 0.0f, 0.0f, 0.0f};
+            f4_t v[N];
+            const float* h[N];
+            bool real[N];
+            const int64_t step = p.m * p.pitch;
+#pragma unroll
+            for (int i = 0; i < N; ++i) {
+                const int at = threadIdx.x + i * kUpWaves * 64, n = at / TH, r = at % TH * 4;
+                const int row = __shfl(order, n & 63);
+                real[i] = n < rows && r < rank;
+                h[i] = real[i] ? p.h + (row0 + row) * p.pitch + r : p.h;
+                v[i] = zero;
+            }
+            int s = 0;
+            for (; s + AT_ONCE <= p.splits; s += AT_ONCE) {
+                f4_t q[AT_ONCE][N];
+#pragma unroll
+                for (int k = 0; k < AT_ONCE; ++k)
+#pragma unroll
+                    for (int i = 0; i < N; ++i) q[k][i] = *reinterpret_cast<const f4_t*>(h[i] + (s + k) * step);
+#pragma unroll
+                for (int k = 0; k < AT_ONCE; ++k)
+#pragma unroll
+                    for (int i = 0; i < N; ++i) v[i] += q[k][i];
+            }
+            for (; s < p.splits; ++s)
+#pragma unroll
+                for (int i = 0; i < N; ++i) v[i] += *reinterpret_cast<const f4_t*>(h[i] + s * step);
             __syncthreads();                            // the last adapter's has been read
-            for (int at = threadIdx.x; at < (rows + 15) / 16 * 16 * TH; at += kUpWaves * 64) {
-                const int n = at / TH, r = at % TH * 4;
-                const float* h = p.h + (row0 + __shfl(order, n & 63)) * p.pitch + r;
-                f4_t v = {0.0f, 0.0f, 0.0f, 0.0f};
-                if (n < rows && r < rank) {
-                    const int64_t step = p.m * p.pitch;
-                    int s = 0;
-                    for (; s + 4 <= p.splits; s += 4, h += 4 * step) {
-                        f4_t q[4];
 #pragma unroll
-                        for (int k = 0; k < 4; ++k) q[k] = *reinterpret_cast<const f4_t*>(h + k * step);
+            for (int i = 0; i < N; ++i) {
+                const int at = threadIdx.x + i * kUpWaves * 64, n = at / TH, r = at % TH * 4;
+                if (n >= (rows + 15) / 16 * 16) break;
 #pragma unroll
-                        for (int k = 0; k < 4; ++k) v += q[k];
-                    }
-                    for (; s < p.splits; ++s, h += step) v += *reinterpret_cast<const f4_t*>(h);
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) v[i] = r + i < rank ? v[i] : 0.0f;
-                }
-                const float f = O::put(v, n, r, hf);
+                for (int e = 0; e < 4; ++e) v[i][e] = real[i] && r + e < rank ? v[i][e] : 0.0f;
+                const float f = O::put(v[i], n, r, hf);
                 if (r == 0) back[n] = f;
             }
             __syncthreads();
@@ -443,10 +485,10 @@ template <typename T, int RC> __global__ __launch_bounds__(kUpWaves * 64, RC <= 
         if (rows <= 16) {
             // a few rows wait for their loads: base on its way beside h.  (More have no registers for it.)
             const auto in = w.template request<1>(order, rows, 0);
-            prepare();
+            prepare(std::integral_constant<int, TH < 16 ? 1 : TH / 16>());
             if (w.busy) w.finish(in, rows, 0, hf, back, turn[wave]);
         } else {
-            prepare();
+            prepare(std::integral_constant<int, TH / 4>());
             if (!w.busy) return;
 #pragma unroll
             for (int g = 0; g < 4; g += PRE)
@@ -470,13 +512,14 @@ template <typename T, int RC> __global__ __launch_bounds__(kOneWaves * 64, 2) vo
     static_assert(sizeof(lds) >= sizeof(float) * KW * 16 * 68, "a tile of every wave fits");
 
     const int lane = threadIdx.x & 63, wave = uniform(threadIdx.x >> 6);
-    const int slot = blockIdx.x % p.slots;
-    const int64_t n0 = ((int64_t)(blockIdx.x / p.slots % p.nblocks) * KW + wave) * 64;
-    const int64_t row0 = (int64_t)(blockIdx.x / p.slots / p.nblocks) * 32;
-    const bool there = lane < 32 && row0 + lane < p.m;
-    const Rows mine = rows_of(p, there ? row0 + lane : p.m);
+    const Place at = place_near(p);
+    const int slot = at.slot;
+    if (slot >= p.slots) return;
+    const int64_t n0 = ((int64_t)(at.rest % p.nblocks) * KW + wave) * 64;
+    const int64_t row0 = (int64_t)(at.rest / p.nblocks) * p.tile;   // at most 32
+    const Rows mine = rows_of(p, row0, lane);
     Columns<T, RC> w(p, row0, n0);
-    const uint64_t none = __builtin_amdgcn_ballot_w64(there && mine.adapter < 0);
+    const uint64_t none = __builtin_amdgcn_ballot_w64(mine.adapter < 0 && mine.there);
     if (slot == 0) w.copy(none);
     for_adapters(mine, slot, p.slots, [&](int ad, int rank, uint64_t same) {
         const int order = gathered(same, lane), rows = __builtin_popcountll(same);
@@ -507,10 +550,11 @@ template <typename T, int RC> __global__ __launch_bounds__(kOneWaves * 64, 2) vo
 template <typename T> hipError_t launch_down(Params p, const Plan& c, hipStream_t s)
 {
     p.slots = c.down_slots;
-    p.rblocks = (p.rank + 63) / 64;
-    const dim3 grid((unsigned)(ceil_div(p.m, 64) * p.splits * p.slots * p.rblocks)), block(kDownWaves * 64);
-    if (p.rank <= 16) adapters_down_kernel<T, 1><<<grid, block, 0, s>>>(p);
-    else if (p.rank <= 32) adapters_down_kernel<T, 2><<<grid, block, 0, s>>>(p);
+    p.tile = c.down_tile;
+    p.rblocks = (p.rank + 16 * c.down_ranks - 1) / (16 * c.down_ranks);
+    const dim3 grid((unsigned)(ceil_div(p.m, p.tile) * p.splits * p.slots * p.rblocks)), block(kDownWaves * 64);
+    if (c.down_ranks == 1) adapters_down_kernel<T, 1><<<grid, block, 0, s>>>(p);
+    else if (c.down_ranks == 2) adapters_down_kernel<T, 2><<<grid, block, 0, s>>>(p);
     else adapters_down_kernel<T, 4><<<grid, block, 0, s>>>(p);
     return hipGetLastError();
 }
@@ -518,8 +562,9 @@ template <typename T> hipError_t launch_down(Params p, const Plan& c, hipStream_
 template <typename T> hipError_t launch_up(Params p, const Plan& c, hipStream_t s)
 {
     p.slots = c.up_slots;
+    p.tile = c.up_tile;
     p.nblocks = (int)ceil_div(p.n, 64 * kUpWaves);
-    const dim3 grid((unsigned)(ceil_div(p.m, 64) * p.nblocks * p.slots)), block(kUpWaves * 64);
+    const dim3 grid((unsigned)(ceil_div(p.m, p.tile) * p.nblocks * p.slots)), block(kUpWaves * 64);
     if (p.rank <= 16) adapters_up_kernel<T, 0><<<grid, block, 0, s>>>(p);
     else if (p.rank <= 32) adapters_up_kernel<T, 1><<<grid, block, 0, s>>>(p);
     else if (p.rank <= 64) adapters_up_kernel<T, 2><<<grid, block, 0, s>>>(p);
@@ -530,9 +575,11 @@ template <typename T> hipError_t launch_up(Params p, const Plan& c, hipStream_t 
 template <typename T> hipError_t launch_one(Params p, const Plan& c, hipStream_t s)
 {
     p.slots = c.one_slots;
+    p.tile = 32;
     p.k_per = p.k;
     p.nblocks = (int)ceil_div(p.n, 64 * kOneWaves);
-    const dim3 grid((unsigned)(ceil_div(p.m, 32) * p.nblocks * p.slots)), block(kOneWaves * 64);
+    const int slots = p.slots < 8 ? p.slots : (p.slots + 7) / 8 * 8;
+    const dim3 grid((unsigned)(ceil_div(p.m, 32) * p.nblocks * slots)), block(kOneWaves * 64);
     if (p.rank <= 16) adapters_one_kernel<T, 0><<<grid, block, 0, s>>>(p);
     else adapters_one_kernel<T, 1><<<grid, block, 0, s>>>(p);
     return hipGetLastError();

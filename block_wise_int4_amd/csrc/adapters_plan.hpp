@@ -16,8 +16,9 @@ struct Plan {
     bool one;                        // both products in one launch
     int splits;                      // workgroups that share k
     int64_t k_per;                   // k of a split, a multiple of a step
-    int one_slots;                   // workgroups that share the adapters of 32 rows,
-    int down_slots, up_slots;        // and of 64
+    int down_tile, up_tile;          // rows of a workgroup: 16, 32, 64
+    int down_ranks;                  // 16-rank tiles of one: 1, 2, 4
+    int one_slots, down_slots, up_slots;   // workgroups that share the adapters of its rows
     int pitch;                       // floats of a row between the products
 };
 
@@ -42,20 +43,42 @@ inline Plan plan_of(int64_t m, int64_t n, int64_t k, int rank, int count, int f1
         const int64_t d = m < rows ? m : rows;
         return count < 1 ? (int64_t)1 : d < count ? d : count;
     };
-    // one launch while a CU has one adapter to see to and reads its A quickly (one token, k = n = 4096,
-    // rank 16: 6.6 us against 7.0; 32 rows of 24 adapters 8.5 against 9.2, with k = 1024 columns 7.5
-    // against 8.5; n = 11008, 22 sets of columns, 14.7 against 11.2; fp32, 256 KB, 13.4 against 11.5).  A call of one
-    // launch also spares its caller an enqueue.
+    // One launch while a CU has one adapter to see to and reads its A quickly: from 64 KB on it takes as long as
+    // two, and few rows still gain the enqueue that their caller is spared (k = n = 4096, rank 16, in a graph and
+    // call by call: one token 6.8 and 7.0 us against 7.0 and 9.6, 32 rows of 24 adapters 8.5 and 7.6 against 8.8 and 11.0,
+    // 32 rows of one 9.0 against 7.3; k = n = 1024 5.9 against 8.1; 575 fp32 rows, 131 KB, 15.1 against 13.2).
     const int64_t sets = ceil_div(m, 32) * ceil_div(n, 64 * kOneWaves);
-    c.one = rank <= 32 && k * c.pitch * (f16 ? 2 : 4) <= 144 * 1024 && sets * distinct(32) <= 256;
-    // a workgroup without an adapter costs a quarter of a microsecond of its CU: few where there are many tiles
+    c.one = rank <= 32 && k * c.pitch * (f16 ? 2 : 4) <= (m <= 64 ? 144 : 64) * 1024 && sets * distinct(32) <= 256;
     auto slots = [&](int64_t workgroups, int64_t most, int64_t rows) {
         const int64_t s = most / workgroups < 1 ? 1 : most / workgroups;
         return (int)(s < distinct(rows) ? s : distinct(rows));
     };
     c.one_slots = slots(sets, 256, 32);
-    c.down_slots = slots(tiles * c.splits, 1024, 64);
-    c.up_slots = slots(tiles * ceil_div(n, 64 * kUpWaves), 1024, 64);
+    // slots for the workgroups that the CUs hold at once (512 rows of 64 adapters, k = n = 4096: rank 16
+    // 38 us with 1024, 46 with 512; rank 64 75 with 512, 81 with 1024)
+    const int64_t held = rank <= 32 ? 1024 : 512;
+    // 64 rows read A and B least often; with fewer workgroups than keep the memory busy 32 are
+    // better (1000 rows of one adapter, k = n = 4096: second product 7.8 and 6.9 us, 8416 rows 83
+    // and 88; first, 3100 rows 10.8 and 9.0, 8416 rows 18.0 and 19.9), and 16, then fewer ranks, until
+    // there is one for every CU (121 rows, rank 64 in fp32: first 18 and 6.5 us, second 17 and 8)
+    c.down_ranks = rank <= 16 ? 1 : rank <= 32 ? 2 : 4;
+    auto down = [&] { return ceil_div(m, c.down_tile) * c.splits * ceil_div(rank, 16 * c.down_ranks); };
+    c.down_tile = 64;
+    if (down() <= 384) c.down_tile = 32;
+    c.down_slots = slots(down(), held, c.down_tile);
+    if (down() * c.down_slots < 256) {
+        c.down_tile = 16;
+        c.down_slots = slots(down(), held, c.down_tile);
+    }
+    while (c.down_ranks > 1 && down() * c.down_slots < 256) c.down_ranks /= 2;
+    auto up = [&] { return ceil_div(m, c.up_tile) * ceil_div(n, 64 * kUpWaves); };
+    c.up_tile = 64;
+    if (up() < 1024) c.up_tile = 32;
+    c.up_slots = slots(up(), held, c.up_tile);
+    if (up() * c.up_slots < 256) {
+        c.up_tile = 16;
+        c.up_slots = slots(up(), held, c.up_tile);
+    }
     return c;
 }
 

@@ -100,13 +100,15 @@ int main()
         if (m * n >= (int64_t)1 << 37) m = ((int64_t)1 << 37) / n - 1;
         const int rank = (int)mild(128), f16 = (int)(next() % 2), count = (int)(next() % 20 ? mild(2000) : 0);
         const mnb::adapters::Plan c = mnb::adapters::plan_of(m, n, k, rank, count, f16);
-        const int64_t tiles = (m + 63) / 64, blocks = (n + 255) / 256;
+        const int64_t blocks = (n + 255) / 256, ranks = 16 * c.down_ranks;
+        expect((c.down_tile == 16 || c.down_tile == 32 || c.down_tile == 64) && (c.up_tile == 16 || c.up_tile == 32 || c.up_tile == 64), "tiles");
+        expect(c.down_ranks == 1 || c.down_ranks == 2 || c.down_ranks == 4, "ranks");
         expect(c.pitch >= rank && c.pitch <= 128 && c.pitch % 16 == 0, "pitch");
         expect(c.splits >= 1 && c.splits <= 8 && c.k_per % (f16 ? 64 : 32) == 0, "splits");
         expect(c.k_per * c.splits >= k && c.k_per * (c.splits - 1) < k, "all of k");
         for (int s : {c.one_slots, c.down_slots, c.up_slots}) expect(s >= 1 && s <= 64 && (s <= count || s == 1) && s <= m, "slots");
-        expect((uint64_t)tiles * c.splits * c.down_slots * ((rank + 63) / 64) * 256 < (uint64_t)1 << 32, "first grid");
-        expect((uint64_t)tiles * blocks * c.up_slots * 256 < (uint64_t)1 << 32, "second grid");
+        expect((uint64_t)((m + c.down_tile - 1) / c.down_tile) * c.splits * c.down_slots * ((rank + ranks - 1) / ranks) * 256 < (uint64_t)1 << 32, "first grid");
+        expect((uint64_t)((m + c.up_tile - 1) / c.up_tile) * blocks * c.up_slots * 256 < (uint64_t)1 << 32, "second grid");
         if (c.one) expect((m + 31) / 32 * ((n + 511) / 512) * c.one_slots <= 256 && rank <= 32, "one launch");
     }
     std::printf("%s: %d failures\n", failures ? "FAILED" : "ok", failures);
