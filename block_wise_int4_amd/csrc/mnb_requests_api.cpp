@@ -87,6 +87,9 @@ mnb_status mnb_adapters_add(const mnb_adapter_desc* d, const void* a, const void
     MNB_TRY(check_stride(y_stride, d->n, m, "y_stride"));
     if (base) MNB_TRY(check_stride(base_stride, d->n, m, "base_stride"));
     if (m == 0 || d->n == 0) return ok("noop");
+    if (base && base == y && base_stride != y_stride && m > 1)
+        return fail(MNB_ERR_INVALID_ARGUMENT, "y is base, but their strides differ (%lld, %lld)", (long long)y_stride,
+                    (long long)base_stride);
     const uintptr_t elem = d->dtype == MNB_F16 ? 2 : 4;
     if (d->count > 0) {
         MNB_TRY(check_ptr(a, 16, "a"));

@@ -29,7 +29,7 @@ def verify(**kw):
     dict(dt=2), dict(dt=-1), dict(reserved=1), dict(n=-1), dict(k=0), dict(rank=0), dict(count=-1), dict(m=-1), dict(xs=127),
     dict(bs=95), dict(ys=95), dict(xs=1 << 62), dict(ys=1 << 62), dict(bs=1 << 62), dict(a=None), dict(b=None),
     dict(ad=None), dict(x=None), dict(y=None), dict(a=P + 8), dict(b=P + 8), dict(sc=P + 2), dict(ranks=P + 1),
-    dict(ad=P + 2), dict(x=P + 1), dict(base=P + 1), dict(y=P + 1), dict(dt=F32, x=P + 2), dict(rank=65, ws=None),
+    dict(ad=P + 2), dict(x=P + 1), dict(base=P + 1), dict(y=P + 1), dict(dt=F32, x=P + 2), dict(bs=97), dict(rank=65, ws=None),
     dict(rank=65, ws=P + 16), dict(rank=65, wb=16)])
 def test_adapters_refuse(kw):
     _refused(INVALID, add, **kw)
