@@ -56,6 +56,7 @@ CASES = [  # rows of the sequences, vocabulary
     ([1], 1), ([2], 2), ([3, 1], 5), ([1, 5, 0, 2], 100), ([4], 4095), ([4, 4], 4096), ([9, 1, 3], 4097), ([6] * 20, 1000),
     ([3, 2], 1023), ([3, 2], 1025), ([2], 65537),
     ([5, 0, 0, 7], 50257), ([70, 130], 33), ([3], 200001), ([0, 0], 10), ([2] * 300, 40),
+    ([1, 4, 2], 16385), ([3], 32769), ([1] * 255 + [0, 2, 3], 33000),
 ]
 
 
