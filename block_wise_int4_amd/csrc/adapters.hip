@@ -3,7 +3,32 @@
 //   y[t] = base[t] + s_a B_a (A_a x[t]),   a = adapter[t],
 //
 // A_a [rank, k], B_a [n, rank]; rows of a call may have any adapters in any
-// order.  Two kernels: h = A x in fp32, then y = base + s B h.
+// order.  Two products, h = A x in fp32, then y = base + s B h, in two launches, or in one for few
+// rows (every workgroup then forms the h of its adapters by itself).
+//
+// What bounds it: x, base and y read and written once, for few rows A and B of the adapters that
+// occur; the products are small (rank 32: 32 operations a byte).  So both kernels are built
+// around their loads.
+//
+// Rows are gathered by adapter inside a tile of 16, 32 or 64 (a lane a row: a ballot names the rows of an
+// adapter, a move between lanes lists them), so the matrix cores see 16 rows of one adapter where
+// the tile has them, in whatever order they came, and nothing is sorted beforehand.  The adapters of a
+// tile are shared out to `slots` workgroups; a slot takes every slots-th of the tile's adapters.
+//
+// First product: the waves share k.  A load takes 128 neighbouring bytes of 8 rows and the
+// operands of v_mfma_f32_16x16x32_f16 form in the wave's own LDS (loaded as operands, each of a load's
+// lanes goes to another row, at 16 bytes a cycle and CU: 8416 rows, k = 4096, rank 32 18 us, 60 so).
+// Second product: h is prepared once a workgroup, as operands in LDS: in fp16 calls as two fp16 parts of the row
+// scaled by a power of two, 22 bits, so that h is not rounded to 16 bits (at rank 16 and below one product takes both
+// parts); in fp32 calls as it is, for v_mfma_f32_16x16x4f32.  The result turns through
+// LDS so that base is read and y is written 128 bytes or more of a row at a time.
+//
+// Measured, call by call.  k = n = 4096, rank 16, fp16: one token 7.0 us, 32 tokens of 24 adapters 8.0 (6.2
+// MB asked for), both one launch and the time of its chain: adapter, rank, A and x, two meetings in LDS, base and
+// y.  8416 rows, k = 4096, n = 11008, rank 32: 92 us for 443 MB, 4.8 TB/s where a large copy moves 5.07;
+// the first kernel 25 of them (69 MB, beside the last call's y on its way out), the second 75.  4000 rows, k = n = 4096:
+// rank 16 27 us, 32 28, 64 40, 128 50 (floor 20): at the higher ranks h comes from the L2 once for
+// every 512 columns.  In fp32 rank 64 takes 78 us (floor 39): its products run at a sixteenth of the fp16 rate.
 #include <type_traits>
 
 #include "adapters_plan.hpp"
@@ -27,7 +52,7 @@ struct Params {
     void* y;
     float* h;                         // [splits][m][pitch]
     int64_t m, n, k, x_stride, base_stride, y_stride, k_per;
-    int rank, count, splits, slots, pitch, rblocks, nblocks, tile;
+    int rank, count, splits, slots, pitch, rblocks, nblocks, blocks, tile;
 };
 
 __device__ __forceinline__ f4_t mfma16(const h8_t& a, const h8_t& b, const f4_t& c)
@@ -318,9 +343,8 @@ template <typename T, int RC> struct Columns {
     V b[O::NC][4];
     float scale;
 
-    __device__ __forceinline__ Columns(const Params& q, int64_t row0, int64_t first) : p(q), n0(first)
+    __device__ __forceinline__ Columns(const Params& q, int64_t row0, int64_t first, int of) : p(q), n0(first), lane(of)
     {
-        lane = threadIdx.x & 63;
         c0 = lane % LANES * E;
         r0 = lane / LANES;
         left = p.n - n0 - c0;
@@ -330,7 +354,7 @@ template <typename T, int RC> struct Columns {
     }
     __device__ __forceinline__ void put(T* at, const V& v) const
     {
-        if (left >= E) store(at, v);
+        if (left >= E) store_through(at, v);            // y is read by no one here (185 MB 107 us kept, 97 so)
         else
 #pragma unroll
             for (int e = 0; e < E; ++e)
@@ -368,15 +392,22 @@ template <typename T, int RC> struct Columns {
     template <int N> __device__ __forceinline__ Base<T, N> request(int order, int rows, int g) const
     {
         Base<T, N> in;
+        auto each = [&](auto from) {
 #pragma unroll
-        for (int u = 0; u < N; ++u)
+            for (int u = 0; u < N; ++u)
 #pragma unroll
-            for (int i = 0; i < PIECES; ++i) {
-                const int n = 16 * (g + u) + i * STEP + r0;
-                in.row[u][i] = __shfl(order, n & 63);
-                in.v[u][i] = V{};
-                if (base && busy && n < rows) in.v[u][i] = load_some(base + in.row[u][i] * p.base_stride, left);
-            }
+                for (int i = 0; i < PIECES; ++i) {
+                    const int n = 16 * (g + u) + i * STEP + r0;
+                    in.row[u][i] = __shfl(order, n & 63);
+                    in.v[u][i] = V{};
+                    if (base && busy && n < rows) in.v[u][i] = from(base + in.row[u][i] * p.base_stride);
+                }
+        };
+        // A base past half the last cache is not there from the projection before, and kept for no one
+        // (185 MB 97.3 and 94.8 us; 16 MB 15.3 and 17.2)
+        if (p.m * p.n * (int64_t)sizeof(T) >= (int64_t)128 << 20)
+            each([&](const T* at) { return left >= E ? load_once(at) : load_some(at, left); });
+        else each([&](const T* at) { return load_some(at, left); });
         return in;
     }
     template <int N>
@@ -417,7 +448,9 @@ template <typename T, int RC> struct Columns {
     }
 };
 
-template <typename T, int RC> __global__ __launch_bounds__(kUpWaves * 64, RC <= 1 ? 4 : 2) void adapters_up_kernel(Params p)
+// MORE: further blocks of 256 columns with the same h, for ranks whose h is long to read.
+template <typename T, int RC, bool MORE>
+__global__ __launch_bounds__(kUpWaves * 64, RC <= 1 ? 4 : 2) void adapters_up_kernel(Params p)
 {
     typedef Up<T, RC> O;
     constexpr int TH = O::PITCH / 4;                    // lanes to a row of h
@@ -429,15 +462,18 @@ template <typename T, int RC> __global__ __launch_bounds__(kUpWaves * 64, RC <= 
     const int lane = threadIdx.x & 63, wave = uniform(threadIdx.x >> 6);
     const Place at = place_of(p);
     const int slot = at.slot;
-    const int64_t n0 = ((int64_t)(at.rest % p.nblocks) * kUpWaves + wave) * 64;
+    const int blocks = MORE ? p.blocks : 1;
+    const int64_t n0 = ((int64_t)(at.rest % p.nblocks) * blocks * kUpWaves + wave) * 64;
     const int64_t row0 = (int64_t)(at.rest / p.nblocks) * p.tile;
     const Rows mine = rows_of(p, row0, lane);
-    Columns<T, RC> w(p, row0, n0);
     const uint64_t none = __builtin_amdgcn_ballot_w64(mine.adapter < 0 && mine.there);
+    Columns<T, RC> w(p, row0, n0, lane);
     if (slot == 0) w.copy(none);
+    if (MORE && slot == 0)
+        for (int block = 1; block < blocks; ++block)
+            Columns<T, RC>(p, row0, n0 + (int64_t)block * (64 * kUpWaves), lane).copy(none);
     for_adapters(mine, slot, p.slots, [&](int ad, int rank, uint64_t same) {
         const int order = gathered(same, lane), rows = __builtin_popcountll(same);
-        w.load_b(ad, rank);
         // h: N times four ranks to a thread, some splits of each at once.  Where there is nothing to read the
         // first of h stands in, so that no load waits for a branch
         auto prepare = [&](auto count) {
@@ -482,18 +518,29 @@ template <typename T, int RC> __global__ __launch_bounds__(kUpWaves * 64, RC <= 
             }
             __syncthreads();
         };
-        if (rows <= 16) {
-            // a few rows wait for their loads: base on its way beside h.  (More have no registers for it.)
-            const auto in = w.template request<1>(order, rows, 0);
-            prepare(std::integral_constant<int, TH < 16 ? 1 : TH / 16>());
-            if (w.busy) w.finish(in, rows, 0, hf, back, turn[wave]);
-        } else {
-            prepare(std::integral_constant<int, TH / 4>());
-            if (!w.busy) return;
+        auto columns = [&](Columns<T, RC>& w, bool first) {
+            if (first || w.busy) w.load_b(ad, rank);
+            if (rows <= 16) {
+                // a few rows wait for their loads: base on its way beside h.  (More have no registers for it.)
+                const auto in = w.template request<1>(order, rows, 0);
+                if (first) prepare(std::integral_constant<int, TH < 16 ? 1 : TH / 16>());
+                if (w.busy) w.finish(in, rows, 0, hf, back, turn[wave]);
+            } else {
+                if (first) prepare(std::integral_constant<int, TH / 4>());
+                if (!w.busy) return;
 #pragma unroll
-            for (int g = 0; g < 4; g += PRE)
-                if (16 * g < rows) w.finish(w.template request<PRE>(order, rows, g), rows, g, hf, back, turn[wave]);
-        }
+                for (int g = 0; g < 4; g += PRE)
+                    if (16 * g < rows) w.finish(w.template request<PRE>(order, rows, g), rows, g, hf, back, turn[wave]);
+            }
+        };
+        if constexpr (!MORE) columns(w, true);
+        else
+            for (int block = 0; block < blocks; ++block) {
+                int again = lane;
+                asm volatile("" : "+v"(again));         // the lanes' addresses stay in no registers from block to block
+                Columns<T, RC> next(p, row0, n0 + (int64_t)block * (64 * kUpWaves), again);
+                columns(next, block == 0);
+            }
     });
 }
 
@@ -518,7 +565,7 @@ template <typename T, int RC> __global__ __launch_bounds__(kOneWaves * 64, 2) vo
     const int64_t n0 = ((int64_t)(at.rest % p.nblocks) * KW + wave) * 64;
     const int64_t row0 = (int64_t)(at.rest / p.nblocks) * p.tile;   // at most 32
     const Rows mine = rows_of(p, row0, lane);
-    Columns<T, RC> w(p, row0, n0);
+    Columns<T, RC> w(p, row0, n0, lane);
     const uint64_t none = __builtin_amdgcn_ballot_w64(mine.adapter < 0 && mine.there);
     if (slot == 0) w.copy(none);
     for_adapters(mine, slot, p.slots, [&](int ad, int rank, uint64_t same) {
@@ -563,12 +610,15 @@ template <typename T> hipError_t launch_up(Params p, const Plan& c, hipStream_t 
 {
     p.slots = c.up_slots;
     p.tile = c.up_tile;
-    p.nblocks = (int)ceil_div(p.n, 64 * kUpWaves);
+    p.blocks = c.up_blocks;
+    p.nblocks = (int)ceil_div(p.n, 64 * kUpWaves * p.blocks);
     const dim3 grid((unsigned)(ceil_div(p.m, p.tile) * p.nblocks * p.slots)), block(kUpWaves * 64);
-    if (p.rank <= 16) adapters_up_kernel<T, 0><<<grid, block, 0, s>>>(p);
-    else if (p.rank <= 32) adapters_up_kernel<T, 1><<<grid, block, 0, s>>>(p);
-    else if (p.rank <= 64) adapters_up_kernel<T, 2><<<grid, block, 0, s>>>(p);
-    else adapters_up_kernel<T, 4><<<grid, block, 0, s>>>(p);
+    if (p.rank <= 16) adapters_up_kernel<T, 0, false><<<grid, block, 0, s>>>(p);
+    else if (p.rank <= 32) adapters_up_kernel<T, 1, false><<<grid, block, 0, s>>>(p);
+    else if (p.rank <= 64 && p.blocks == 1) adapters_up_kernel<T, 2, false><<<grid, block, 0, s>>>(p);
+    else if (p.rank <= 64) adapters_up_kernel<T, 2, true><<<grid, block, 0, s>>>(p);
+    else if (p.blocks == 1) adapters_up_kernel<T, 4, false><<<grid, block, 0, s>>>(p);
+    else adapters_up_kernel<T, 4, true><<<grid, block, 0, s>>>(p);
     return hipGetLastError();
 }
 

@@ -19,6 +19,7 @@ struct Plan {
     int down_tile, up_tile;          // rows of a workgroup: 16, 32, 64
     int down_ranks;                  // 16-rank tiles of one: 1, 2, 4
     int one_slots, down_slots, up_slots;   // workgroups that share the adapters of its rows
+    int up_blocks;                   // 256-column blocks of a workgroup of the second product
     int pitch;                       // floats of a row between the products
 };
 
@@ -36,6 +37,12 @@ inline Plan plan_of(int64_t m, int64_t n, int64_t k, int rank, int count, int f1
     int64_t splits = ceil_div(512, tiles);
     splits = splits > most ? most : splits;
     splits = splits > 8 ? 8 : splits;
+    // every 256 columns of the second product read all of h: past 48 MB that costs more than the splits
+    // gain (4000 rows, k = n = 4096, fp16: rank 32 in eight 31.3 us, in four 28.3; rank 64 46.4 and 41.3, in two
+    // 45.1; rank 128 74.4 and 61.1, in two 56.7; 1000 fp32 rows of rank 64, 33 MB, 26.4 and 30.0)
+    const int64_t fewest = rank > 64 ? 2 : 4;
+    while (splits > fewest && m * splits * c.pitch * 4 * ceil_div(n, 64 * kUpWaves) > ((int64_t)48 << 20))
+        splits = (splits + 1) / 2 < fewest ? fewest : (splits + 1) / 2;
     c.k_per = ceil_div(ceil_div(k, splits), step) * step;
     c.splits = (int)ceil_div(k, c.k_per);
     // adapters that `rows` rows can have
@@ -79,6 +86,10 @@ inline Plan plan_of(int64_t m, int64_t n, int64_t k, int rank, int count, int f1
         c.up_tile = 16;
         c.up_slots = slots(up(), held, c.up_tile);
     }
+    // At ranks above 32 h is long to read: two blocks of columns a workgroup where there is more than a
+    // round of workgroups, two a CU (4000 rows, rank 128: 57 us and 50; 1500 rows 29.0 and 27.8; rank 64 41.3
+    // and 39.7; 1000 rows, 512 workgroups, 17.3 and 20.1.  Rank 32 gains nothing)
+    c.up_blocks = rank > 32 && up() * c.up_slots > 512 ? 2 : 1;
     return c;
 }
 

@@ -25,6 +25,17 @@ template <typename T> __device__ __forceinline__ void store(T* p, const typename
 {
     *reinterpret_cast<typename Vec<T>::raw*>(p) = __builtin_bit_cast(u4_t, v);
 }
+// The same of memory that no one reads again soon: nothing is kept in the caches.
+template <typename T> __device__ __forceinline__ typename Vec<T>::type load_once(const T* p)
+{
+    return __builtin_bit_cast(typename Vec<T>::type,
+                              (u4_t)__builtin_nontemporal_load(reinterpret_cast<const typename Vec<T>::raw*>(p)));
+}
+template <typename T> __device__ __forceinline__ void store_through(T* p, const typename Vec<T>::type& v)
+{
+    __builtin_nontemporal_store((typename Vec<T>::raw)__builtin_bit_cast(u4_t, v),
+                                reinterpret_cast<typename Vec<T>::raw*>(p));
+}
 // The first `valid` of them, zeros behind.
 template <typename T> __device__ __forceinline__ typename Vec<T>::type load_some(const T* p, int64_t valid)
 {

@@ -60,6 +60,8 @@ SIZES = [  # m, k, n, rank, count
     # two launches: many sets of rows and adapters, or ranks past 64
     (800, 130, 70, 16, 200), (1030, 200, 321, 24, 40), (1000, 513, 65, 33, 64), (830, 2100, 40, 9, 64), (70, 300, 60, 100, 9),
     (3, 5000, 200, 128, 3), (2100, 64, 300, 8, 5), (33, 600, 16400, 5, 33),
+    # several blocks of columns a workgroup, the last one's missing
+    (130, 64, 32800, 40, 6), (600, 72, 8200, 128, 3), (50, 100, 66000, 64, 20),
 ]
 
 
@@ -74,6 +76,19 @@ def test_against_the_oracle(mnb, size, order, dt):
     if order == "grouped":
         adapter = np.sort(adapter)
     check(mnb, a, b, scales, ranks, adapter, x, base)
+
+
+@pytest.mark.parametrize("size", [(8193, 8193, "f16"), (4097, 8193, "f32")])
+def test_base_and_output_past_the_caches(mnb, size):
+    m, n, dt = size
+    rng = np.random.default_rng((969, m))
+    a, b, x, base, scales, _ = operands(rng, m, 24, n, 3, 4, dt)
+    adapter = rng.integers(-1, 4, m)
+    got = G.host(run(mnb, a, b, scales, None, adapter, x, base))
+    for i in range(0, m, 1000):                        # the definition, some rows at a time
+        rows = slice(i, i + 1000)
+        w, tol = o.adapters(a, b, scales, None, adapter[rows], x[rows], base[rows])
+        G.assert_within(got[rows], w, None, "adapters", bound=tol)
 
 
 @pytest.mark.parametrize("dt", ["f16", "f32"])
