@@ -24,11 +24,11 @@
 // LDS so that base is read and y is written 128 bytes or more of a row at a time.
 //
 // Measured, call by call.  k = n = 4096, rank 16, fp16: one token 7.0 us, 32 tokens of 24 adapters 8.0 (6.2
-// MB asked for), both one launch and the time of its chain: adapter, rank, A and x, two meetings in LDS, base and
-// y.  8416 rows, k = 4096, n = 11008, rank 32: 92 us for 443 MB, 4.8 TB/s where a large copy moves 5.07;
-// the first kernel 25 of them (69 MB, beside the last call's y on its way out), the second 75.  4000 rows, k = n = 4096:
-// rank 16 27 us, 32 28, 64 40, 128 50 (floor 20): at the higher ranks h comes from the L2 once for
-// every 512 columns.  In fp32 rank 64 takes 78 us (floor 39): its products run at a sixteenth of the fp16 rate.
+// MB asked for), both one launch and the time of its chain: adapter, rank, A and x, two meetings in LDS,
+// base and y.  8416 rows, k = 4096, n = 11008, rank 32: 89 us for 443 MB, 5.0 TB/s where a large copy
+// moves 5.1; the first kernel 17 of them (69 MB).  4000 rows, k = n = 4096: rank 16 27 us, 32 29, 64 42,
+// 128 52 (floor 20): at the higher ranks h comes from the L2 once for every 512 columns.  In fp32 rank 64
+// takes 78 us (floor 39): its products run at a sixteenth of the fp16 rate.
 #include <type_traits>
 
 #include "adapters_plan.hpp"
@@ -533,11 +533,14 @@ __global__ __launch_bounds__(kUpWaves * 64, RC <= 1 ? 4 : 2) void adapters_up_ke
                     if (16 * g < rows) w.finish(w.template request<PRE>(order, rows, g), rows, g, hf, back, turn[wave]);
             }
         };
-        if constexpr (!MORE) columns(w, true);
+        // Where the registers are short the lanes' addresses are formed anew, from a lane's number that the compiler
+        // cannot take for the last one, and not kept from block to block or beside h (rank 32, 8416 rows: 3 registers
+        // spilled and 95.6 us with them kept, none and 91.3 so; 512 rows of 64 adapters of rank 64 75 and 87)
+        if constexpr (!MORE && RC != 1) columns(w, true);
         else
             for (int block = 0; block < blocks; ++block) {
                 int again = lane;
-                asm volatile("" : "+v"(again));         // the lanes' addresses stay in no registers from block to block
+                asm volatile("" : "+v"(again));
                 Columns<T, RC> next(p, row0, n0 + (int64_t)block * (64 * kUpWaves), again);
                 columns(next, block == 0);
             }

@@ -38,8 +38,8 @@ inline Plan plan_of(int64_t m, int64_t n, int64_t k, int rank, int count, int f1
     splits = splits > most ? most : splits;
     splits = splits > 8 ? 8 : splits;
     // every 256 columns of the second product read all of h: past 48 MB that costs more than the splits
-    // gain (4000 rows, k = n = 4096, fp16: rank 32 in eight 31.3 us, in four 28.3; rank 64 46.4 and 41.3, in two
-    // 45.1; rank 128 74.4 and 61.1, in two 56.7; 1000 fp32 rows of rank 64, 33 MB, 26.4 and 30.0)
+    // gain (4000 rows, k = n = 4096, fp16: rank 64 in eight 46.4 us, in four 41.3, in two 45.1;
+    // rank 128 74.4 and 61.1, in two 56.7; 1000 fp32 rows of rank 64, 33 MB, 26.4 and 30.0)
     const int64_t fewest = rank > 64 ? 2 : 4;
     while (splits > fewest && m * splits * c.pitch * 4 * ceil_div(n, 64 * kUpWaves) > ((int64_t)48 << 20))
         splits = (splits + 1) / 2 < fewest ? fewest : (splits + 1) / 2;
