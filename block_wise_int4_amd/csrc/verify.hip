@@ -296,7 +296,7 @@ template <typename T> __global__ __launch_bounds__(kOneThreads) void verify_one_
     }
     const int n = uniform(accepted_of<T>(p, r, lane));
     const Draw<T> d(p, r, n);
-    for (int chunk = wave; chunk < p.chunks; chunk += kOneThreads / 64) {
+    for (int chunk = wave; chunk < p.chunks; chunk += blockDim.x / 64) {
         Chunk<T> c;
         c.load(p, d, chunk, lane);
         const d2_t v = c.sums(d, chunk, lane);
@@ -338,8 +338,10 @@ hipError_t launch_verify(const VerifyArgs& a, hipStream_t stream, const char** v
     const int64_t bytes = (int64_t)p.chunks * kVerifyChunk * (a.f16 ? 2 : 4) * (a.draft ? 2 : 1);
     if ((p.chunks <= 32 && bytes <= 128 * 1024) || (a.batch >= 256 && p.chunks <= verify::kOneChunks)) {
         *variant = "verify_one";
-        if (a.f16) verify::verify_one_kernel<_Float16><<<one, verify::kOneThreads, 0, stream>>>(p);
-        else verify::verify_one_kernel<float><<<one, verify::kOneThreads, 0, stream>>>(p);
+        // a wave a chunk at most, so the grid has 64 batch * chunks < 2^30 threads
+        const int threads = 64 * p.chunks < verify::kOneThreads ? 64 * p.chunks : verify::kOneThreads;
+        if (a.f16) verify::verify_one_kernel<_Float16><<<one, threads, 0, stream>>>(p);
+        else verify::verify_one_kernel<float><<<one, threads, 0, stream>>>(p);
         return hipGetLastError();
     }
     *variant = "verify_drafts";

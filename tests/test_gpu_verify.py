@@ -213,3 +213,20 @@ def test_binding_refuses_wrong_tensors(mnb):
     for bad in (dict(workspace=None), dict(q_start=None)):
         with pytest.raises(mnb.MnbError):
             mnb.mnb_verify_drafts(**dict(good, **bad))
+
+
+@pytest.mark.parametrize("vocab, batch", [(3, (1 << 22) + 5), (2049, 70000), (15400, 1500)])
+def test_many_sequences(mnb, vocab, batch):
+    """Sequences of one row: the token alone.  Weights are whole numbers, so every sum is exact in any order."""
+    t = G.torch()
+    gen = t.Generator(device="cuda").manual_seed(986)
+    p = t.empty(batch, vocab, dtype=t.float16, device="cuda").random_(0, 4, generator=gen)
+    pick = t.rand(batch, device="cuda", generator=gen)
+    ids = t.zeros(batch, dtype=t.int32, device="cuda")
+    out, accepted = run(mnb, p, None, ids, None, t.zeros(batch, device="cuda"), pick)
+    assert not accepted.any()
+    for i in range(0, batch, 1 << 17):
+        upto = p[i:i + (1 << 17)].to(t.float32).cumsum(1)
+        over = upto.double() > (pick[i:i + (1 << 17)].double() * upto[:, -1].double())[:, None]
+        want = t.where(over.any(1), over.to(t.uint8).argmax(1).to(t.int32), t.tensor(-1, dtype=t.int32, device="cuda"))
+        assert t.equal(out[i:i + (1 << 17)], want)
