@@ -15,8 +15,8 @@
 // A chunk of 1024 tokens a wave, of the one row that the draw needs (every workgroup
 // finds that row for itself); then a wave takes the sequence's chunk and in it the token.
 // Two launches, or one where a workgroup does for a sequence.  What is read bounds large calls,
-// the row and its draft's once: 32 sequences of 128000 tokens in fp32, 32.8 MB, 12.1 us, the
-// sums' kernel 8.6 of them.  Beside the loads it is work in 64 bits: per token a conversion and
+// the row and its draft's once: 32 sequences of 128000 tokens in fp32, 32.8 MB, 12.3 us, the
+// sums' kernel 8.1 of them.  Beside the loads it is work in 64 bits: per token a conversion and
 // an addition, with drafts of a distribution five (512 certain fp16 rows of 128000: 47 us
 // before the weights were chosen in 32 bits and a second sum taken only where it differs, 34 after
 // in the same two launches).
