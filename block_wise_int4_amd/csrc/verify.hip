@@ -200,9 +200,10 @@ __device__ __forceinline__ void draw_token(const Params& p, const Rows& r, int b
     const double rest_before = before(mine[0], lane, rest), all_before = before(mine[1], lane, all);
     // nothing is left of p where q is no smaller anywhere: then p itself
     const bool left = n < r.count - 1 && rest > 0.0;
+    // no sum passes a pick of 1 or more: sums of another order than the total's might end above it
     const float u = p.pick[b];
-    const double border = (u > 0.0f ? (double)u : 0.0) * (left ? rest : all);
-    // the first chunk that passes the border; pick of 1 or more passes all: the last with a weight
+    const double border = u >= 1.0f ? __builtin_inf() : (u > 0.0f ? (double)u : 0.0) * (left ? rest : all);
+    // the first chunk that passes the border, else the last with a weight
     double run = left ? rest_before : all_before, under = 0.0;
     int hit = -1, end = -1;
     for (int c = c0; c < c1; ++c) {
