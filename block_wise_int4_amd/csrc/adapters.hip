@@ -277,7 +277,10 @@ template <int RC> struct Up<_Float16, RC> {
     typedef h8_t piece;
     typedef _Float16 h4 __attribute__((ext_vector_type(4)));
     static __device__ __forceinline__ int rank0(int c, int quarter) { return RC == 0 ? 8 * (quarter & 1) : 32 * c + 8 * quarter; }
-    // h as two fp16 parts, 22 bits, of the row scaled to below 2^15; the power of two taken out
+    // h as two fp16 parts, 22 bits, of the row scaled to below 2^16; the power of two taken out.  Both parts have h's
+    // sign and are 0 only where h is, so that their products with an infinite B are of one sign: the first is cut
+    // off below h, and neither is less than fp16's least number, 2^-39 of the row's largest (rounded to nearest
+    // the second was 0 or of the other sign in half of all places, and the sum NaN).
     static __device__ __forceinline__ float put(const f4_t& v, int row, int r0, piece (*hf)[NH][64])
     {
         float mx = 0.0f;
@@ -285,15 +288,28 @@ template <int RC> struct Up<_Float16, RC> {
         for (int i = 0; i < 4; ++i) mx = fmaxf(mx, fabsf(v[i]) < __builtin_inff() ? fabsf(v[i]) : 0.0f);
 #pragma unroll
         for (int off = 1; off < PITCH / 4; off <<= 1) mx = fmaxf(mx, __shfl_xor(mx, off));
-        int e = mx > 0.0f ? (int)(__builtin_bit_cast(uint32_t, mx) >> 23) - 127 - 14 : 0;
+        int e = mx > 0.0f ? (int)(__builtin_bit_cast(uint32_t, mx) >> 23) - 127 - 15 : 0;
         e = e < -126 ? -126 : e;
         const float down = __builtin_bit_cast(float, (uint32_t)(127 - e) << 23);
+        typedef __fp16 rz2 __attribute__((ext_vector_type(2)));
         h4 hi, lo;
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const float s = v[i] * down;
-            hi[i] = (_Float16)s;
-            lo[i] = fabsf(s) < __builtin_inff() ? (_Float16)(s - (float)hi[i]) : (_Float16)0.0f;
+        for (int i = 0; i < 4; i += 2) {
+            float s[2], least[2];
+            rz2 cut;
+#pragma unroll
+            for (int k = 0; k < 2; ++k) {
+                s[k] = fabsf(v[i + k] * down);
+                least[k] = v[i + k] != 0.0f ? 1.25f / (1 << 24) : 0.0f;    // rounds to 2^-24, also less an ulp
+                s[k] = __builtin_elementwise_maximum(s[k], least[k]);      // NaN stays
+            }
+            const float below = 1.0f - 1.0f / (1 << 23);
+            cut = __builtin_amdgcn_cvt_pkrtz(s[0] * below, s[1] * below);
+#pragma unroll
+            for (int k = 0; k < 2; ++k) {
+                hi[i + k] = (_Float16)__builtin_copysignf((float)cut[k], v[i + k]);
+                lo[i + k] = (_Float16)__builtin_copysignf(fmaxf(s[k] - (float)cut[k], least[k]), v[i + k]);
+            }
         }
         const int u = row / 16, at = 16 * (r0 % 32 / 8) + row % 16, half = r0 / 4 & 1;
         if constexpr (RC == 0) {

@@ -532,8 +532,9 @@ mnb_status mnb_attention_kv4_sinks(const mnb_kv4_desc* c, const void* cache, con
  * x [m, k], base and y [m, n] of dtype, rows *_stride elements apart (a projection's
  * slice of a fused one, say).  y may be base itself, with the same stride; it
  * must not overlap x, or base in another way.  h = A x and the sums are kept in fp32;
- * in fp16 calls h enters the second product as two fp16 parts, 22 bits (to 2^-39 of its
- * row's largest where that is more), and y is rounded once.
+ * in fp16 calls h enters the second product as two fp16 parts, 22 bits (to 2^-38 of its
+ * row's largest where that is more), and y is rounded once.  Infinities and NaN of x, A and B
+ * give what the formula gives.
  * workspace (256-byte aligned): mnb_adapters_workspace_bytes of the same m; contents
  * need no initialisation.  rank at most 128, n and k at most 2^24, m < 2^24, m * n <
  * 2^37, else MNB_ERR_UNSUPPORTED.  m == 0 is a no-op.  Deterministic. */

@@ -13,8 +13,10 @@ def adapters(a, b, scales, ranks, adapter, x, base):
     """y [m, n] in float64 and its bound |kernel - y|, for operands of fp16 or fp32.
 
     h is a sum of k products in fp32, a product rounded once in fp32 calls: off by at
-    most (2 k + 32) 2^-24 sum |a x|.  In fp16 calls h enters the second product as two
-    fp16 parts: 2^-22 relative, and 2^-39 of the row's largest below their range.  That
+    most (2 k + 32) 2^-24 sum |a x|.  In fp16 calls h enters the second product as two fp16
+    parts of its sign, the row scaled to a largest in [2^15, 2^16): the first cut off to 11 bits, at most an ulp (2^-10
+    relative) below, the second rounded to 11 bits: 2^-22 relative.  Neither is less than 2^-24, so the two of a
+    smaller h are off by at most 2^-23, 2^-38 of the row's largest.  That
     product has rank terms (each twice in fp16 calls) and is scaled in two steps: (4 rank +
     32) 2^-24 of the sum of magnitudes.  The output is rounded once, to 2^-11 (2^-25
     absolute below fp16's normal range) or 2^-24, after its addition to base."""
@@ -36,7 +38,7 @@ def adapters(a, b, scales, ranks, adapter, x, base):
             eh = (2 * x.shape[1] + 32) * EPS32 * (np.abs(A) @ np.abs(v))
             part = np.abs(h) * ((2.0 ** -22 if f16 else 0) + (4 * r + 32) * EPS32) + eh
             if f16:
-                part = part + 2.0 ** -39 * np.abs(h).max()
+                part = part + 2.0 ** -38 * np.abs(h).max()
             y[t] += s * (B @ h)
             tol[t] = abs(s) * (np.abs(B) @ part)
             tol[t] += (np.abs(y[t]) + tol[t]) * (EPS16 if f16 else EPS32) * 1.001 + (2.0 ** -25 if f16 else 2.0 ** -149)
