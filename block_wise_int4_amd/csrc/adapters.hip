@@ -449,13 +449,14 @@ template <typename T, int RC> struct Columns {
 #pragma unroll
             for (int i = 0; i < PIECES; ++i) {
                 const int at = i * STEP + r0, n = 16 * (g + u) + at;
-                const float factor = scale * back[n];
+                // h's power of two first: times the scale it may leave fp32's range, which times 0 or infinity is NaN
+                const float up = sizeof(T) == 2 ? back[n] : 1.0f;
                 V v;
 #pragma unroll
                 for (int q = 0; q < E / 4; ++q) {
                     const f4_t t = *reinterpret_cast<const f4_t*>(&turn[at][c0 + 4 * q]);
 #pragma unroll
-                    for (int e = 0; e < 4; ++e) v[4 * q + e] = (T)__builtin_fmaf(t[e], factor, (float)in.v[u][i][4 * q + e]);
+                    for (int e = 0; e < 4; ++e) v[4 * q + e] = (T)__builtin_fmaf(t[e] * up, scale, (float)in.v[u][i][4 * q + e]);
                 }
                 if (n < rows) put(y + in.row[u][i] * p.y_stride, v);
             }

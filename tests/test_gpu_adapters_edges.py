@@ -38,3 +38,22 @@ def test_infinite_weights(mnb, size, dt):  # noqa: F811
     want, tol = o.adapters(a, b, scales, None, adapter, x, base)
     assert np.isinf(want[:, [3, 7, 8, n - 1]]).any(0).all() and np.isinf(want[:, 4]).any() and np.isnan(want[:, 20]).all()
     G.assert_within(got, want, None, "adapters", bound=np.where(np.isfinite(tol), tol, 0))
+
+
+@pytest.mark.parametrize("size", SIZES[:1] + SIZES[4:6], ids=IDS[:1] + IDS[4:6])
+@pytest.mark.parametrize("far", [60000.0, 2.0 ** -12])
+def test_scales_at_the_ends_of_their_range(mnb, far, size):  # noqa: F811
+    """h far above 1, or far below: a scale that leaves fp32's range together with h's power of two still leaves a
+    column without weights as it is, and an infinite weight infinite."""
+    m, k, n, rank, count = size
+    rng = np.random.default_rng((962,) + size)
+    x = (far * rng.uniform(0.5, 1, (m, k))).astype(np.float16)
+    a = (far * rng.uniform(0.5, 1, (count, rank, k))).astype(np.float16)
+    b = rng.integers(-2, 3, (count, n, rank)).astype(np.float16)
+    b[:, 10:30] = 0
+    b[:, 30, 1] = np.inf
+    base = rng.normal(size=(m, n)).astype(np.float16)
+    adapter = rng.integers(0, count, m)
+    for scale in (3e38, -2.0 ** 120, 2.0 ** -126, -2.0 ** -149):
+        got = G.host(run(mnb, a, b, np.full(count, scale, np.float32), None, adapter, x, base))
+        assert (got[:, 10:30] == base[:, 10:30]).all() and (got[:, 30] == np.copysign(np.inf, scale)).all()
