@@ -552,8 +552,10 @@ __global__ __launch_bounds__(kUpWaves * 64, RC <= 1 ? 4 : 2) void adapters_up_ke
         };
         // Where the registers are short the lanes' addresses are formed anew, from a lane's number that the compiler
         // cannot take for the last one, and not kept from block to block or beside h (rank 32, 8416 rows: 3 registers
-        // spilled and 95.6 us with them kept, none and 91.3 so; 512 rows of 64 adapters of rank 64 75 and 87)
-        if constexpr (!MORE && RC != 1) columns(w, true);
+        // in memory and 95.6 us with them kept, none and 91.3 so; rank 128, one token 10 and 11.4, none and 10.6, 64 rows
+        // of 64 adapters 35.0 and 33.5.  Elsewhere none is in memory either way: 512 rows of 64 adapters of rank 64 75 and
+        // 87, of rank 16 36.3 and 37.7)
+        if constexpr (!MORE && RC != 1 && RC != 4) columns(w, true);
         else
             for (int block = 0; block < blocks; ++block) {
                 int again = lane;
