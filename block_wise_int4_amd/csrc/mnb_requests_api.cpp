@@ -47,6 +47,8 @@ mnb_status check_adapters(const mnb_adapter_desc* d, int64_t m)
         return fail(MNB_ERR_UNSUPPORTED, "rank %d not supported (at most %d)", d->rank, mnb::adapters::kMaxRank);
     if (d->n > (1 << 24) || d->k > (1 << 24))
         return fail(MNB_ERR_UNSUPPORTED, "N=%lld, K=%lld not supported (at most 2^24)", (long long)d->n, (long long)d->k);
+    if ((int64_t)d->count * d->rank > INT64_MAX / 8 / (d->n > d->k ? d->n : d->k))
+        return fail(MNB_ERR_INVALID_ARGUMENT, "count=%d times rank=%d times N or K overflows", d->count, d->rank);
     // a workgroup of 256 threads takes 64 rows of 256 columns, in a grid of less than 2^32 threads
     if (m >= (1 << 24) || m * d->n >= (int64_t(1) << 37))
         return fail(MNB_ERR_UNSUPPORTED, "M=%lld not supported (below 2^24, and M*N below 2^37)", (long long)m);
