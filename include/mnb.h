@@ -535,8 +535,9 @@ mnb_status mnb_attention_kv4_sinks(const mnb_kv4_desc* c, const void* cache, con
  * in fp16 calls h enters the second product as two fp16 parts, 22 bits (to 2^-38 of its
  * row's largest where that is more), and y is rounded once.  Infinities and NaN of x, A and B
  * give what the formula gives.
- * workspace (256-byte aligned): mnb_adapters_workspace_bytes of the same m; contents
- * need no initialisation.  rank at most 128, n and k at most 2^24, m < 2^24, m * n <
+ * workspace (256-byte aligned): mnb_adapters_workspace_bytes of the same m, which a smaller
+ * m may pass; for every m up to M 4 R min(8 M, M + 32768) bytes suffice, R the rank rounded up to 16,
+ * 32, 64 or 128.  Its contents need no initialisation.  rank at most 128, n and k at most 2^24, m < 2^24, m * n <
  * 2^37, else MNB_ERR_UNSUPPORTED.  m == 0 is a no-op.  Deterministic. */
 typedef struct {
     int64_t n, k;

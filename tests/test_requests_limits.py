@@ -1,5 +1,6 @@
 """Sizes of the adapters and of the verification at the ends of their ranges, through the C ABI.  No GPU."""
 import ctypes
+import random
 
 import pytest
 
@@ -20,3 +21,22 @@ def test_weights_whose_bytes_overflow_are_refused(kw, dt):
     if _no_device():
         _refused(DEVICE, add, rank=128, count=1 << 20, dt=dt, wb=1 << 40, **kw)
         _refused(DEVICE, add, count=MOST, dt=dt, wb=1 << 40)
+
+
+def test_a_workspace_for_every_batch_up_to_a_size():
+    """The documented bound holds for all smaller batches, whose own sizes may be larger than the largest one's."""
+    rng = random.Random(1)
+    uneven = 0
+    for case in range(300):
+        n, k = (int(2 ** rng.uniform(0, 15)) for _ in range(2))
+        rank, count, dt = rng.randint(1, 128), int(2 ** rng.uniform(0, 9)), rng.choice([F16, F32])
+        if case == 0:
+            n, k, rank, count, dt = 4096, 4096, 16, 4, F16
+        d = mnb.mnb_adapter_desc(n, k, rank, count, dt, 0)
+        pitch = next(p for p in (16, 32, 64, 128) if rank <= p)
+        sizes = sorted({int(2 ** rng.uniform(0, 17)) for _ in range(60)} | {8120, 8580})
+        need = [mnb.mnb_adapters_workspace_bytes(d, m) for m in sizes]
+        for i, m in enumerate(sizes):
+            assert max(need[:i + 1]) <= 4 * pitch * min(8 * m, m + 32768), (n, k, rank, m)
+        uneven += any(a > b for a, b in zip(need, need[1:]))
+    assert uneven > 0
