@@ -127,7 +127,7 @@ def run(requests=5, steps=4, drafts=3, prompt=90, seed=0, **kw):
     ids = torch.randint(0, V, (sum(rows),), generator=gen, device="cuda").to(torch.int32)
     worst, taken, calls = [0.0] * 3, 0, []
     for step in range(steps + 1):
-        # the prompt's tokens are sure: each is "accepted", whatever its probability
+        # the prompt's tokens are sure: an accept below 0 takes a certain draft whatever its probability
         T = len(ids)
         draft = torch.softmax(1.5 * torch.randn(T, V, generator=gen, device="cuda"), 1) if step else None
         accept = rand(T) if step else torch.full((T,), -1.0, device="cuda")

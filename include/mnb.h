@@ -568,9 +568,10 @@ mnb_status mnb_adapters_add(const mnb_adapter_desc* d, const void* a, const void
  * out [tokens]: in the sequence's rows its accepted drafts, the drawn token, then -1;
  * accepted [batch]: n (0 for a sequence without rows).  Rows of no sequence are left.
  * A probability that is NaN, infinite or negative counts as 0; a row with no positive
- * one draws -1.  accept [tokens] and pick [batch] are fp32 in [0, 1); a pick that is NaN or
- * below 0 is 0, one of 1 or more draws the last token with a weight.  Rows need not be
- * normalised.  Products and sums are kept in 64 bits.
+ * one draws -1.  accept [tokens] and pick [batch] are fp32 in [0, 1).  An accept outside is taken
+ * as it is: one below 0 accepts a certain draft of the vocabulary whatever its p (a prompt's own tokens, say), one
+ * that is NaN refuses.  A pick that is NaN or below 0 is 0, one of 1 or more draws the last
+ * token with a weight.  Rows need not be normalised.  Products and sums are kept in 64 bits.
  * target_stride, draft_stride >= vocab.  out must not overlap ids.  workspace (256-byte
  * aligned): mnb_verify_workspace_bytes; contents need no initialisation.  vocab at most
  * 2^30, batch * ceil(vocab / 1024) < 2^24, else MNB_ERR_UNSUPPORTED.  batch == 0 is a
