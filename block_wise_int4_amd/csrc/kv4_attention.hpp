@@ -32,8 +32,8 @@ struct AttnParams {
     float scale_log2;
     int causal;
     int window;                       // 0: none; else below max_kv
-    int sinks;                        // first keys that stay visible; -1: keys are counted from the first
     int max_q, max_kv;
+    int sinks;                        // first keys that stay visible; -1: keys are counted from the first
     int gqa;                          // query heads per key head
     int splits, chunk;                // keys per split, a multiple of 32
     int row_tiles, rows_per_wg;
