@@ -129,10 +129,11 @@ template <int GRP, typename F> __device__ __forceinline__ void for_copies(F f)
 // registers in memory: with groups of 32 in fp32 and up to 4 rows (8 sequences of 4000 keys 26.6 us,
 // 31.8 with one wave), and with larger groups.
 // GAP: the call with first tokens that stay visible; the call without keeps its own
-// instances, some of which have no register left for the gap (with groups of 64 in fp32 and more than 8
-// rows at head size 256, 17 would be in memory).
+// instances, some of which have no register left for the gap.  At head size 256 in fp32 with the gap two waves a SIMD
+// are not worth it with groups of 32 (8 registers in memory; 32 sequences, window 4096, 65.8 us, 57.4 with one
+// wave) and with groups of 64 and more than 8 rows (17).
 template <int D, int NG, bool F32, int GRP, int NR, int KW, int PF, bool GAP>
-__global__ __launch_bounds__(KW * 64, D == 256 && (GRP == 4 || NG <= 4) && !(GAP && F32 && NG == 4 && GRP == 1) ? 2 : 1) void kv4_attention_kernel(AttnParams p)
+__global__ __launch_bounds__(KW * 64, D == 256 && (GRP == 4 || NG <= 4) && !(GAP && F32 && (NG == 8 || (NG == 4 && GRP == 1))) ? 2 : 1) void kv4_attention_kernel(AttnParams p)
 {
     static_assert(GRP == 1 || NR == 1, "copies of the rows need one column tile");
     typedef typename std::conditional<F32, float, _Float16>::type T;
