@@ -20,15 +20,17 @@
 // lanes goes to another row, at 16 bytes a cycle and CU: 8416 rows, k = 4096, rank 32 18 us, 60 so).
 // Second product: h is prepared once a workgroup, as operands in LDS: in fp16 calls as two fp16 parts of the row
 // scaled by a power of two, 22 bits, so that h is not rounded to 16 bits (at rank 16 and below one product takes both
-// parts); in fp32 calls as it is, for v_mfma_f32_16x16x4f32.  The result turns through
+// parts; both have h's sign, so that an infinite B meets no difference of infinities); in fp32 calls as it is, for v_mfma_f32_16x16x4f32.  The result turns through
 // LDS so that base is read and y is written 128 bytes or more of a row at a time.
 //
-// Measured, call by call.  k = n = 4096, rank 16, fp16: one token 7.0 us, 32 tokens of 24 adapters 8.0 (6.2
+// Measured, call by call.  k = n = 4096, rank 16, fp16: one token 7.1 us, 32 tokens of 24 adapters 8.1 (6.2
 // MB asked for), both one launch and the time of its chain: adapter, rank, A and x, two meetings in LDS,
-// base and y.  8416 rows, k = 4096, n = 11008, rank 32: 89 us for 443 MB, 5.0 TB/s where a large copy
-// moves 5.1; the first kernel 17 of them (69 MB).  4000 rows, k = n = 4096: rank 16 27 us, 32 29, 64 42,
-// 128 52 (floor 20): at the higher ranks h comes from the L2 once for every 512 columns.  In fp32 rank 64
-// takes 78 us (floor 39): its products run at a sixteenth of the fp16 rate.
+// base and y (fp32, two launches: 8.8 and 10.9).  8416 rows, k = 4096, n = 11008, rank 32: 89 us for 443 MB, 5.0 TB/s
+// where a large copy moves 5.1; the first kernel a fifth of it (69 MB).  4000 rows, k = n = 4096: rank 16 25.6 us,
+// 32 27.5, 64 39.6, 128 52.3 (floor 20), of which the first kernel takes 9, 10, 13 and 21: every 32 rows
+// read all of A, above rank 64 x is read twice, and every 512 columns read h and part it anew.  In
+// fp32 rank 64 takes 77 us (floor 39), 30 + 48: its products run at a sixteenth of the fp16 rate, two waves a SIMD.
+// No instance keeps a vector register in memory.
 #include <type_traits>
 
 #include "adapters_plan.hpp"

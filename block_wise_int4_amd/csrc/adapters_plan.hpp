@@ -32,14 +32,15 @@ inline Plan plan_of(int64_t m, int64_t n, int64_t k, int rank, int count, int f1
     c.pitch = rank <= 16 ? 16 : rank <= 32 ? 32 : rank <= 64 ? 64 : 128;
     const int64_t tiles = ceil_div(m, 64);
     // more splits fill the chip, and each adds a row of h to what the second product reads (8416
-    // rows, rank 32, k = 4096: 110, 105, 111 us with 2, 4, 8; 32 rows, rank 16: 11.3, 9.7, 9.2, and 9.7 with 16)
+    // rows, rank 32, k = 4096: 91.9, 89.0, 90.7, 95.9 us with 1, 2, 4, 8; 82 rows, rank 64, k = 11008: 19.3, 16.1, 16.0
+    // with 4, 8, 16; 64 rows of 64 adapters, rank 16, k = 8192: 17.9, 15.8, 14.1, 16.8 with 2, 4, 8, 16)
     const int64_t most = ceil_div(k, (int64_t)step * kDownWaves);
     int64_t splits = ceil_div(512, tiles);
     splits = splits > most ? most : splits;
     splits = splits > 8 ? 8 : splits;
     // every 256 columns of the second product read all of h: past 48 MB that costs more than the splits
-    // gain (4000 rows, k = n = 4096, fp16: rank 64 in eight 46.4 us, in four 41.3, in two 45.1;
-    // rank 128 74.4 and 61.1, in two 56.7; 1000 fp32 rows of rank 64, 33 MB, 26.4 and 30.0)
+    // gain (4000 rows, k = n = 4096, fp16: rank 64 in eight 43.3 us, in four 39.2, in two 38.7;
+    // rank 128 64.8, 54.4, 52.3, in one 53.8; 1000 fp32 rows of rank 64, 33 MB, 26.9 in eight, 25.7 in four)
     const int64_t fewest = rank > 64 ? 2 : 4;
     while (splits > fewest && m * splits * c.pitch * 4 * ceil_div(n, 64 * kUpWaves) > ((int64_t)48 << 20))
         splits = (splits + 1) / 2 < fewest ? fewest : (splits + 1) / 2;
@@ -54,6 +55,9 @@ inline Plan plan_of(int64_t m, int64_t n, int64_t k, int rank, int count, int f1
     // two, and few rows still gain the enqueue that their caller is spared (k = n = 4096, rank 16, in a graph and
     // call by call: one token 6.8 and 7.0 us against 7.0 and 9.6, 32 rows of 24 adapters 8.5 and 7.6 against 8.8 and 11.0,
     // 32 rows of one 9.0 against 7.3; k = n = 1024 5.9 against 8.1; 575 fp32 rows, 131 KB, 15.1 against 13.2).
+    // Above it two are better, in a graph, one launch and two, one token and 32 rows of 24 adapters: 163 KB (k = 5120) 8.5
+    // and 8.3, 9.8 and 10.1; 262 KB as k = 8192 10.2 and 8.6, as rank 32 9.4 and 8.3, 10.8 and 10.7, in fp32 12.3 and 8.8,
+    // 14.0 and 11.0.
     const int64_t sets = ceil_div(m, 32) * ceil_div(n, 64 * kOneWaves);
     c.one = rank <= 32 && k * c.pitch * (f16 ? 2 : 4) <= (m <= 64 ? 144 : 64) * 1024 && sets * distinct(32) <= 256;
     auto slots = [&](int64_t workgroups, int64_t most, int64_t rows) {

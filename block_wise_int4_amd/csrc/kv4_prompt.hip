@@ -25,8 +25,9 @@
 // 32, whose zero points and scales are loaded late, 469 in fp32 (which holds 6 registers in memory
 // until after the loop; head size 64 in groups of 32 holds two words of a stage there).
 // First tokens that stay visible beside a window (GAP): stages are taken from the keys counted without the gap;
-// 2048 and 1100 new tokens of 32 heads by 8 after prefixes, window 2048, 192 us (106 GFLOP: 555 TFLOP/s),
-// 400 workgroups of nearly one length in two rounds over 256 CUs.
+// 2048 and 1100 new tokens of 32 heads by 8 after prefixes, window 2048, 193 us a call in a stream of them (106
+// GFLOP: 550 TFLOP/s; the first dozen launches after a pause take 214), 400 workgroups of nearly one
+// length in two rounds over 256 CUs.
 #include "kv4_attention.hpp"
 
 namespace mnb {
@@ -34,8 +35,8 @@ namespace kv4 {
 
 namespace {
 
-// GAP: the call with first tokens that stay visible.  The call without keeps its own instances: with the
-// gap's scalars in them they spilled three times as many (250 us for the long case, 214 without).
+// GAP: the call with first tokens that stay visible.  The call without keeps its own instances: one instance for
+// both, whose blocks' places hung on the gap in either, took 250 us for the long case, 214 without.
 template <int D, int NG, bool F32, int NR, int RW, bool GAP>
 __global__ __launch_bounds__(RW * 64, 2) void kv4_prompt_kernel(AttnParams p)
 {

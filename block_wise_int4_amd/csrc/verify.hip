@@ -15,12 +15,12 @@
 // A chunk of 1024 tokens a wave, of the one row that the draw needs (every workgroup
 // finds that row for itself); then a wave takes the sequence's chunk and in it the token.
 // Two launches, or one where a workgroup does for a sequence.  What is read bounds large calls,
-// the row and its draft's once: 32 sequences of 128000 tokens in fp32, 32.8 MB, 12.3 us, the
-// sums' kernel 8.1 of them.  Beside the loads it is work in 64 bits: per token a conversion and
+// the row and its draft's once: 32 sequences of 128000 tokens in fp32, 32.8 MB, 12.1 us, the
+// sums' kernel 7.8 of them (fp16 10.7 and 5.7).  Beside the loads it is work in 64 bits: per token a conversion and
 // an addition, with drafts of a distribution five (512 certain fp16 rows of 128000: 47 us
 // before the weights were chosen in 32 bits and a second sum taken only where it differs, 34 after
 // in the same two launches).
-// Small calls are latency: 6.6 us of one sequence are two launches, and the loads that wait
+// Small calls are latency: 7.3 us of one sequence in a graph are two launches, and the loads that wait
 // for each other: rows, ids, a probability, the row; then the sums, the chunk.
 #include "mnb_requests.hpp"
 #include "mnb_vec.hpp"
