@@ -56,11 +56,12 @@ inline Plan plan_of(const AttentionArgs& a)
             // 16384 21.7 in eight, 26.8 in sixteen), and halves only of longer spans than 2048 (16 sequences,
             // window 1024: 11.1 whole, 12.0)
             const int64_t units = ((rows + c.rows - 1) / c.rows) * a.v.kv_heads * a.v.batch;
+            const int64_t most = want;
             want = units >= 128 && span <= 2048 ? 1 : units > 256 ? 1 : 256 / units * units;
             // but lengths are not known here, and a workgroup that walks 5120 keys by itself is on its way for 35 us: no
             // piece is longer, up to as many as the call without first tokens cuts (32 sequences, one of 65536 keys and
             // the others of 300: window 60000 39 us, 309 whole, window 16384 33 and 91; all of 16384 keys 116 and 108)
-            const int64_t pieces = (span + 5119) / 5120 * units, most = 3072;
+            const int64_t pieces = (span + 5119) / 5120 * units;
             if (want < pieces) want = pieces < most ? pieces : most;
             grain = 128;
         }
